@@ -53,6 +53,9 @@ EP_MAP_HT_RANK_OFFSET = 5
 EP_MAP_HT_EXPERT_COUNT = 6
 EP_MAP_HT_EXPERT_OFFSET = 7
 
+EP_ACT_SILU = 0
+EP_ACT_GELU_TANH = 1
+
 EP_NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024
 
 EP_BUF_LL_RECV = 0
@@ -142,6 +145,10 @@ SIGNATURES = {
     "ep_complete": (_S, [_P, _P]),
     "ep_combine_backward": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _P]),
     "ep_dispatch_backward": (_S, [_P, _PT, _PT, _P]),
+    "ep_expert_gated": (_S, [_P, _PT, _PT, _PT, _PT, _PT, ctypes.c_int32, _PT, _P]),
+    "ep_expert_gated_backward": (_S, [_P, _PT, _PT, _PT, _PT, ctypes.c_int32, _PT, _PT, _PT, _PT, _PT, _P]),
+    "ep_expert_linear": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _P]),
+    "ep_expert_linear_backward": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _P]),
     "ep_dequantize_rows": (_S, [_P, _PT, _PT, _P]),
     "ep_status_string": (ctypes.c_char_p, [_S]),
     "ep_get_device_error": (_S, [_P, ctypes.POINTER(ctypes.c_int32)]),

@@ -140,6 +140,8 @@ struct Handle {
   int32_t* off1 = nullptr;       // HT [R]
   int32_t* c2 = nullptr;         // HT [E]
   int32_t* off2 = nullptr;       // HT [E]
+  int32_t* rows_total = nullptr; // LL, several sources [E]: rows per expert, for the experts' products
+  int32_t* rows_list = nullptr;  // LL, several sources [n_max * K]: their message indices, expert after expert
   int32_t* hist_e = nullptr;     // [tiles_max, E] tile counts -> prefixes
   int32_t* hist_n = nullptr;     // [tiles_max, N]
   int buf_half = -1;             // receive buffer / stage set of the last dispatch
@@ -294,5 +296,79 @@ struct DequantArgs {
   int64_t ld_y;           // elements
 };
 hipError_t launch_dequant(const DequantArgs& a, hipStream_t stream);
+
+// ---------------------------------------------------------------------------
+// The experts' products
+// ---------------------------------------------------------------------------
+
+namespace expert {
+
+// Rows of expert e, p = 0 .. count[e]-1, in the receive layout: list[before(e) + p] with a list (LL, many
+// sources: slots are filled per source); else e*stride + p with a stride (LL, one source); else
+// before(e) + p (HT).  before(e) is the sum of the counts of the experts before e.
+struct ExpertRows {
+  const int32_t* count;   // [E]
+  const int32_t* list;
+  int64_t limit;          // rows that the caller's tensors hold
+  int32_t E, stride;
+  int32_t* err;           // device error word: rows beyond the limit are left out and reported
+};
+
+// The launchers return hipErrorInvalidConfiguration, before any work, for more tiles than one grid holds;
+// with `check` they only say whether they would.
+// Strides (ld_*, *_expert) and k_bytes are in bytes, those of bf16 outputs (ld_out) and grad in elements.
+struct AlongArgs {
+  ExpertRows rows;
+  int64_t rows_max, per_expert_max;   // bounds that the host knows
+  int64_t k_bytes;                    // bytes of a row that are contracted
+  int32_t N;
+  const uint8_t* x;
+  int64_t ld_x;
+  const uint8_t* x_scales;            // FP8: one float per 128 values of a row
+  int64_t ld_xs;
+  const uint8_t* w[2];                // linear: w[0]; gated: gate and up
+  int64_t ld_w[2], w_expert[2];
+  const uint8_t* w_scales[2];         // FP8: one float per 128 x 128 values
+  int64_t ld_ws[2], ws_expert[2];
+  uint16_t* out[2];
+  int64_t ld_out[2];
+  const uint16_t* grad;               // gated gradient: the gradient of the gated product
+  int64_t ld_grad;
+};
+hipError_t launch_linear(const AlongArgs& a, bool fp8, hipStream_t stream, bool check = false);
+hipError_t launch_gated(const AlongArgs& a, bool fp8, int act, hipStream_t stream, bool check = false);
+// out = the gradients of the gate's and of the up product
+hipError_t launch_gated_grad(const AlongArgs& a, int act, hipStream_t stream, bool check = false);
+
+struct RowGradArgs {
+  ExpertRows rows;
+  int64_t rows_max, per_expert_max;
+  int32_t I, N, parts;                // contracted size, columns, 1 or 2 (dy, w)
+  const uint8_t* dy[2];
+  int64_t ld_dy[2];
+  const uint8_t* w[2];
+  int64_t ld_w[2], w_expert[2];
+  uint16_t* dx;
+  int64_t ld_dx;                      // elements
+};
+hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check = false);
+
+struct WeightGradArgs {
+  ExpertRows rows;
+  int32_t I, H, parts;
+  const uint8_t* dy[2];
+  int64_t ld_dy[2];
+  const uint8_t* x;
+  int64_t ld_x;
+  uint8_t* dw[2];
+  int64_t ld_dw[2], dw_expert[2];
+};
+hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check = false);
+
+// LL with several sources: rows per expert and the list of rows, from the slots' counts [E, S].
+hipError_t launch_list_rows(const int32_t* counts, int E, int S, int slots, int32_t* total, int32_t* list,
+                            hipStream_t stream);
+
+}  // namespace expert
 
 }  // namespace ep

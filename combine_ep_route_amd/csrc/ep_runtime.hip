@@ -209,10 +209,12 @@ DispatchArgs dispatch_base(const Handle* h) {
   return p;
 }
 
-// An expert-row tensor (expert outputs or their gradients) as 2-D BF16 rows
-// [rows, H]: given as [rows, H], or in LL as [E, S*T_max, H] with a dense
-// middle dimension.  Rows 16-byte aligned, innermost contiguous.
-bool expert_rows(const Group* g, const ep_tensor_t* t, ep_tensor_t* out) {
+// A tensor of rows at the dispatch geometry as 2-D rows of `cols` values of a
+// type: given as [rows, cols], or in LL as [E, S*T_max, cols] with a dense
+// middle dimension.  Innermost contiguous, rows 16-byte aligned unless
+// `aligned` is false.
+bool geometry_rows(const Group* g, const ep_tensor_t* t, int32_t dtype, int64_t cols, int32_t tag, bool aligned,
+                   ep_tensor_t* out) {
   if (!t) return false;
   *out = *t;
   if (t->ndim == 3) {
@@ -227,7 +229,12 @@ bool expert_rows(const Group* g, const ep_tensor_t* t, ep_tensor_t* out) {
     out->strides[0] = t->strides[1];
     out->strides[1] = 1;
   }
-  return check2d(out, EP_DTYPE_BF16, -1, g->cfg.hidden, EP_TAG_TOKENS, true);
+  return check2d(out, dtype, -1, cols, tag, aligned);
+}
+
+// Expert outputs or their gradients: BF16 [rows, H].
+bool expert_rows(const Group* g, const ep_tensor_t* t, ep_tensor_t* out) {
+  return geometry_rows(g, t, EP_DTYPE_BF16, g->cfg.hidden, EP_TAG_TOKENS, true, out);
 }
 
 // Make sure the slot / row maps and the HT key offsets exist (dispatch
@@ -411,6 +418,7 @@ EP_API ep_status_t ep_create_group(const ep_config_t* cfg_in, ep_stream_t stream
     size_t bytes = align_up(nm * K * 4) * 2 + align_up(nm * N * 4);   // topk copy, ranks
     if (cfg.mode == EP_MODE_LL) {
       bytes += align_up(nm * K * 4) + align_up(static_cast<size_t>(E) * S * 4);
+      if (S > 1) bytes += align_up(E * 4) + align_up(nm * K * 4);   // rows per expert and their list
     } else {
       bytes += align_up(nm * N * 4) + align_up(nm * K * 4) + align_up(R * 4) * 2 + align_up(E * 4) * 2;
     }
@@ -428,6 +436,10 @@ EP_API ep_status_t ep_create_group(const ep_config_t* cfg_in, ep_stream_t stream
     if (cfg.mode == EP_MODE_LL) {
       h->slot_map = cv.take<int32_t>(nm * K);
       h->ll_count = cv.take<int32_t>(static_cast<size_t>(E) * S);
+      if (S > 1) {
+        h->rows_total = cv.take<int32_t>(E);
+        h->rows_list = cv.take<int32_t>(nm * K);
+      }
     } else {
       h->node_row = cv.take<int32_t>(nm * N);
       h->row2 = cv.take<int32_t>(nm * K);
@@ -1077,6 +1089,351 @@ EP_API ep_status_t ep_complete(ep_handle_t handle, ep_stream_t stream) {
           h->n);
   }
   return st;
+}
+
+// ===========================================================================
+// The experts' products
+// ===========================================================================
+
+namespace {
+
+using expert::AlongArgs;
+using expert::ExpertRows;
+using expert::RowGradArgs;
+using expert::WeightGradArgs;
+
+constexpr int64_t kMaxProductSize = 1 << 20;
+
+// A [E, rows, cols] tensor of weights: innermost contiguous, 16-byte aligned.
+bool check_weights(const Group* g, const ep_tensor_t* t, int32_t dtype, int64_t rows, int64_t cols) {
+  if (!t || t->dtype != dtype || t->ndim != 3 || t->tag != EP_TAG_NONE || !t->data) return false;
+  if (t->sizes[0] != g->cfg.num_experts || t->sizes[1] != rows || t->sizes[2] != cols) return false;
+  const int64_t es = dtype_size(dtype);
+  if (t->strides[2] != 1 || t->strides[1] < cols || t->strides[0] < 0) return false;
+  return ((reinterpret_cast<uintptr_t>(t->data) | (t->strides[1] * es) | (t->strides[0] * es)) & 15) == 0;
+}
+
+// Gradients of weights: BF16 or F32, every matrix in memory of its own.
+bool check_weight_grad(const Group* g, const ep_tensor_t* t, int64_t rows, int64_t cols) {
+  if (!t || (t->dtype != EP_DTYPE_BF16 && t->dtype != EP_DTYPE_F32)) return false;
+  if (!check_weights(g, t, t->dtype, rows, cols)) return false;
+  return t->strides[0] >= (rows - 1) * t->strides[1] + cols;
+}
+
+// Scales of FP8 weights [E, rows, cols]: F32 [E, ceil(rows/128), cols/128].
+bool check_weight_scales(const Group* g, const ep_tensor_t* t, int64_t rows, int64_t cols) {
+  if (!t || t->dtype != EP_DTYPE_F32 || t->ndim != 3 || (t->tag != EP_TAG_NONE && t->tag != EP_TAG_SCALES) ||
+      !t->data)
+    return false;
+  return t->sizes[0] == g->cfg.num_experts && t->sizes[1] == (rows + 127) / 128 && t->sizes[2] == cols / 128 &&
+         t->strides[2] == 1 && t->strides[1] >= t->sizes[2] && t->strides[0] >= 0 &&
+         (reinterpret_cast<uintptr_t>(t->data) & 3) == 0;
+}
+
+bool product_size(int64_t v) { return v > 0 && v % 8 == 0; }
+
+// The received rows of a gated product: BF16 [rows, H] at the dispatch
+// geometry, or the dispatch's own packed rows (U8).  *codes: FP8 rows.
+bool received_rows(const Group* g, const ep_tensor_t* t, ep_tensor_t* out, bool* codes) {
+  *codes = false;
+  if (!t) return false;
+  if (t->dtype != EP_DTYPE_U8) return expert_rows(g, t, out);
+  if (t->ndim != 2 || t->sizes[1] < g->row_bytes || !check2d(t, EP_DTYPE_U8, -1, -1, EP_TAG_TOKENS, true)) return false;
+  *out = *t;
+  *codes = g->fp8;
+  if (!g->fp8) {   // BF16 rows: the same in elements
+    out->dtype = EP_DTYPE_BF16;
+    out->sizes[1] = g->cfg.hidden;
+    out->strides[0] = t->strides[0] / 2;
+  }
+  return true;
+}
+
+// LL tensors hold every slot; HT rows are checked on the device.
+bool holds_slots(const Group* g, const ep_tensor_t& t) {
+  return g->cfg.mode != EP_MODE_LL ||
+         t.sizes[0] >= static_cast<int64_t>(g->cfg.num_experts) * g->cfg.num_src_ranks * g->cfg.max_tokens_per_rank;
+}
+
+ep_status_t expert_ready(const Handle* h) {
+  if (h->g->s2_rank) return EP_ERR_UNSUPPORTED;   // a row belongs to several experts there
+  return h->pend == Handle::kPendNone ? EP_OK : EP_ERR_INVALID_ARGUMENT;
+}
+
+ExpertRows rows_of_experts(const Handle* h, int64_t limit) {
+  const Group* g = h->g;
+  ExpertRows r{};
+  r.E = g->cfg.num_experts;
+  r.limit = limit;
+  r.err = g->err;
+  if (g->cfg.mode == EP_MODE_HT) {
+    r.count = h->c2;
+  } else if (g->cfg.num_src_ranks == 1) {
+    r.count = h->ll_count;
+    r.stride = g->cfg.max_tokens_per_rank;
+  } else {
+    r.count = h->rows_total;
+    r.list = h->rows_list;
+  }
+  return r;
+}
+
+// Enqueues what the products need first: the rows' list in LL with several
+// sources.  It is formed at every call, from the handle's counts alone, so a
+// captured call does not depend on what ran outside its graph.
+ep_status_t start_products(Handle* h, hipStream_t s) {
+  Group* g = h->g;
+  if (const ep_status_t st = ensure_device(g, s); st != EP_OK) return st;
+  h->stream = s;
+  if (g->cfg.mode == EP_MODE_LL && g->cfg.num_src_ranks > 1)
+    EP_HIP(expert::launch_list_rows(h->ll_count, g->cfg.num_experts, g->cfg.num_src_ranks,
+                                    g->cfg.max_tokens_per_rank, h->rows_total, h->rows_list, s));
+  return EP_OK;
+}
+
+ep_status_t fits(hipError_t e) { return e == hipSuccess ? EP_OK : EP_ERR_UNSUPPORTED; }
+
+void set_weights(AlongArgs* a, int i, const ep_tensor_t* w, const ep_tensor_t* scales) {
+  const int64_t es = dtype_size(w->dtype);
+  a->w[i] = static_cast<const uint8_t*>(w->data);
+  a->ld_w[i] = w->strides[1] * es;
+  a->w_expert[i] = w->strides[0] * es;
+  if (!scales) return;
+  a->w_scales[i] = static_cast<const uint8_t*>(scales->data);
+  a->ld_ws[i] = scales->strides[1] * 4;
+  a->ws_expert[i] = scales->strides[0] * 4;
+}
+
+void set_out(AlongArgs* a, int i, const ep_tensor_t& t) {
+  a->out[i] = static_cast<uint16_t*>(t.data);
+  a->ld_out[i] = t.strides[0];
+}
+
+// The part of a forward product's arguments that does not depend on its kind.
+AlongArgs along_args(const Handle* h, const ep_tensor_t& x, int64_t k, int64_t n, int64_t limit) {
+  AlongArgs a{};
+  const int64_t es = x.dtype == EP_DTYPE_BF16 ? 2 : 1;
+  a.rows = rows_of_experts(h, limit);
+  a.rows_max = h->n * h->g->cfg.top_k;
+  a.per_expert_max = h->n;   // a token names an expert at most once
+  a.k_bytes = k * es;
+  a.N = static_cast<int32_t>(n);
+  a.x = static_cast<const uint8_t*>(x.data);
+  a.ld_x = x.strides[0] * es;
+  return a;
+}
+
+RowGradArgs row_grad_args(const Handle* h, int64_t i, int64_t n, const ep_tensor_t& dx, int64_t limit) {
+  RowGradArgs r{};
+  r.rows = rows_of_experts(h, limit);
+  r.rows_max = h->n * h->g->cfg.top_k;
+  r.per_expert_max = h->n;
+  r.I = static_cast<int32_t>(i);
+  r.N = static_cast<int32_t>(n);
+  r.dx = static_cast<uint16_t*>(dx.data);
+  r.ld_dx = dx.strides[0];
+  return r;
+}
+
+void add_part(RowGradArgs* r, const ep_tensor_t& dy, const ep_tensor_t* w) {
+  const int i = r->parts++;
+  r->dy[i] = static_cast<const uint8_t*>(dy.data);
+  r->ld_dy[i] = dy.strides[0] * 2;
+  r->w[i] = static_cast<const uint8_t*>(w->data);
+  r->ld_w[i] = w->strides[1] * 2;
+  r->w_expert[i] = w->strides[0] * 2;
+}
+
+WeightGradArgs weight_grad_args(const Handle* h, const ep_tensor_t& x, int64_t i, int64_t n, int64_t limit) {
+  WeightGradArgs r{};
+  r.rows = rows_of_experts(h, limit);
+  r.I = static_cast<int32_t>(i);
+  r.H = static_cast<int32_t>(n);
+  r.x = static_cast<const uint8_t*>(x.data);
+  r.ld_x = x.strides[0] * 2;
+  return r;
+}
+
+void add_part(WeightGradArgs* r, const ep_tensor_t& dy, const ep_tensor_t* dw) {
+  const int i = r->parts++;
+  const int64_t es = dtype_size(dw->dtype);
+  r->dy[i] = static_cast<const uint8_t*>(dy.data);
+  r->ld_dy[i] = dy.strides[0] * 2;
+  r->dw[i] = static_cast<uint8_t*>(dw->data);
+  r->ld_dw[i] = dw->strides[1] * es;
+  r->dw_expert[i] = dw->strides[0] * es;
+}
+
+}  // namespace
+
+EP_API ep_status_t ep_expert_gated(ep_handle_t handle, const ep_tensor_t* rows, const ep_tensor_t* w_gate,
+                                   const ep_tensor_t* w_up, const ep_tensor_t* w_gate_scales,
+                                   const ep_tensor_t* w_up_scales, int32_t activation, ep_tensor_t* out,
+                                   ep_stream_t stream) {
+  Handle* h = reinterpret_cast<Handle*>(handle);
+  if (!handle_ok(h) || !w_gate || w_gate->ndim != 3) return EP_ERR_INVALID_ARGUMENT;
+  Group* g = h->g;
+  if (const ep_status_t st = expert_ready(h); st != EP_OK) return st;
+  const int64_t H = g->cfg.hidden, I = w_gate->sizes[1];
+  if (activation != EP_ACT_SILU && activation != EP_ACT_GELU_TANH) return EP_ERR_INVALID_ARGUMENT;
+  ep_tensor_t x, o;
+  bool fp8;
+  if (!received_rows(g, rows, &x, &fp8) || !product_size(I)) return EP_ERR_INVALID_ARGUMENT;
+  const int32_t type = fp8 ? EP_DTYPE_FP8_E4M3 : EP_DTYPE_BF16;
+  if (!check_weights(g, w_gate, type, I, H) || !check_weights(g, w_up, type, I, H)) return EP_ERR_INVALID_ARGUMENT;
+  if (fp8 ? !check_weight_scales(g, w_gate_scales, I, H) || !check_weight_scales(g, w_up_scales, I, H)
+          : w_gate_scales || w_up_scales)
+    return EP_ERR_INVALID_ARGUMENT;
+  if (!geometry_rows(g, out, EP_DTYPE_BF16, I, EP_TAG_TOKENS, true, &o)) return EP_ERR_INVALID_ARGUMENT;
+  if (!holds_slots(g, x) || !holds_slots(g, o)) return EP_ERR_INVALID_ARGUMENT;
+  if (I > kMaxProductSize) return EP_ERR_UNSUPPORTED;
+
+  AlongArgs a = along_args(h, x, H, I, std::min(x.sizes[0], o.sizes[0]));
+  if (fp8) {
+    a.x_scales = a.x + H;   // behind the row's codes
+    a.ld_xs = a.ld_x;
+  }
+  set_weights(&a, 0, w_gate, w_gate_scales);
+  set_weights(&a, 1, w_up, w_up_scales);
+  set_out(&a, 0, o);
+  const hipStream_t s = as_stream(stream);
+  if (const ep_status_t st = fits(expert::launch_gated(a, fp8, activation, s, true)); st != EP_OK) return st;
+  if (const ep_status_t st = start_products(h, s); st != EP_OK) return st;
+  const ep_status_t st = from_hip(expert::launch_gated(a, fp8, activation, s));
+  if (st == EP_OK) trace(g, "expert_gated", h->n);
+  return st;
+}
+
+EP_API ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_t* rows, const ep_tensor_t* w_gate,
+                                            const ep_tensor_t* w_up, const ep_tensor_t* grad_out, int32_t activation,
+                                            ep_tensor_t* grad_gate, ep_tensor_t* grad_up, ep_tensor_t* grad_rows,
+                                            ep_tensor_t* grad_w_gate, ep_tensor_t* grad_w_up, ep_stream_t stream) {
+  Handle* h = reinterpret_cast<Handle*>(handle);
+  if (!handle_ok(h) || !w_gate || w_gate->ndim != 3) return EP_ERR_INVALID_ARGUMENT;
+  Group* g = h->g;
+  if (const ep_status_t st = expert_ready(h); st != EP_OK) return st;
+  const int64_t H = g->cfg.hidden, I = w_gate->sizes[1];
+  if (activation != EP_ACT_SILU && activation != EP_ACT_GELU_TANH) return EP_ERR_INVALID_ARGUMENT;
+  ep_tensor_t x, d, dg, du, dx{};
+  bool fp8;
+  if (!received_rows(g, rows, &x, &fp8) || fp8 || !product_size(I)) return EP_ERR_INVALID_ARGUMENT;
+  if (!check_weights(g, w_gate, EP_DTYPE_BF16, I, H) || !check_weights(g, w_up, EP_DTYPE_BF16, I, H) ||
+      !geometry_rows(g, grad_out, EP_DTYPE_BF16, I, EP_TAG_TOKENS, true, &d) ||
+      !geometry_rows(g, grad_gate, EP_DTYPE_BF16, I, EP_TAG_TOKENS, true, &dg) ||
+      !geometry_rows(g, grad_up, EP_DTYPE_BF16, I, EP_TAG_TOKENS, true, &du) ||
+      (grad_rows && !geometry_rows(g, grad_rows, EP_DTYPE_BF16, H, EP_TAG_TOKENS, true, &dx)))
+    return EP_ERR_INVALID_ARGUMENT;
+  if (!grad_w_gate != !grad_w_up) return EP_ERR_INVALID_ARGUMENT;
+  if (grad_w_gate && (!check_weight_grad(g, grad_w_gate, I, H) || !check_weight_grad(g, grad_w_up, I, H) ||
+                      grad_w_gate->dtype != grad_w_up->dtype))
+    return EP_ERR_INVALID_ARGUMENT;
+  if (!holds_slots(g, x) || !holds_slots(g, d) || !holds_slots(g, dg) || !holds_slots(g, du) ||
+      (grad_rows && !holds_slots(g, dx)))
+    return EP_ERR_INVALID_ARGUMENT;
+  if (I > kMaxProductSize) return EP_ERR_UNSUPPORTED;
+
+  int64_t limit = std::min({x.sizes[0], d.sizes[0], dg.sizes[0], du.sizes[0]});
+  if (grad_rows) limit = std::min(limit, dx.sizes[0]);
+  AlongArgs a = along_args(h, x, H, I, limit);
+  set_weights(&a, 0, w_gate, nullptr);
+  set_weights(&a, 1, w_up, nullptr);
+  set_out(&a, 0, dg);
+  set_out(&a, 1, du);
+  a.grad = static_cast<const uint16_t*>(d.data);
+  a.ld_grad = d.strides[0];
+  RowGradArgs r = row_grad_args(h, I, H, dx, limit);
+  add_part(&r, dg, w_gate);
+  add_part(&r, du, w_up);
+  WeightGradArgs w = weight_grad_args(h, x, I, H, limit);
+  const bool f32 = grad_w_gate && grad_w_gate->dtype == EP_DTYPE_F32;
+  if (grad_w_gate) {
+    add_part(&w, dg, grad_w_gate);
+    add_part(&w, du, grad_w_up);
+  }
+  const hipStream_t s = as_stream(stream);
+  if (const ep_status_t st = fits(expert::launch_gated_grad(a, activation, s, true)); st != EP_OK) return st;
+  if (const ep_status_t st = fits(expert::launch_row_grad(r, s, true)); st != EP_OK) return st;
+  if (const ep_status_t st = fits(expert::launch_weight_grad(w, f32, s, true)); st != EP_OK) return st;
+  if (const ep_status_t st = start_products(h, s); st != EP_OK) return st;
+  EP_HIP(expert::launch_gated_grad(a, activation, s));
+  if (grad_rows) EP_HIP(expert::launch_row_grad(r, s));
+  if (grad_w_gate) EP_HIP(expert::launch_weight_grad(w, f32, s));
+  trace(g, "expert_gated_backward", h->n);
+  return EP_OK;
+}
+
+EP_API ep_status_t ep_expert_linear(ep_handle_t handle, const ep_tensor_t* x_in, const ep_tensor_t* x_scales,
+                                    const ep_tensor_t* w, const ep_tensor_t* w_scales, ep_tensor_t* out,
+                                    ep_stream_t stream) {
+  Handle* h = reinterpret_cast<Handle*>(handle);
+  if (!handle_ok(h) || !x_in || !w || w->ndim != 3) return EP_ERR_INVALID_ARGUMENT;
+  Group* g = h->g;
+  if (const ep_status_t st = expert_ready(h); st != EP_OK) return st;
+  const int64_t N = w->sizes[1], C = w->sizes[2];
+  const bool fp8 = x_in->dtype == EP_DTYPE_FP8_E4M3;
+  const int32_t type = fp8 ? EP_DTYPE_FP8_E4M3 : EP_DTYPE_BF16;
+  ep_tensor_t x, xs{}, o;
+  if (!product_size(N) || !product_size(C) || (fp8 && C % 128 != 0)) return EP_ERR_INVALID_ARGUMENT;
+  if (!geometry_rows(g, x_in, type, C, EP_TAG_TOKENS, true, &x) || !check_weights(g, w, type, N, C))
+    return EP_ERR_INVALID_ARGUMENT;
+  if (fp8 ? !geometry_rows(g, x_scales, EP_DTYPE_F32, C / 128, EP_TAG_SCALES, false, &xs) ||
+                xs.sizes[0] < x.sizes[0] || (reinterpret_cast<uintptr_t>(xs.data) & 3) ||
+                !check_weight_scales(g, w_scales, N, C)
+          : x_scales || w_scales)
+    return EP_ERR_INVALID_ARGUMENT;
+  if (!geometry_rows(g, out, EP_DTYPE_BF16, N, EP_TAG_TOKENS, true, &o)) return EP_ERR_INVALID_ARGUMENT;
+  if (!holds_slots(g, x) || !holds_slots(g, o)) return EP_ERR_INVALID_ARGUMENT;
+  if (N > kMaxProductSize || C > kMaxProductSize) return EP_ERR_UNSUPPORTED;
+
+  AlongArgs a = along_args(h, x, C, N, std::min(x.sizes[0], o.sizes[0]));
+  if (fp8) {
+    a.x_scales = static_cast<const uint8_t*>(xs.data);
+    a.ld_xs = xs.strides[0] * 4;
+  }
+  set_weights(&a, 0, w, w_scales);
+  set_out(&a, 0, o);
+  const hipStream_t s = as_stream(stream);
+  if (const ep_status_t st = fits(expert::launch_linear(a, fp8, s, true)); st != EP_OK) return st;
+  if (const ep_status_t st = start_products(h, s); st != EP_OK) return st;
+  const ep_status_t st = from_hip(expert::launch_linear(a, fp8, s));
+  if (st == EP_OK) trace(g, "expert_linear", h->n);
+  return st;
+}
+
+EP_API ep_status_t ep_expert_linear_backward(ep_handle_t handle, const ep_tensor_t* x_in, const ep_tensor_t* w,
+                                             const ep_tensor_t* grad_out, ep_tensor_t* grad_x, ep_tensor_t* grad_w,
+                                             ep_stream_t stream) {
+  Handle* h = reinterpret_cast<Handle*>(handle);
+  if (!handle_ok(h) || !w || w->ndim != 3) return EP_ERR_INVALID_ARGUMENT;
+  Group* g = h->g;
+  if (const ep_status_t st = expert_ready(h); st != EP_OK) return st;
+  const int64_t N = w->sizes[1], C = w->sizes[2];
+  ep_tensor_t x, d, dx{};
+  if (!product_size(N) || !product_size(C)) return EP_ERR_INVALID_ARGUMENT;
+  if (!geometry_rows(g, x_in, EP_DTYPE_BF16, C, EP_TAG_TOKENS, true, &x) ||
+      !check_weights(g, w, EP_DTYPE_BF16, N, C) ||
+      !geometry_rows(g, grad_out, EP_DTYPE_BF16, N, EP_TAG_TOKENS, true, &d) ||
+      (grad_x && !geometry_rows(g, grad_x, EP_DTYPE_BF16, C, EP_TAG_TOKENS, true, &dx)) ||
+      (grad_w && !check_weight_grad(g, grad_w, N, C)))
+    return EP_ERR_INVALID_ARGUMENT;
+  if (!holds_slots(g, x) || !holds_slots(g, d) || (grad_x && !holds_slots(g, dx))) return EP_ERR_INVALID_ARGUMENT;
+  if (N > kMaxProductSize || C > kMaxProductSize) return EP_ERR_UNSUPPORTED;
+
+  int64_t limit = std::min(x.sizes[0], d.sizes[0]);
+  if (grad_x) limit = std::min(limit, dx.sizes[0]);
+  RowGradArgs r = row_grad_args(h, N, C, dx, limit);
+  add_part(&r, d, w);
+  WeightGradArgs wg = weight_grad_args(h, x, N, C, limit);
+  const bool f32 = grad_w && grad_w->dtype == EP_DTYPE_F32;
+  if (grad_w) add_part(&wg, d, grad_w);
+  const hipStream_t s = as_stream(stream);
+  if (const ep_status_t st = fits(expert::launch_row_grad(r, s, true)); st != EP_OK) return st;
+  if (const ep_status_t st = fits(expert::launch_weight_grad(wg, f32, s, true)); st != EP_OK) return st;
+  if (const ep_status_t st = start_products(h, s); st != EP_OK) return st;
+  if (grad_x) EP_HIP(expert::launch_row_grad(r, s));
+  if (grad_w) EP_HIP(expert::launch_weight_grad(wg, f32, s));
+  trace(g, "expert_linear_backward", h->n);
+  return EP_OK;
 }
 
 // ===========================================================================

@@ -243,6 +243,62 @@ def ep_complete(handle: Handle, stream=None) -> None:
     handle._staged = None
 
 
+_ACTIVATIONS = {"silu": A.EP_ACT_SILU, "gelu_tanh": A.EP_ACT_GELU_TANH}
+
+
+def _activation(activation) -> int:
+    if isinstance(activation, str):
+        if activation not in _ACTIVATIONS:
+            raise ValueError(f"activation is one of {sorted(_ACTIVATIONS)}, got {activation!r}")
+        return _ACTIVATIONS[activation]
+    return activation
+
+
+def ep_expert_gated(handle: Handle, rows: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                    out: torch.Tensor, activation="silu", w_gate_scales: Optional[torch.Tensor] = None,
+                    w_up_scales: Optional[torch.Tensor] = None, stream=None) -> None:
+    r = desc(rows, A.EP_TAG_TOKENS)
+    g, u = desc(w_gate), desc(w_up)
+    gs, us = desc(w_gate_scales, A.EP_TAG_SCALES), desc(w_up_scales, A.EP_TAG_SCALES)
+    o = desc(out, A.EP_TAG_TOKENS)
+    _check("ep_expert_gated", A.lib().ep_expert_gated(handle.ptr, _ref(r), _ref(g), _ref(u), _ref(gs), _ref(us),
+                                                      _activation(activation), _ref(o), _stream(stream)))
+
+
+def ep_expert_gated_backward(handle: Handle, rows: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                             grad_out: torch.Tensor, grad_gate: torch.Tensor, grad_up: torch.Tensor,
+                             activation="silu", grad_rows: Optional[torch.Tensor] = None,
+                             grad_w_gate: Optional[torch.Tensor] = None,
+                             grad_w_up: Optional[torch.Tensor] = None, stream=None) -> None:
+    r, g, u = desc(rows, A.EP_TAG_TOKENS), desc(w_gate), desc(w_up)
+    d = desc(grad_out, A.EP_TAG_TOKENS)
+    dg, du = desc(grad_gate, A.EP_TAG_TOKENS), desc(grad_up, A.EP_TAG_TOKENS)
+    dr = desc(grad_rows, A.EP_TAG_TOKENS)
+    wg, wu = desc(grad_w_gate), desc(grad_w_up)
+    _check("ep_expert_gated_backward", A.lib().ep_expert_gated_backward(
+        handle.ptr, _ref(r), _ref(g), _ref(u), _ref(d), _activation(activation), _ref(dg), _ref(du), _ref(dr),
+        _ref(wg), _ref(wu), _stream(stream)))
+
+
+def ep_expert_linear(handle: Handle, x: torch.Tensor, w: torch.Tensor, out: torch.Tensor,
+                     x_scales: Optional[torch.Tensor] = None, w_scales: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    xd, xs = desc(x, A.EP_TAG_TOKENS), desc(x_scales, A.EP_TAG_SCALES)
+    wd, ws = desc(w), desc(w_scales, A.EP_TAG_SCALES)
+    o = desc(out, A.EP_TAG_TOKENS)
+    _check("ep_expert_linear", A.lib().ep_expert_linear(handle.ptr, _ref(xd), _ref(xs), _ref(wd), _ref(ws), _ref(o),
+                                                        _stream(stream)))
+
+
+def ep_expert_linear_backward(handle: Handle, x: torch.Tensor, w: torch.Tensor, grad_out: torch.Tensor,
+                              grad_x: Optional[torch.Tensor] = None, grad_w: Optional[torch.Tensor] = None,
+                              stream=None) -> None:
+    xd, wd, d = desc(x, A.EP_TAG_TOKENS), desc(w), desc(grad_out, A.EP_TAG_TOKENS)
+    dx, dw = desc(grad_x, A.EP_TAG_TOKENS), desc(grad_w)
+    _check("ep_expert_linear_backward", A.lib().ep_expert_linear_backward(
+        handle.ptr, _ref(xd), _ref(wd), _ref(d), _ref(dx), _ref(dw), _stream(stream)))
+
+
 def ep_dequantize_rows(group: Group, rows: torch.Tensor, y: torch.Tensor, stream=None) -> None:
     r = desc(rows)
     o = desc(y, A.EP_TAG_TOKENS)
