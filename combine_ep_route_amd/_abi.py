@@ -149,6 +149,11 @@ SIGNATURES = {
     "ep_expert_gated_backward": (_S, [_P, _PT, _PT, _PT, _PT, ctypes.c_int32, _PT, _PT, _PT, _PT, _PT, _P]),
     "ep_expert_linear": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _P]),
     "ep_expert_linear_backward": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _P]),
+    "ep_residual_norm": (_S, [_P, _PT, _PT, _PT, _PT, _PT, ctypes.c_float, ctypes.c_float, ctypes.c_float, _PT, _PT,
+                              _P]),
+    "ep_residual_norm_workspace": (_S, [_P, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]),
+    "ep_residual_norm_backward": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _PT, _PT, ctypes.c_float, ctypes.c_float,
+                                       ctypes.c_float, _PT, _PT, _PT, _PT, _PT, _PT, _P]),
     "ep_dequantize_rows": (_S, [_P, _PT, _PT, _P]),
     "ep_status_string": (ctypes.c_char_p, [_S]),
     "ep_get_device_error": (_S, [_P, ctypes.POINTER(ctypes.c_int32)]),

@@ -371,4 +371,68 @@ hipError_t launch_list_rows(const int32_t* counts, int E, int S, int slots, int3
 
 }  // namespace expert
 
+// ---------------------------------------------------------------------------
+// Norms around the block
+// ---------------------------------------------------------------------------
+
+namespace norm {
+
+constexpr int kGradBlocks = 512;   // workgroups of the backward pass, each with a share of the column sums
+
+// Strides in elements.
+struct NormArgs {
+  int64_t n;
+  int32_t H;
+  const uint16_t* y;
+  int64_t ld_y;
+  const uint16_t* x;         // the residual stream
+  int64_t ld_x;
+  const void* w_post;        // or null: no norm on y
+  const void* w_pre;
+  int32_t post_f32, pre_f32;
+  const uint16_t* gate;      // or null
+  int64_t ld_gate;
+  int32_t gate_rows;         // a gate per token, else per channel
+  float a, b, eps;
+  uint16_t* out_x;
+  int64_t ld_out_x;
+  uint16_t* out_n;
+  int64_t ld_out_n;
+};
+hipError_t launch_residual_norm(const NormArgs& a, hipStream_t stream);
+
+struct NormGradArgs {
+  int64_t n;
+  int32_t H;
+  const uint16_t* y;
+  int64_t ld_y;
+  const uint16_t* x;         // the stream behind the block
+  int64_t ld_x;
+  const uint16_t* g_res;     // or null: zeros
+  int64_t ld_g_res;
+  const uint16_t* g_norm;
+  int64_t ld_g_norm;
+  const void* w_post;
+  const void* w_pre;
+  int32_t post_f32, pre_f32;
+  const uint16_t* gate;
+  int64_t ld_gate;
+  int32_t gate_rows;
+  float a, b, eps;
+  uint16_t* dres;
+  int64_t ld_dres;
+  uint16_t* dy;
+  int64_t ld_dy;
+  uint16_t* dgate_token;     // optional outputs
+  int64_t ld_dgate;
+  float* dw_pre;
+  float* dw_post;
+  float* dgate_channel;
+  float* work;               // up to 3 x grad_blocks(n) x H
+};
+int grad_blocks(int64_t n);
+hipError_t launch_residual_norm_backward(const NormGradArgs& a, hipStream_t stream);
+
+}  // namespace norm
+
 }  // namespace ep

@@ -14,6 +14,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -1434,6 +1435,162 @@ EP_API ep_status_t ep_expert_linear_backward(ep_handle_t handle, const ep_tensor
   if (grad_w) EP_HIP(expert::launch_weight_grad(wg, f32, s));
   trace(g, "expert_linear_backward", h->n);
   return EP_OK;
+}
+
+// ===========================================================================
+// Norms around the block
+// ===========================================================================
+
+namespace {
+
+constexpr int64_t kMaxNormRows = 1 << 22;
+
+// A vector of H values: [H] or [1, H], contiguous, 16-byte aligned; F32, or
+// BF16 unless `f32_only`.
+bool check_vector(const ep_tensor_t* t, int64_t H, bool f32_only) {
+  if (!t || (t->dtype != EP_DTYPE_F32 && (f32_only || t->dtype != EP_DTYPE_BF16)) || t->tag != EP_TAG_NONE) return false;
+  if (t->ndim != 1 && (t->ndim != 2 || t->sizes[0] != 1)) return false;
+  return t->sizes[t->ndim - 1] == H && t->strides[t->ndim - 1] == 1 && t->data &&
+         (reinterpret_cast<uintptr_t>(t->data) & 15) == 0;
+}
+
+bool check_scales(float a, float b, float eps) {
+  return std::isfinite(a) && std::isfinite(b) && std::isfinite(eps) && eps >= 0.0f;
+}
+
+bool rows_bf16(const ep_tensor_t* t, int64_t n, int64_t H) {
+  return check2d(t, EP_DTYPE_BF16, n, H, EP_TAG_TOKENS, true);
+}
+
+// A gate: BF16, one row for all tokens or one per token.
+bool check_gate(const ep_tensor_t* t, int64_t n, int64_t H) {
+  return !t || rows_bf16(t, 1, H) || rows_bf16(t, n, H);
+}
+
+}  // namespace
+
+EP_API ep_status_t ep_residual_norm(ep_group_t group, const ep_tensor_t* y, const ep_tensor_t* residual,
+                                    const ep_tensor_t* w_post, const ep_tensor_t* gate, const ep_tensor_t* w_pre,
+                                    float residual_scale, float block_scale, float eps, ep_tensor_t* out_residual,
+                                    ep_tensor_t* out_norm, ep_stream_t stream) {
+  Group* g = reinterpret_cast<Group*>(group);
+  if (!group_ok(g) || !check_scales(residual_scale, block_scale, eps)) return EP_ERR_INVALID_ARGUMENT;
+  const int64_t H = g->cfg.hidden;
+  if (!rows_bf16(y, -1, H)) return EP_ERR_INVALID_ARGUMENT;
+  const int64_t n = y->sizes[0];
+  if (!rows_bf16(residual, n, H) || !rows_bf16(out_residual, n, H) || !rows_bf16(out_norm, n, H) ||
+      (w_post && !check_vector(w_post, H, false)) || !check_vector(w_pre, H, false) || !check_gate(gate, n, H))
+    return EP_ERR_INVALID_ARGUMENT;
+  if (n > kMaxNormRows) return EP_ERR_UNSUPPORTED;
+  const hipStream_t s = as_stream(stream);
+  if (const ep_status_t st = ensure_device(g, s); st != EP_OK) return st;
+  norm::NormArgs a{};
+  a.n = n;
+  a.H = static_cast<int32_t>(H);
+  a.y = static_cast<const uint16_t*>(y->data);
+  a.ld_y = y->strides[0];
+  a.x = static_cast<const uint16_t*>(residual->data);
+  a.ld_x = residual->strides[0];
+  a.w_post = w_post ? w_post->data : nullptr;
+  a.post_f32 = w_post && w_post->dtype == EP_DTYPE_F32;
+  a.w_pre = w_pre->data;
+  a.pre_f32 = w_pre->dtype == EP_DTYPE_F32;
+  if (gate) {
+    a.gate = static_cast<const uint16_t*>(gate->data);
+    a.ld_gate = gate->strides[0];
+    a.gate_rows = gate->sizes[0] == n;   // with one token both are the same
+  }
+  a.a = residual_scale;
+  a.b = block_scale;
+  a.eps = eps;
+  a.out_x = static_cast<uint16_t*>(out_residual->data);
+  a.ld_out_x = out_residual->strides[0];
+  a.out_n = static_cast<uint16_t*>(out_norm->data);
+  a.ld_out_n = out_norm->strides[0];
+  const ep_status_t st = from_hip(norm::launch_residual_norm(a, s));
+  if (st == EP_OK) trace(g, "residual_norm", n);
+  return st;
+}
+
+EP_API ep_status_t ep_residual_norm_workspace(ep_group_t group, int64_t n, int64_t* bytes) {
+  Group* g = reinterpret_cast<Group*>(group);
+  if (!group_ok(g) || n < 0 || !bytes) return EP_ERR_INVALID_ARGUMENT;
+  *bytes = static_cast<int64_t>(3) * norm::grad_blocks(n) * g->cfg.hidden * 4;
+  return EP_OK;
+}
+
+EP_API ep_status_t ep_residual_norm_backward(ep_group_t group, const ep_tensor_t* y, const ep_tensor_t* x,
+                                             const ep_tensor_t* grad_out_residual, const ep_tensor_t* grad_out_norm,
+                                             const ep_tensor_t* w_post, const ep_tensor_t* gate,
+                                             const ep_tensor_t* w_pre, float residual_scale, float block_scale,
+                                             float eps, ep_tensor_t* grad_residual, ep_tensor_t* grad_y,
+                                             ep_tensor_t* grad_w_pre, ep_tensor_t* grad_w_post, ep_tensor_t* grad_gate,
+                                             ep_tensor_t* workspace, ep_stream_t stream) {
+  Group* g = reinterpret_cast<Group*>(group);
+  if (!group_ok(g) || !check_scales(residual_scale, block_scale, eps)) return EP_ERR_INVALID_ARGUMENT;
+  const int64_t H = g->cfg.hidden;
+  if (!rows_bf16(y, -1, H)) return EP_ERR_INVALID_ARGUMENT;
+  const int64_t n = y->sizes[0];
+  if (!rows_bf16(x, n, H) || !rows_bf16(grad_out_norm, n, H) ||
+      (grad_out_residual && !rows_bf16(grad_out_residual, n, H)) || !rows_bf16(grad_residual, n, H) ||
+      !rows_bf16(grad_y, n, H) || (w_post && !check_vector(w_post, H, false)) || !check_vector(w_pre, H, false) ||
+      !check_gate(gate, n, H) || !check_vector(grad_w_pre, H, true) ||
+      (grad_w_post && (!w_post || !check_vector(grad_w_post, H, true))) || (grad_gate && !gate))
+    return EP_ERR_INVALID_ARGUMENT;
+  // a gate's kind: by its rows; of one row and one token by the gradient's type
+  bool per_token = gate && gate->sizes[0] == n && n != 1;
+  if (gate && n == 1) per_token = grad_gate && grad_gate->dtype == EP_DTYPE_BF16;
+  if (grad_gate && !(per_token ? rows_bf16(grad_gate, n, H) : check_vector(grad_gate, H, true)))
+    return EP_ERR_INVALID_ARGUMENT;
+  if (n > kMaxNormRows) return EP_ERR_UNSUPPORTED;
+  const int64_t need = static_cast<int64_t>(3) * norm::grad_blocks(n) * H * 4;
+  if (n > 0 && (!workspace || workspace->dtype != EP_DTYPE_U8 || workspace->ndim != 1 || workspace->strides[0] != 1 ||
+                workspace->sizes[0] < need || !workspace->data ||
+                (reinterpret_cast<uintptr_t>(workspace->data) & 15) != 0))
+    return EP_ERR_INVALID_ARGUMENT;
+  const hipStream_t s = as_stream(stream);
+  if (const ep_status_t st = ensure_device(g, s); st != EP_OK) return st;
+  norm::NormGradArgs a{};
+  a.n = n;
+  a.H = static_cast<int32_t>(H);
+  a.y = static_cast<const uint16_t*>(y->data);
+  a.ld_y = y->strides[0];
+  a.x = static_cast<const uint16_t*>(x->data);
+  a.ld_x = x->strides[0];
+  if (grad_out_residual) {
+    a.g_res = static_cast<const uint16_t*>(grad_out_residual->data);
+    a.ld_g_res = grad_out_residual->strides[0];
+  }
+  a.g_norm = static_cast<const uint16_t*>(grad_out_norm->data);
+  a.ld_g_norm = grad_out_norm->strides[0];
+  a.w_post = w_post ? w_post->data : nullptr;
+  a.post_f32 = w_post && w_post->dtype == EP_DTYPE_F32;
+  a.w_pre = w_pre->data;
+  a.pre_f32 = w_pre->dtype == EP_DTYPE_F32;
+  if (gate) {
+    a.gate = static_cast<const uint16_t*>(gate->data);
+    a.ld_gate = gate->strides[0];
+    a.gate_rows = per_token;
+  }
+  a.a = residual_scale;
+  a.b = block_scale;
+  a.eps = eps;
+  a.dres = static_cast<uint16_t*>(grad_residual->data);
+  a.ld_dres = grad_residual->strides[0];
+  a.dy = static_cast<uint16_t*>(grad_y->data);
+  a.ld_dy = grad_y->strides[0];
+  a.dw_pre = static_cast<float*>(grad_w_pre->data);
+  a.dw_post = grad_w_post ? static_cast<float*>(grad_w_post->data) : nullptr;
+  if (grad_gate && per_token) {
+    a.dgate_token = static_cast<uint16_t*>(grad_gate->data);
+    a.ld_dgate = grad_gate->strides[0];
+  } else if (grad_gate) {
+    a.dgate_channel = static_cast<float*>(grad_gate->data);
+  }
+  a.work = n > 0 ? static_cast<float*>(workspace->data) : nullptr;
+  const ep_status_t st = from_hip(norm::launch_residual_norm_backward(a, s));
+  if (st == EP_OK) trace(g, "residual_norm_backward", n);
+  return st;
 }
 
 // ===========================================================================

@@ -299,6 +299,42 @@ def ep_expert_linear_backward(handle: Handle, x: torch.Tensor, w: torch.Tensor, 
         handle.ptr, _ref(xd), _ref(wd), _ref(d), _ref(dx), _ref(dw), _stream(stream)))
 
 
+def ep_residual_norm(group: Group, y: torch.Tensor, residual: torch.Tensor, out_residual: torch.Tensor,
+                     out_norm: torch.Tensor, w_pre: torch.Tensor, w_post: Optional[torch.Tensor] = None,
+                     gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0, block_scale: float = 1.0,
+                     eps: float = 1e-6, stream=None) -> None:
+    yd, r = desc(y, A.EP_TAG_TOKENS), desc(residual, A.EP_TAG_TOKENS)
+    wp, g, wn = desc(w_post), desc(gate), desc(w_pre)
+    o, n = desc(out_residual, A.EP_TAG_TOKENS), desc(out_norm, A.EP_TAG_TOKENS)
+    _check("ep_residual_norm", A.lib().ep_residual_norm(
+        group.ptr, _ref(yd), _ref(r), _ref(wp), _ref(g), _ref(wn), residual_scale, block_scale, eps, _ref(o), _ref(n),
+        _stream(stream)))
+
+
+def ep_residual_norm_workspace(group: Group, n: int) -> int:
+    b = ctypes.c_int64()
+    _check("ep_residual_norm_workspace", A.lib().ep_residual_norm_workspace(group.ptr, n, ctypes.byref(b)))
+    return b.value
+
+
+def ep_residual_norm_backward(group: Group, y: torch.Tensor, x: torch.Tensor,
+                              grad_out_residual: Optional[torch.Tensor], grad_out_norm: torch.Tensor,
+                              w_pre: torch.Tensor, grad_residual: torch.Tensor, grad_y: torch.Tensor,
+                              grad_w_pre: torch.Tensor, workspace: torch.Tensor,
+                              w_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                              grad_w_post: Optional[torch.Tensor] = None, grad_gate: Optional[torch.Tensor] = None,
+                              residual_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6,
+                              stream=None) -> None:
+    yd, xd = desc(y, A.EP_TAG_TOKENS), desc(x, A.EP_TAG_TOKENS)
+    gr, gn = desc(grad_out_residual, A.EP_TAG_TOKENS), desc(grad_out_norm, A.EP_TAG_TOKENS)
+    wp, g, wn = desc(w_post), desc(gate), desc(w_pre)
+    dr, dy = desc(grad_residual, A.EP_TAG_TOKENS), desc(grad_y, A.EP_TAG_TOKENS)
+    dn, dp, dg, ws = desc(grad_w_pre), desc(grad_w_post), desc(grad_gate), desc(workspace)
+    _check("ep_residual_norm_backward", A.lib().ep_residual_norm_backward(
+        group.ptr, _ref(yd), _ref(xd), _ref(gr), _ref(gn), _ref(wp), _ref(g), _ref(wn), residual_scale, block_scale,
+        eps, _ref(dr), _ref(dy), _ref(dn), _ref(dp), _ref(dg), _ref(ws), _stream(stream)))
+
+
 def ep_dequantize_rows(group: Group, rows: torch.Tensor, y: torch.Tensor, stream=None) -> None:
     r = desc(rows)
     o = desc(y, A.EP_TAG_TOKENS)

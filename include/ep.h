@@ -629,6 +629,64 @@ ep_status_t ep_expert_linear_backward(ep_handle_t handle, const ep_tensor_t *x, 
                                       ep_tensor_t *grad_w, ep_stream_t stream);
 
 /* ----------------------------------------------------------------------- */
+/* Norms around the block                                                    */
+/* ----------------------------------------------------------------------- */
+
+/* What stands between one block's ep_combine and the next block's router, in
+ * one pass: the norm behind the block, its gate, the scaled sum into the
+ * residual stream, and the norm in front of the next block.  With
+ * rms(v; w)[h] = v[h] w[h] / sqrt(mean_h v^2 + eps):
+ *   out_residual[i] = residual_scale * residual[i]
+ *                     + block_scale * gate * rms(y[i]; w_post)      (rounded to bf16)
+ *   out_norm[i]     = rms(out_residual[i]; w_pre)                   (of the bf16 stream)
+ *   y, residual, out_residual, out_norm : BF16 [n, H] (H the group's), rows
+ *            16-byte aligned.  out_residual may be residual, and out_norm may
+ *            be y (same data, same stride); else outputs overlap nothing.
+ *   w_post : [H] (or [1, H]) F32 or BF16, 16-byte aligned; NULL: y itself.
+ *   gate   : BF16 [1, H] (per channel) or [n, H] (per token), or NULL (1).
+ *   w_pre  : [H] F32 or BF16.
+ *   eps    : finite, >= 0.
+ * Sums are fp32; n may be 0.  EP_ERR_INVALID_ARGUMENT for anything else, and
+ * EP_ERR_UNSUPPORTED for more than 2^22 rows. */
+ep_status_t ep_residual_norm(ep_group_t group, const ep_tensor_t *y, const ep_tensor_t *residual,
+                             const ep_tensor_t *w_post, const ep_tensor_t *gate,
+                             const ep_tensor_t *w_pre, float residual_scale, float block_scale,
+                             float eps, ep_tensor_t *out_residual, ep_tensor_t *out_norm,
+                             ep_stream_t stream);
+
+/* Bytes of working memory the backward pass needs for n rows. */
+ep_status_t ep_residual_norm_workspace(ep_group_t group, int64_t n, int64_t *bytes);
+
+/* Its backward pass.  x is the stream ep_residual_norm left (out_residual);
+ * with dx = grad_out_residual + the adjoint of rms(x; w_pre) at grad_out_norm:
+ *   grad_residual = residual_scale * dx                              BF16 [n, H]
+ *   grad_y        = the adjoint of rms(y; w_post) at block_scale * gate * dx
+ *                   (without w_post that product itself)             BF16 [n, H]
+ *   grad_w_pre, grad_w_post : F32 [H] (or [1, H]), sums over the tokens;
+ *                   grad_w_post NULL without w_post, optional with it.
+ *   grad_gate     : optional.  Of a gate per channel: F32 [1, H], the sum over
+ *                   the tokens of block_scale * dx * rms(y; w_post); per token:
+ *                   BF16 [n, H].  (With n = 1 its type says which.)  NULL
+ *                   without a gate.
+ *   grad_out_residual : BF16 [n, H] or NULL (zeros).
+ *   workspace     : U8 [bytes], 16-byte aligned, of at least
+ *                   ep_residual_norm_workspace(n) bytes; its contents before
+ *                   and after do not matter.  Calls that run at the same time
+ *                   need workspaces of their own.
+ * grad_residual may be grad_out_residual and grad_y may be y or grad_out_norm
+ * (same data and stride); else outputs overlap nothing.  The column sums are
+ * added in a fixed order: repeated calls give the same bits. */
+ep_status_t ep_residual_norm_backward(ep_group_t group, const ep_tensor_t *y, const ep_tensor_t *x,
+                                      const ep_tensor_t *grad_out_residual,
+                                      const ep_tensor_t *grad_out_norm, const ep_tensor_t *w_post,
+                                      const ep_tensor_t *gate, const ep_tensor_t *w_pre,
+                                      float residual_scale, float block_scale, float eps,
+                                      ep_tensor_t *grad_residual, ep_tensor_t *grad_y,
+                                      ep_tensor_t *grad_w_pre, ep_tensor_t *grad_w_post,
+                                      ep_tensor_t *grad_gate, ep_tensor_t *workspace,
+                                      ep_stream_t stream);
+
+/* ----------------------------------------------------------------------- */
 /* Identity expert (test aid and debugging)                                  */
 /* ----------------------------------------------------------------------- */
 
