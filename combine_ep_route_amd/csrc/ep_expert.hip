@@ -83,13 +83,13 @@ __global__ __launch_bounds__(C::NT) void along_kernel(AlongArgs a) {
 
   typename C::Acc acc = {};
   AlongSrc<C, GATED> src(a, s, n0, m0);
-  C::run(src, static_cast<int>((a.k_bytes + kPiece - 1) / kPiece), acc);
+  C::run(src, static_cast<int>((a.k_bytes + kPiece - 1) / kPiece), s.count - m0, acc);
 
   const int l = lane_id(), w = wave_id();
-  const int fa = (w % C::WA) * src.wave_span_a(), fb = (w / C::WA) * C::TB;
+  const int fa = (w % C::WA) * src.wave_span_a();
 #pragma unroll
   for (int j = 0; j < C::FB; ++j) {
-    const int p = m0 + fb + j * 16 + (l & 15);
+    const int p = m0 + C::from_b(j) + (l & 15);
     if (p >= s.count) continue;
     const int64_t r = row_of(a.rows, s, p);
 #pragma unroll
@@ -137,10 +137,10 @@ template <class C>
 struct RowGradSrc {
   const RowGradArgs& g;
   const Span& s;
-  const uint8_t* pa[C::JA];
+  const uint8_t* pa[C::JA];   // advanced step by step
   const uint8_t* pb[C::JB];
-  int n0, m0, steps, part;
-  bool inside;
+  int64_t advance;
+  int n0, m0, steps, part, left;
 
   static constexpr int wave_span_a() { return C::TA; }
   static __device__ __forceinline__ int frag_a_at(int fa, int i) { return fa + i * 16; }
@@ -163,21 +163,28 @@ struct RowGradSrc {
       pb[j] = g.dy[which] + static_cast<int64_t>(row_of(g.rows, s, p < s.count ? p : s.count - 1)) * g.ld_dy[which] +
               C::along_piece() * 16;
     }
+    advance = g.ld_w[which] * kStepRows;
     part = which;
+    left = g.I;
   }
+  // the core asks for every step once, in order
   __device__ __forceinline__ void step(int t) {
     const int which = t >= steps;
-    if (which != part) begin(which);
-    const int at = t - which * steps;
-    inside = at * kStepRows + C::along_piece() * 8 < g.I;
+    if (which != part) {
+      begin(which);
+      return;
+    }
+    left -= kStepRows;
+#pragma unroll
+    for (int j = 0; j < C::JA; ++j) pa[j] += advance;
+#pragma unroll
+    for (int j = 0; j < C::JB; ++j) pb[j] += kPiece;
   }
-  __device__ __forceinline__ const uint8_t* a(int j, int t) const {
-    const int at = t - part * steps;
-    return at * kStepRows + C::template across_row<C::BA>(j * C::NW + wave_id()) < g.I
-               ? pa[j] + static_cast<int64_t>(at) * kStepRows * g.ld_w[part] : zeros();
+  __device__ __forceinline__ const uint8_t* a(int j, int) const {
+    return C::template across_row<C::BA>(j * C::NW + wave_id()) < left ? pa[j] : zeros();
   }
-  __device__ __forceinline__ const uint8_t* b(int j, int t) const {
-    return inside ? pb[j] + (t - part * steps) * kPiece : zeros();
+  __device__ __forceinline__ const uint8_t* b(int j, int) const {
+    return C::along_piece() * 8 < left ? pb[j] : zeros();
   }
 };
 
@@ -192,12 +199,12 @@ __global__ __launch_bounds__(C::NT) void row_grad_kernel(RowGradArgs g) {
 
   typename C::Acc acc = {};
   RowGradSrc<C> src(g, s, n0, m0);
-  C::run(src, src.steps * g.parts, acc);
+  C::run(src, src.steps * g.parts, s.count - m0, acc);
 
   const int l = lane_id(), w = wave_id();
 #pragma unroll
   for (int j = 0; j < C::FB; ++j) {
-    const int p = m0 + (w / C::WA) * C::TB + j * 16 + (l & 15);
+    const int p = m0 + C::from_b(j) + (l & 15);
     if (p >= s.count) continue;
     const int64_t r = row_of(g.rows, s, p);
 #pragma unroll
@@ -249,12 +256,12 @@ __global__ __launch_bounds__(C::NT) void weight_grad_kernel(WeightGradArgs g) {
 
   typename C::Acc acc = {};
   WeightGradSrc<C> src{g, s, g.dy[which], g.ld_dy[which], h0, i0};
-  C::run(src, (s.count + kStepRows - 1) / kStepRows, acc);
+  C::run(src, (s.count + kStepRows - 1) / kStepRows, g.I - i0, acc);
 
   const int l = lane_id(), w = wave_id();
 #pragma unroll
   for (int j = 0; j < C::FB; ++j) {
-    const int i = i0 + (w / C::WA) * C::TB + j * 16 + (l & 15);
+    const int i = i0 + C::from_b(j) + (l & 15);
     if (i >= g.I) continue;
 #pragma unroll
     for (int f = 0; f < C::FA; ++f) {
