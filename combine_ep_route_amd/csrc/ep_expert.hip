@@ -67,7 +67,7 @@ struct AlongSrc {
   __device__ __forceinline__ void step(int t) { inside = t * kPiece < limit; }
   __device__ __forceinline__ const uint8_t* a(int j, int t) const { return inside ? pa[j] + t * kPiece : zeros(); }
   __device__ __forceinline__ const uint8_t* b(int j, int t) const { return inside ? pb[j] + t * kPiece : zeros(); }
-  __device__ __forceinline__ const uint8_t* scale(int t) const { return ps + t * 4; }
+  __device__ __forceinline__ const uint8_t* scale(int t) const { return inside ? ps + t * 4 : zeros(); }
 };
 
 template <class C, int KIND, int ACT>
@@ -169,7 +169,7 @@ struct RowGradSrc {
   }
   // the core asks for every step once, in order
   __device__ __forceinline__ void step(int t) {
-    const int which = t >= steps;
+    const int which = g.parts == 2 && t >= steps;
     if (which != part) {
       begin(which);
       return;
@@ -329,7 +329,7 @@ template <bool F8, int KIND, int ACT>
 hipError_t launch_along_kind(const AlongArgs& a, hipStream_t stream, bool check) {
   if (a.rows_max <= static_cast<int64_t>(a.rows.E) * 32)
     return launch_along_as<Core<128, 32, 4, 1, false, false, F8, 4>, KIND, ACT>(a, stream, check);
-  return launch_along_as<Core<256, 256, F8 ? 2 : 4, F8 ? 4 : 2, false, false, F8, 2>, KIND, ACT>(a, stream, check);
+  return launch_along_as<Core<256, 256, 2, 4, false, false, F8, 2>, KIND, ACT>(a, stream, check);
 }
 
 template <bool F8>
@@ -361,7 +361,7 @@ hipError_t launch_gated_grad(const AlongArgs& a, int act, hipStream_t stream, bo
 }
 
 hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check) {
-  using C = Core<256, 256, 4, 2, true, false, false, 2>;
+  using C = Core<256, 256, 2, 4, true, false, false, 2>;
   const int64_t tiles = row_tiles<C::BB>(g.rows, g.rows_max, g.per_expert_max) * ((g.N + C::BA - 1) / C::BA);
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
   if (tiles == 0 || check) return hipSuccess;
@@ -370,7 +370,7 @@ hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check)
 }
 
 hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check) {
-  using C = Core<256, 256, 4, 2, true, true, false, 2>;
+  using C = Core<256, 256, 2, 4, true, true, false, 2>;
   const int64_t tiles = static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + C::BA - 1) / C::BA) *
                         ((g.I + C::BB - 1) / C::BB);
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;

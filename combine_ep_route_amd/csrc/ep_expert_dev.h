@@ -163,11 +163,10 @@ struct Core {
   static constexpr int JA = BA / 8 / NW, JB = BB / 8 / NW;   // 1 KiB loads a wave issues per step
   static constexpr int SCALES = F8 ? NT * 4 : 0;
   static constexpr int STAGE = (BA + BB) * kPiece + SCALES;
-  static constexpr int LOADS = JA + JB + (F8 ? 1 : 0);
   static_assert(BA / 8 % NW == 0 && BB / 8 % NW == 0, "loads must divide over the waves");
   static_assert(TA % 16 == 0 && TB % 16 == 0, "whole fragments");
   static_assert(!F8 || (!ANC && !BNC && BB + 2 <= NT), "FP8 operands lie along");
-  static_assert(ST >= 2 && ST <= 4 && LOADS * (ST - 2) < 64, "the wait counts at most 63 loads");
+  static_assert(ST >= 2 && ST <= 4 && (JA + JB + 1) * (ST - 2) < 64, "the wait counts at most 63 loads");
 
   typedef f32x4 Acc[FA][FB];
 
@@ -188,15 +187,19 @@ struct Core {
     return ((at >> 5) ^ (mix(across_row<B>(g)) & (B / 16 - 1))) * 16 + ((at >> 4) & 1) * 8;
   }
 
-  template <class Src>
+  // 1 KiB loads of the second operand that NJ fragments of each wave column need, and all loads of a step.
+  static constexpr int loads_b(int nj) { return BNC ? JB : (2 * nj + WA - 1) / WA < JB ? (2 * nj + WA - 1) / WA : JB; }
+  static constexpr int loads(int nj) { return JA + loads_b(nj) + (F8 ? 1 : 0); }
+
+  template <int NJ, class Src>
   static __device__ __forceinline__ void issue(Src& src, int step, uint8_t* buf) {
     const int w = wave_id();
-    if constexpr (F8) load_lds4(src.scale(step), buf + (BA + BB) * kPiece + w * 256);
     src.step(step);
+    if constexpr (F8) load_lds4(src.scale(step), buf + (BA + BB) * kPiece + w * 256);
 #pragma unroll
     for (int j = 0; j < JA; ++j) load_lds16(src.a(j, step), buf + (j * NW + w) * 1024);
 #pragma unroll
-    for (int j = 0; j < JB; ++j) load_lds16(src.b(j, step), buf + BA * kPiece + (j * NW + w) * 1024);
+    for (int j = 0; j < loads_b(NJ); ++j) load_lds16(src.b(j, step), buf + BA * kPiece + (j * NW + w) * 1024);
   }
 
   // 16 rows or columns from `from` of the step's half s, 8 contracted values a lane: lane group
@@ -207,8 +210,9 @@ struct Core {
   }
   template <int B>
   static __device__ __forceinline__ i32x4 across_frag(const uint8_t* t, int from, int s) {
-    const int l = lane_id(), q = l >> 4, k = s * 32 + q * 8 + ((l & 15) >> 2);
-    const uint8_t* p = t + k * (B * 2) + (((from >> 4) ^ (mix(k) & (B / 16 - 1))) << 5) + (l & 3) * 8;
+    const int l = lane_id(), k = (l >> 4) * 8 + ((l & 15) >> 2);   // mix(k + 32) == mix(k)
+    const int at = (k * (B * 2) + ((mix(k) & (B / 16 - 1)) << 5) + (l & 3) * 8) ^ (from << 1);
+    const uint8_t* p = t + at + s * 32 * (B * 2);
     typedef __attribute__((address_space(3))) s16x4 lds4;
     union { s16x4 h[2]; i32x4 v; } u;
     u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
@@ -275,100 +279,118 @@ struct Core {
     }
   }
 
-  // Half a step of bf16 (32 contracted values): the fragments, and their products.
-  template <int NJ>
-  struct Frags {
-    i32x4 a[FA], b[NJ];
-  };
-  template <int NJ, class Src>
-  static __device__ __forceinline__ void read(const Src&, const uint8_t* buf, int half, int fa, Frags<NJ>& f) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) f.b[j] = frag_b(buf + BA * kPiece, from_b(j), half);
-#pragma unroll
-    for (int i = 0; i < FA; ++i) f.a[i] = frag_a(buf, Src::frag_a_at(fa, i), half);
-  }
-  template <int NJ>
-  static __device__ __forceinline__ void multiply(const Frags<NJ>& f, Acc& acc) {
-#pragma unroll
-    for (int i = 0; i < FA; ++i)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.a[i]),
-                                                            __builtin_bit_cast(bf16x8, f.b[j]), acc[i][j], 0, 0, 0);
-  }
-
   template <int NJ, class Src>
   static __device__ __forceinline__ void compute(const Src& src, const uint8_t* buf, Acc& acc, int fa) {
     if constexpr (F8) {
       compute_fp8<NJ>(src, buf, acc, fa);
     } else {
-      Frags<NJ> f;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        read<NJ>(src, buf, s, fa, f);
-        multiply<NJ>(f, acc);
+        i32x4 a[FA], b[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) b[j] = frag_b(buf + BA * kPiece, from_b(j), s);
+#pragma unroll
+        for (int i = 0; i < FA; ++i) a[i] = frag_a(buf, Src::frag_a_at(fa, i), s);
+#pragma unroll
+        for (int i = 0; i < FA; ++i)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[i]),
+                                                                __builtin_bit_cast(bf16x8, b[j]), acc[i][j], 0, 0, 0);
       }
     }
   }
 
   // Ring of ST stages, each an array of its own so that the compiler sees that the loads into one do not
-  // touch the others.  At step t: wait for stage t (the loads of at most ST-2 later steps stay in flight),
-  // meet, start the loads of step t+ST-1 into the stage that step t-1 read (every wave has read it: its LDS
-  // reads ended before the barrier), multiply.
-  template <int NJ, class Src>
-  static __device__ __forceinline__ void ring_step(Src& src, int t, int steps, uint8_t* cur, uint8_t* next, Acc& acc,
-                                                   int fa) {
-    if (ST > 2 && t + ST - 2 < steps) wait_and_meet<LOADS * (ST - 2)>();
-    else wait_and_meet<0>();
-    if (t + ST - 1 < steps) issue(src, t + ST - 1, next);
+  // touch the others.  At step t: wait for stage t (the loads of LEFT later steps stay in flight), meet,
+  // start the loads of step t+ST-1 into the stage that step t-1 read (every wave has read it: its LDS reads
+  // ended before the barrier), multiply.
+  template <int NJ, int LEFT, bool MORE, class Src>
+  static __device__ __forceinline__ void ring_step(Src& src, int t, uint8_t* cur, uint8_t* next, Acc& acc, int fa) {
+    wait_and_meet<loads(NJ) * LEFT>();
+    if constexpr (MORE) issue<NJ>(src, t + ST - 1, next);
     compute<NJ>(src, cur, acc, fa);
   }
-
-  // Two stages in bf16: the fragments of a half step are read while the products of the half before run.
-  // In the middle of step t every wave holds the second half of stage t in registers, so that stage takes
-  // the loads of step t+2; stage t+1 was started a whole step earlier.
-  template <int NJ, class Src>
-  static __device__ __forceinline__ void piped_step(Src& src, int t, int steps, uint8_t* cur, uint8_t* next, Acc& acc,
-                                                    int fa, Frags<NJ>& f0) {
-    Frags<NJ> f1;
-    read<NJ>(src, cur, 1, fa, f1);
-    multiply<NJ>(f0, acc);
-    __builtin_amdgcn_sched_barrier(0);
-    wait_and_meet<0>();
-    if (t + 2 < steps) issue(src, t + 2, cur);
-    if (t + 1 < steps) read<NJ>(src, next, 0, fa, f0);
-    multiply<NJ>(f1, acc);
-    __builtin_amdgcn_sched_barrier(0);
+  // Steps t .. t+ST-1; LAST: only the first of them has loads left to start.
+  template <int NJ, bool LAST, class Src>
+  static __device__ __forceinline__ void ring_round(Src& src, int t, Acc& acc, int fa, uint8_t* s0, uint8_t* s1,
+                                                    uint8_t* s2, uint8_t* s3) {
+    uint8_t* const last = ST == 2 ? s1 : ST == 3 ? s2 : s3;
+    ring_step<NJ, ST - 2, true>(src, t, s0, last, acc, fa);
+    ring_step<NJ, LAST && ST == 2 ? 0 : ST - 2, !LAST>(src, t + 1, s1, s0, acc, fa);
+    if constexpr (ST > 2) ring_step<NJ, LAST ? ST - 3 : ST - 2, !LAST>(src, t + 2, s2, s1, acc, fa);
+    if constexpr (ST > 3) ring_step<NJ, LAST ? ST - 4 : ST - 2, !LAST>(src, t + 3, s3, s2, acc, fa);
   }
 
+  // Two stages in bf16: a software pipeline over the first operand's fragments.  While the NJ products of
+  // fragment i run, fragment i+2 is read; with the last two run those of the next half step's first two and
+  // its second operand.  When a stage's last fragment is in registers, the stage takes the loads of two
+  // steps on; the next stage was started a whole step earlier.
+  template <int NJ, int HALF, bool MORE, bool NEXT, class Src>
+  static __device__ __forceinline__ void piped_half(Src& src, int t, uint8_t* cur, uint8_t* next, Acc& acc, int fa,
+                                                    i32x4 (&b)[NJ], i32x4 (&a)[2]) {
+    i32x4 c[NJ];
+#pragma unroll
+    for (int i = 0; i < FA; ++i) {
+      i32x4 ahead = {};
+      if (i + 2 < FA) {
+        ahead = frag_a(cur, Src::frag_a_at(fa, i + 2), HALF);
+      } else if (HALF == 0 || NEXT) {
+        const uint8_t* from = HALF == 0 ? cur : next;
+        if (i == FA - 2) {
+          if constexpr (HALF == 1) {
+            wait_and_meet<0>();
+            if constexpr (MORE) issue<NJ>(src, t + 2, cur);
+          }
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) c[j] = frag_b(from + BA * kPiece, from_b(j), 1 - HALF);
+        }
+        ahead = frag_a(from, Src::frag_a_at(fa, i + 2 - FA), 1 - HALF);
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[i & 1]),
+                                                            __builtin_bit_cast(bf16x8, b[j]), acc[i][j], 0, 0, 0);
+      a[i & 1] = ahead;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) b[j] = c[j];
+  }
+  template <int NJ, bool MORE, bool NEXT, class Src>
+  static __device__ __forceinline__ void piped_step(Src& src, int t, uint8_t* cur, uint8_t* next, Acc& acc, int fa,
+                                                    i32x4 (&b)[NJ], i32x4 (&a)[2]) {
+    piped_half<NJ, 0, false, true>(src, t, cur, next, acc, fa, b, a);
+    piped_half<NJ, 1, MORE, NEXT>(src, t, cur, next, acc, fa, b, a);
+  }
+
+  // The steps are rounded up to whole rounds (sources give zeros past the end), and the loops hold no
+  // condition: with one, the compiler waits for all LDS reads where blocks join.
   template <int NJ, class Src>
   static __device__ __forceinline__ void run(Src& src, int steps, Acc& acc, uint8_t* s0, uint8_t* s1, uint8_t* s2,
                                              uint8_t* s3) {
     const int fa = (wave_id() % WA) * Src::wave_span_a();
-    if (steps <= 0) return;
-    issue(src, 0, s0);
+    issue<NJ>(src, 0, s0);
+    int t = 0;
     if constexpr (ST == 2 && !F8) {
-      Frags<NJ> f0;
-      if (steps > 1) {
-        issue(src, 1, s1);
-        wait_and_meet<LOADS>();
-      } else {
-        wait_and_meet<0>();
+      i32x4 b[NJ], a[2];
+      issue<NJ>(src, 1, s1);
+      wait_and_meet<loads(NJ)>();
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) b[j] = frag_b(s0 + BA * kPiece, from_b(j), 0);
+      a[0] = frag_a(s0, Src::frag_a_at(fa, 0), 0);
+      a[1] = frag_a(s0, Src::frag_a_at(fa, 1), 0);
+      for (; t + 2 < steps; t += 2) {
+        piped_step<NJ, true, true>(src, t, s0, s1, acc, fa, b, a);
+        piped_step<NJ, true, true>(src, t + 1, s1, s0, acc, fa, b, a);
       }
-      read<NJ>(src, s0, 0, fa, f0);
-      for (int t = 0; t < steps; t += 2) {
-        piped_step<NJ>(src, t, steps, s0, s1, acc, fa, f0);
-        if (t + 1 < steps) piped_step<NJ>(src, t + 1, steps, s1, s0, acc, fa, f0);
-      }
-      return;
-    }
-    if (ST > 2 && steps > 1) issue(src, 1, s1);
-    if (ST > 3 && steps > 2) issue(src, 2, s2);
-    for (int t = 0; t < steps; t += ST) {
-      ring_step<NJ>(src, t, steps, s0, ST == 2 ? s1 : ST == 3 ? s2 : s3, acc, fa);
-      if (t + 1 < steps) ring_step<NJ>(src, t + 1, steps, s1, s0, acc, fa);
-      if (ST > 2 && t + 2 < steps) ring_step<NJ>(src, t + 2, steps, s2, s1, acc, fa);
-      if (ST > 3 && t + 3 < steps) ring_step<NJ>(src, t + 3, steps, s3, s2, acc, fa);
+      piped_step<NJ, false, true>(src, t, s0, s1, acc, fa, b, a);
+      piped_step<NJ, false, false>(src, t + 1, s1, s0, acc, fa, b, a);
+    } else {
+      if constexpr (ST > 2) issue<NJ>(src, 1, s1);
+      if constexpr (ST > 3) issue<NJ>(src, 2, s2);
+      for (; t + ST < steps; t += ST) ring_round<NJ, false>(src, t, acc, fa, s0, s1, s2, s3);
+      ring_round<NJ, true>(src, t, acc, fa, s0, s1, s2, s3);
     }
   }
 
@@ -379,6 +401,7 @@ struct Core {
     __shared__ __attribute__((aligned(1024))) uint8_t s1[STAGE];
     __shared__ __attribute__((aligned(1024))) uint8_t s2[ST > 2 ? STAGE : 16];
     __shared__ __attribute__((aligned(1024))) uint8_t s3[ST > 3 ? STAGE : 16];
+    if (steps <= 0) return;
     constexpr int Q = FB >= 4 ? FB / 4 : 1;   // the loop exists for one to four quarters of the fragments
     const int quarters = (rows + 16 * WB * Q - 1) / (16 * WB * Q);
     if (Q < FB && quarters <= 1) run<Q>(src, steps, acc, s0, s1, s2, s3);
