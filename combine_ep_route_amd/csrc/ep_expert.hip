@@ -15,13 +15,15 @@ enum Kind { kLinear, kGated, kGatedGrad };
 // ---------------------------------------------------------------------------
 
 // Gated tiles hold half their columns' gate weights and then the same columns' up weights, and a wave the
-// same columns of both, so that the product of the two is formed in its registers.
+// same columns of both, so that the product of the two is formed in its registers.  Rows past the expert's
+// last one and columns past the last one are read as zeros and not stored.
 template <class C, bool GATED>
 struct AlongSrc {
-  const uint8_t* pa[C::JA];
-  const uint8_t* pb[C::JB];
-  const uint8_t* ps;
-  int limit;
+  static constexpr int kCols = GATED ? C::BA / 2 : C::BA;
+  static_assert(!GATED || kCols % (C::NW * 8) == 0, "a load holds rows of one matrix");
+  const uint8_t *w0, *w1, *x, *sc;   // bases of the next step
+  int offa[C::JA], offb[C::JB], offs;
+  int left;                          // bytes of the contraction behind this lane's piece
   bool inside;
 
   static constexpr int wave_span_a() { return GATED ? C::TA / 2 : C::TA; }
@@ -34,40 +36,51 @@ struct AlongSrc {
 
   __device__ __forceinline__ AlongSrc(const AlongArgs& a, const Span& s, int n0, int m0) {
     const int w = wave_id(), piece = C::along_piece() * 16;
-    constexpr int cols = GATED ? C::BA / 2 : C::BA;
-    limit = static_cast<int>(a.k_bytes) - piece;
+    const int row0 = first_row(a.rows, s, m0);
+    w0 = a.w[0] + s.e * a.w_expert[0] + n0 * a.ld_w[0] - kPiece;
+    w1 = GATED ? a.w[1] + s.e * a.w_expert[1] + n0 * a.ld_w[1] - kPiece : nullptr;
+    x = a.x + row0 * a.ld_x - kPiece;
+    left = static_cast<int>(a.k_bytes) - piece + kPiece;
 #pragma unroll
     for (int j = 0; j < C::JA; ++j) {
       const int r = (j * C::NW + w) * 8 + C::along_row();
-      const bool second = GATED && r >= cols;
-      int n = n0 + (second ? r - cols : r);
-      n = n < a.N ? n : a.N - 1;   // columns past the last one are not stored
-      pa[j] = (second ? a.w[1] + s.e * a.w_expert[1] + n * a.ld_w[1] : a.w[0] + s.e * a.w_expert[0] + n * a.ld_w[0]) + piece;
+      const bool second = GATED && j >= C::JA / 2;
+      const int n = second ? r - kCols : r;
+      offa[j] = n0 + n < a.N ? n * static_cast<int>(a.ld_w[second]) + piece : kOutside;
     }
 #pragma unroll
-    for (int j = 0; j < C::JB; ++j) pb[j] = a.x + row(a, s, m0 + (j * C::NW + w) * 8 + C::along_row()) * a.ld_x + piece;
+    for (int j = 0; j < C::JB; ++j) {
+      const int p = m0 + (j * C::NW + w) * 8 + C::along_row();
+      offb[j] = p < s.count ? (row_of(a.rows, s, p) - row0) * static_cast<int>(a.ld_x) + piece : kOutside;
+    }
     if constexpr (C::F8) {
       const int t = threadIdx.x;
-      if (t < C::BB) {
-        ps = a.x_scales + row(a, s, m0 + t) * a.ld_xs;
+      if (w < C::WS / 64) {
+        sc = a.x_scales + row0 * a.ld_xs - 4;
+        offs = t < C::BB && m0 + t < s.count ? (row_of(a.rows, s, m0 + t) - row0) * static_cast<int>(a.ld_xs) : kOutside;
       } else {
-        // thread BB: the scale of the tile's first 128 columns; BB + 1: of the second matrix or 128 columns
-        const int second = t == C::BB + 1, last = (a.N - 1) >> 7;
-        int nb = (n0 >> 7) + (GATED ? 0 : second);
-        nb = nb < last ? nb : last;
-        const int at = GATED ? second : 0;
-        ps = a.w_scales[at] + s.e * a.ws_expert[at] + nb * a.ld_ws[at];
+        // the first weight scale: of the tile's first 128 columns; the second: of the second matrix, or of
+        // the next 128 columns
+        const int second = w > C::WS / 64, nb = (n0 >> 7) + (GATED ? 0 : second), at = GATED ? second : 0;
+        sc = a.w_scales[at] + s.e * a.ws_expert[at] + nb * a.ld_ws[at] - 4;
+        offs = w < C::WS / 64 + 2 && lane_id() == 0 && nb * 128 < a.N ? 0 : kOutside;
       }
     }
   }
-  // rows past the expert's last one are read as its last row, and not stored
-  static __device__ __forceinline__ int64_t row(const AlongArgs& a, const Span& s, int p) {
-    return row_of(a.rows, s, p < s.count ? p : s.count - 1);
+  __device__ __forceinline__ void step(int) {
+    w0 += kPiece;
+    if (GATED) w1 += kPiece;
+    x += kPiece;
+    left -= kPiece;
+    inside = left > 0;
+    if (C::F8) sc += 4;
   }
-  __device__ __forceinline__ void step(int t) { inside = t * kPiece < limit; }
-  __device__ __forceinline__ const uint8_t* a(int j, int t) const { return inside ? pa[j] + t * kPiece : zeros(); }
-  __device__ __forceinline__ const uint8_t* b(int j, int t) const { return inside ? pb[j] + t * kPiece : zeros(); }
-  __device__ __forceinline__ const uint8_t* scale(int t) const { return inside ? ps + t * 4 : zeros(); }
+  __device__ __forceinline__ Rsrc a_rsrc(int j) const { return rsrc(GATED && j >= C::JA / 2 ? w1 : w0, kExtent); }
+  __device__ __forceinline__ Rsrc b_rsrc() const { return rsrc(x, kExtent); }
+  __device__ __forceinline__ Rsrc scale_rsrc() const { return rsrc(sc, kExtent); }
+  __device__ __forceinline__ int a(int j) const { return inside ? offa[j] : kOutside; }
+  __device__ __forceinline__ int b(int j) const { return inside ? offb[j] : kOutside; }
+  __device__ __forceinline__ int scale() const { return inside ? offs : kOutside; }
 };
 
 template <class C, int KIND, int ACT>
@@ -135,57 +148,42 @@ __global__ __launch_bounds__(C::NT) void along_kernel(AlongArgs a) {
 
 template <class C>
 struct RowGradSrc {
-  const RowGradArgs& g;
-  const Span& s;
-  const uint8_t* pa[C::JA];   // advanced step by step
-  const uint8_t* pb[C::JB];
-  int64_t advance;
-  int n0, m0, steps, part, left;
+  const uint8_t *w, *dy;      // bases of the step
+  int64_t ld_w;
+  int offa[C::JA], offb[C::JB];
+  int left;                   // contracted rows from the step on
 
   static constexpr int wave_span_a() { return C::TA; }
   static __device__ __forceinline__ int frag_a_at(int fa, int i) { return fa + i * 16; }
 
-  __device__ __forceinline__ RowGradSrc(const RowGradArgs& g_, const Span& s_, int n0_, int m0_)
-      : g(g_), s(s_), n0(n0_), m0(m0_), steps((g_.I + kStepRows - 1) / kStepRows), part(-1) {}
-
-  __device__ __forceinline__ void begin(int which) {
-    const int w = wave_id();
+  __device__ __forceinline__ RowGradSrc(const RowGradArgs& g, const Span& s, int n0, int m0, int part) {
+    const int v = wave_id(), row0 = first_row(g.rows, s, m0);
+    ld_w = g.ld_w[part];
+    const int64_t ld_dy = g.ld_dy[part];
 #pragma unroll
     for (int j = 0; j < C::JA; ++j) {
-      const int at = j * C::NW + w;
-      int n = n0 + C::template across_col<C::BA>(at);
-      n = n < g.N ? n : 0;   // columns past the last one are not stored
-      pa[j] = g.w[which] + s.e * g.w_expert[which] + C::template across_row<C::BA>(at) * g.ld_w[which] + n * 2;
+      const int l = j * C::NW + v, n = n0 + C::template across_col<C::BA>(l);
+      offa[j] = n < g.N ? C::template across_row<C::BA>(l) * static_cast<int>(ld_w) + n * 2 : kOutside;
     }
 #pragma unroll
     for (int j = 0; j < C::JB; ++j) {
-      const int p = m0 + (j * C::NW + w) * 8 + C::along_row();
-      pb[j] = g.dy[which] + static_cast<int64_t>(row_of(g.rows, s, p < s.count ? p : s.count - 1)) * g.ld_dy[which] +
-              C::along_piece() * 16;
+      const int p = m0 + (j * C::NW + v) * 8 + C::along_row();
+      offb[j] = p < s.count ? (row_of(g.rows, s, p) - row0) * static_cast<int>(ld_dy) + C::along_piece() * 16 : kOutside;
     }
-    advance = g.ld_w[which] * kStepRows;
-    part = which;
-    left = g.I;
+    w = g.w[part] + s.e * g.w_expert[part] - ld_w * kStepRows;
+    dy = g.dy[part] + row0 * ld_dy - kPiece;
+    left = g.I + kStepRows;
   }
-  // the core asks for every step once, in order
-  __device__ __forceinline__ void step(int t) {
-    const int which = g.parts == 2 && t >= steps;
-    if (which != part) {
-      begin(which);
-      return;
-    }
+  __device__ __forceinline__ void step(int) {
     left -= kStepRows;
-#pragma unroll
-    for (int j = 0; j < C::JA; ++j) pa[j] += advance;
-#pragma unroll
-    for (int j = 0; j < C::JB; ++j) pb[j] += kPiece;
+    w += ld_w * kStepRows;
+    dy += kPiece;
   }
-  __device__ __forceinline__ const uint8_t* a(int j, int) const {
-    return C::template across_row<C::BA>(j * C::NW + wave_id()) < left ? pa[j] : zeros();
-  }
-  __device__ __forceinline__ const uint8_t* b(int j, int) const {
-    return C::along_piece() * 8 < left ? pb[j] : zeros();
-  }
+  // contracted rows past the last one lie behind the extent
+  __device__ __forceinline__ Rsrc a_rsrc(int) const { return rsrc(w, extent_of(left * ld_w)); }
+  __device__ __forceinline__ Rsrc b_rsrc() const { return rsrc(dy, kExtent); }
+  __device__ __forceinline__ int a(int j) const { return offa[j]; }
+  __device__ __forceinline__ int b(int j) const { return C::along_piece() * 8 < left ? offb[j] : kOutside; }
 };
 
 template <class C>
@@ -198,8 +196,11 @@ __global__ __launch_bounds__(C::NT) void row_grad_kernel(RowGradArgs g) {
   if (m0 >= s.count) return;
 
   typename C::Acc acc = {};
-  RowGradSrc<C> src(g, s, n0, m0);
-  C::run(src, src.steps * g.parts, s.count - m0, acc);
+  for (int part = 0; part < g.parts; ++part) {
+    if (part > 0) wait_and_meet<0>();   // the first part's LDS reads have ended
+    RowGradSrc<C> src(g, s, n0, m0, part);
+    C::run(src, (g.I + kStepRows - 1) / kStepRows, s.count - m0, acc);
+  }
 
   const int l = lane_id(), w = wave_id();
 #pragma unroll
@@ -219,31 +220,66 @@ __global__ __launch_bounds__(C::NT) void row_grad_kernel(RowGradArgs g) {
 // Gradient of the weights: dw[e][i][h] = sum over the expert's rows r of dy[r][i] x[r][h]
 // ---------------------------------------------------------------------------
 
-template <class C>
+// LIST: the rows are looked up step by step (LL, many sources); else they follow each other.  Rows past the
+// expert's last one are zeros in both operands.
+template <class C, bool LIST>
 struct WeightGradSrc {
   const WeightGradArgs& g;
   const Span& s;
-  const uint8_t* dy;
+  const uint8_t *x, *dy;      // bases of the step; with a list the expert's first slot
   int64_t ld_dy;
-  int h0, i0;
+  int offa[C::JA], offb[C::JB];
+  int h0, i0, left;
 
   static constexpr int wave_span_a() { return C::TA; }
   static __device__ __forceinline__ int frag_a_at(int fa, int i) { return fa + i * 16; }
-  __device__ __forceinline__ void step(int) {}
-  // rows past the expert's last one are zeros in both operands; columns past the last one are not stored
-  __device__ __forceinline__ const uint8_t* a(int j, int t) const {
-    const int at = j * C::NW + wave_id(), p = t * kStepRows + C::template across_row<C::BA>(at);
-    const int h = h0 + C::template across_col<C::BA>(at);
-    return p < s.count ? g.x + static_cast<int64_t>(row_of(g.rows, s, p)) * g.ld_x + (h < g.H ? h : 0) * 2 : zeros();
+
+  __device__ __forceinline__ WeightGradSrc(const WeightGradArgs& g_, const Span& s_, int which, int h0_, int i0_)
+      : g(g_), s(s_), ld_dy(g_.ld_dy[which]), h0(h0_), i0(i0_) {
+    const int v = wave_id(), back = LIST ? 0 : kStepRows;
+    x = g.x + (s.first - back) * g.ld_x;
+    dy = g.dy[which] + (s.first - back) * ld_dy;
+    left = s.count + kStepRows;
+    if constexpr (!LIST) {
+#pragma unroll
+      for (int j = 0; j < C::JA; ++j) offa[j] = offset_a(j, C::template across_row<C::BA>(j * C::NW + v));
+#pragma unroll
+      for (int j = 0; j < C::JB; ++j) offb[j] = offset_b(j, C::template across_row<C::BB>(j * C::NW + v));
+    }
   }
-  __device__ __forceinline__ const uint8_t* b(int j, int t) const {
-    const int at = j * C::NW + wave_id(), p = t * kStepRows + C::template across_row<C::BB>(at);
-    const int i = i0 + C::template across_col<C::BB>(at);
-    return p < s.count ? dy + static_cast<int64_t>(row_of(g.rows, s, p)) * ld_dy + (i < g.I ? i : 0) * 2 : zeros();
+  __device__ __forceinline__ int offset_a(int j, int row) const {
+    const int h = h0 + C::template across_col<C::BA>(j * C::NW + wave_id());
+    return h < g.H ? row * static_cast<int>(g.ld_x) + h * 2 : kOutside;
   }
+  __device__ __forceinline__ int offset_b(int j, int row) const {
+    const int i = i0 + C::template across_col<C::BB>(j * C::NW + wave_id());
+    return i < g.I ? row * static_cast<int>(ld_dy) + i * 2 : kOutside;
+  }
+  __device__ __forceinline__ void step(int) {
+    left -= kStepRows;
+    if constexpr (!LIST) {
+      x += g.ld_x * kStepRows;
+      dy += ld_dy * kStepRows;
+    } else {
+#pragma unroll
+      for (int j = 0; j < C::JA; ++j) {
+        const int r = C::template across_row<C::BA>(j * C::NW + wave_id());
+        offa[j] = r < left ? offset_a(j, row_of(g.rows, s, s.count - left + r) - s.first) : kOutside;
+      }
+#pragma unroll
+      for (int j = 0; j < C::JB; ++j) {
+        const int r = C::template across_row<C::BB>(j * C::NW + wave_id());
+        offb[j] = r < left ? offset_b(j, row_of(g.rows, s, s.count - left + r) - s.first) : kOutside;
+      }
+    }
+  }
+  __device__ __forceinline__ Rsrc a_rsrc(int) const { return rsrc(x, LIST ? kExtent : extent_of(left * g.ld_x)); }
+  __device__ __forceinline__ Rsrc b_rsrc() const { return rsrc(dy, LIST ? kExtent : extent_of(left * ld_dy)); }
+  __device__ __forceinline__ int a(int j) const { return offa[j]; }
+  __device__ __forceinline__ int b(int j) const { return offb[j]; }
 };
 
-template <class C, bool F32>
+template <class C, bool F32, bool LIST>
 __global__ __launch_bounds__(C::NT) void weight_grad_kernel(WeightGradArgs g) {
   const int ht = (g.H + C::BA - 1) / C::BA, it = (g.I + C::BB - 1) / C::BB;
   const int per = ht * it * g.parts;
@@ -255,7 +291,7 @@ __global__ __launch_bounds__(C::NT) void weight_grad_kernel(WeightGradArgs g) {
   const int which = local / (ht * it), at = local - which * ht * it, i0 = at / ht * C::BB, h0 = at % ht * C::BA;
 
   typename C::Acc acc = {};
-  WeightGradSrc<C> src{g, s, g.dy[which], g.ld_dy[which], h0, i0};
+  WeightGradSrc<C, LIST> src(g, s, which, h0, i0);
   C::run(src, (s.count + kStepRows - 1) / kStepRows, g.I - i0, acc);
 
   const int l = lane_id(), w = wave_id();
@@ -376,8 +412,13 @@ hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t str
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
   if (check) return hipSuccess;
   const int blocks = static_cast<int>((tiles + 7) / 8 * 8);
-  if (f32) weight_grad_kernel<C, true><<<blocks, C::NT, 0, stream>>>(g);
-  else weight_grad_kernel<C, false><<<blocks, C::NT, 0, stream>>>(g);
+  if (g.rows.list) {
+    if (f32) weight_grad_kernel<C, true, true><<<blocks, C::NT, 0, stream>>>(g);
+    else weight_grad_kernel<C, false, true><<<blocks, C::NT, 0, stream>>>(g);
+  } else {
+    if (f32) weight_grad_kernel<C, true, false><<<blocks, C::NT, 0, stream>>>(g);
+    else weight_grad_kernel<C, false, false><<<blocks, C::NT, 0, stream>>>(g);
+  }
   return hipGetLastError();
 }
 

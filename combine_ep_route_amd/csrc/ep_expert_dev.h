@@ -27,17 +27,26 @@ typedef __attribute__((ext_vector_type(8))) int i32x8;
 constexpr int kPiece = 128;    // bytes of the contraction one step holds of an "along" row
 constexpr int kStepRows = 64;  // contracted rows one step holds of an "across" operand
 
-// Source of the pieces that lie outside an operand: read as zeros.
-__device__ const uint4 kZeros = {0, 0, 0, 0};
-__device__ __forceinline__ const uint8_t* zeros() { return reinterpret_cast<const uint8_t*>(&kZeros); }
+// Loads go through buffer descriptors: 32-bit offsets from a base that all lanes share, and what lies
+// outside the descriptor's extent is read as zeros.
+constexpr int kOutside = -1;             // an offset outside every extent
+constexpr uint32_t kExtent = 0x7fffffffu;   // an extent for offsets that were checked on the host
 
-__device__ __forceinline__ void load_lds16(const uint8_t* g, uint8_t* l) {
-  __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) const void*)g,
-                                   (__attribute__((address_space(3))) void*)l, 16, 0, 0);
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+
+__device__ __forceinline__ Rsrc rsrc(const uint8_t* base, uint32_t extent) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, static_cast<int>(extent), 0x27000);
 }
-__device__ __forceinline__ void load_lds4(const uint8_t* g, uint8_t* l) {
-  __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) const void*)g,
-                                   (__attribute__((address_space(3))) void*)l, 4, 0, 0);
+__device__ __forceinline__ uint32_t extent_of(int64_t bytes) {
+  return bytes <= 0 ? 0u : bytes < kExtent ? static_cast<uint32_t>(bytes) : kExtent;
+}
+
+// Straight to LDS: lane l's bytes go to l + 16 l (l + 4 l).
+__device__ __forceinline__ void load_lds16(Rsrc r, int offset, uint8_t* l) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 16, offset, 0, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(Rsrc r, int offset, uint8_t* l) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 4, offset, 0, 0, 0);
 }
 
 // Waits until at most N of this wave's vector loads are in flight and all its LDS reads and writes
@@ -143,6 +152,10 @@ __device__ __forceinline__ Span find_span(const ExpertRows& r, int which, int co
   return s;
 }
 
+// The row that offsets in a tile from its row m0 on count from.
+__device__ __forceinline__ int64_t first_row(const ExpertRows& r, const Span& s, int m0) {
+  return r.list ? s.first : s.first + m0;
+}
 __device__ __forceinline__ int row_of(const ExpertRows& r, const Span& s, int p) {
   return r.list ? r.list[s.before + p] : s.first + p;
 }
@@ -161,11 +174,14 @@ struct Core {
   static constexpr int TA = BA / WA, TB = BB / WB;   // a wave's part
   static constexpr int FA = TA / 16, FB = TB / 16;   // in 16 x 16 fragments
   static constexpr int JA = BA / 8 / NW, JB = BB / 8 / NW;   // 1 KiB loads a wave issues per step
+  // Scales of a step: the rows' from entry 0, the weights' two at entries WS and WS + 64, each loaded by a
+  // wave of its own.
+  static constexpr int WS = (BB + 63) / 64 * 64;
   static constexpr int SCALES = F8 ? NT * 4 : 0;
   static constexpr int STAGE = (BA + BB) * kPiece + SCALES;
   static_assert(BA / 8 % NW == 0 && BB / 8 % NW == 0, "loads must divide over the waves");
   static_assert(TA % 16 == 0 && TB % 16 == 0, "whole fragments");
-  static_assert(!F8 || (!ANC && !BNC && BB + 2 <= NT), "FP8 operands lie along");
+  static_assert(!F8 || (!ANC && !BNC && WS + 128 <= NT), "FP8 operands lie along");
   static_assert(ST >= 2 && ST <= 4 && (JA + JB + 1) * (ST - 2) < 64, "the wait counts at most 63 loads");
 
   typedef f32x4 Acc[FA][FB];
@@ -194,12 +210,12 @@ struct Core {
   template <int NJ, class Src>
   static __device__ __forceinline__ void issue(Src& src, int step, uint8_t* buf) {
     const int w = wave_id();
-    src.step(step);
-    if constexpr (F8) load_lds4(src.scale(step), buf + (BA + BB) * kPiece + w * 256);
+    src.step(step);   // every step once, in order
+    if constexpr (F8) load_lds4(src.scale_rsrc(), src.scale(), buf + (BA + BB) * kPiece + w * 256);
 #pragma unroll
-    for (int j = 0; j < JA; ++j) load_lds16(src.a(j, step), buf + (j * NW + w) * 1024);
+    for (int j = 0; j < JA; ++j) load_lds16(src.a_rsrc(j), src.a(j), buf + (j * NW + w) * 1024);
 #pragma unroll
-    for (int j = 0; j < loads_b(NJ); ++j) load_lds16(src.b(j, step), buf + BA * kPiece + (j * NW + w) * 1024);
+    for (int j = 0; j < loads_b(NJ); ++j) load_lds16(src.b_rsrc(), src.b(j), buf + BA * kPiece + (j * NW + w) * 1024);
   }
 
   // 16 rows or columns from `from` of the step's half s, 8 contracted values a lane: lane group
@@ -242,7 +258,7 @@ struct Core {
     const uint8_t* ta = buf;
     const uint8_t* tb = buf + BA * kPiece;
     const float* sc = reinterpret_cast<const float*>(buf + (BA + BB) * kPiece);
-    const float w0 = sc[BB], w1 = sc[BB + 1];
+    const float w0 = sc[WS], w1 = sc[WS + 64];
     i32x8 b[NJ];
     float x[NJ], c[NJ];
 #pragma unroll

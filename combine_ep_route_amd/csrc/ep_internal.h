@@ -305,7 +305,10 @@ namespace expert {
 
 // Rows of expert e, p = 0 .. count[e]-1, in the receive layout: list[before(e) + p] with a list (LL, many
 // sources: slots are filled per source); else e*stride + p with a stride (LL, one source); else
-// before(e) + p (HT).  before(e) is the sum of the counts of the experts before e.
+// before(e) + p (HT).  before(e) is the sum of the counts of the experts before e; in LL the slots of
+// expert e are e*stride .. (e+1)*stride - 1.
+// In a tile, offsets are 32-bit: 256 rows of any operand, and with a list an expert's slots, span less than
+// 2^31 bytes.
 struct ExpertRows {
   const int32_t* count;   // [E]
   const int32_t* list;

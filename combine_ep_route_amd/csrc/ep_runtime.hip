@@ -1173,6 +1173,7 @@ ExpertRows rows_of_experts(const Handle* h, int64_t limit) {
     r.count = h->ll_count;
     r.stride = g->cfg.max_tokens_per_rank;
   } else {
+    r.stride = g->cfg.num_src_ranks * g->cfg.max_tokens_per_rank;
     r.count = h->rows_total;
     r.list = h->rows_list;
   }
@@ -1191,6 +1192,15 @@ ep_status_t start_products(Handle* h, hipStream_t s) {
                                     g->cfg.max_tokens_per_rank, h->rows_total, h->rows_list, s));
   return EP_OK;
 }
+
+// 256 rows, and in LL one expert's slots, within 32-bit byte offsets.
+bool short_rows(const Group* g, int64_t ld_bytes) {
+  const int64_t slots = g->cfg.mode == EP_MODE_LL && g->cfg.num_src_ranks > 1
+                            ? static_cast<int64_t>(g->cfg.num_src_ranks) * g->cfg.max_tokens_per_rank : 0;
+  return std::max<int64_t>(256, slots) <= INT32_MAX / ld_bytes;
+}
+bool short_rows(const Group* g, const ep_tensor_t& t) { return short_rows(g, t.strides[0] * dtype_size(t.dtype)); }
+bool short_weights(const ep_tensor_t* t) { return t->strides[1] * dtype_size(t->dtype) <= INT32_MAX / 256; }
 
 ep_status_t fits(hipError_t e) { return e == hipSuccess ? EP_OK : EP_ERR_UNSUPPORTED; }
 
@@ -1287,7 +1297,8 @@ EP_API ep_status_t ep_expert_gated(ep_handle_t handle, const ep_tensor_t* rows, 
     return EP_ERR_INVALID_ARGUMENT;
   if (!geometry_rows(g, out, EP_DTYPE_BF16, I, EP_TAG_TOKENS, true, &o)) return EP_ERR_INVALID_ARGUMENT;
   if (!holds_slots(g, x) || !holds_slots(g, o)) return EP_ERR_INVALID_ARGUMENT;
-  if (I > kMaxProductSize) return EP_ERR_UNSUPPORTED;
+  if (I > kMaxProductSize || !short_rows(g, x) || !short_weights(w_gate) || !short_weights(w_up))
+    return EP_ERR_UNSUPPORTED;
 
   AlongArgs a = along_args(h, x, H, I, std::min(x.sizes[0], o.sizes[0]));
   if (fp8) {
@@ -1331,7 +1342,9 @@ EP_API ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_
   if (!holds_slots(g, x) || !holds_slots(g, d) || !holds_slots(g, dg) || !holds_slots(g, du) ||
       (grad_rows && !holds_slots(g, dx)))
     return EP_ERR_INVALID_ARGUMENT;
-  if (I > kMaxProductSize) return EP_ERR_UNSUPPORTED;
+  if (I > kMaxProductSize || !short_rows(g, x) || !short_rows(g, dg) || !short_rows(g, du) ||
+      !short_weights(w_gate) || !short_weights(w_up))
+    return EP_ERR_UNSUPPORTED;
 
   int64_t limit = std::min({x.sizes[0], d.sizes[0], dg.sizes[0], du.sizes[0]});
   if (grad_rows) limit = std::min(limit, dx.sizes[0]);
@@ -1384,7 +1397,9 @@ EP_API ep_status_t ep_expert_linear(ep_handle_t handle, const ep_tensor_t* x_in,
     return EP_ERR_INVALID_ARGUMENT;
   if (!geometry_rows(g, out, EP_DTYPE_BF16, N, EP_TAG_TOKENS, true, &o)) return EP_ERR_INVALID_ARGUMENT;
   if (!holds_slots(g, x) || !holds_slots(g, o)) return EP_ERR_INVALID_ARGUMENT;
-  if (N > kMaxProductSize || C > kMaxProductSize) return EP_ERR_UNSUPPORTED;
+  if (N > kMaxProductSize || C > kMaxProductSize || !short_rows(g, x) || !short_weights(w) ||
+      (fp8 && !short_rows(g, xs)))
+    return EP_ERR_UNSUPPORTED;
 
   AlongArgs a = along_args(h, x, C, N, std::min(x.sizes[0], o.sizes[0]));
   if (fp8) {
@@ -1418,7 +1433,8 @@ EP_API ep_status_t ep_expert_linear_backward(ep_handle_t handle, const ep_tensor
       (grad_w && !check_weight_grad(g, grad_w, N, C)))
     return EP_ERR_INVALID_ARGUMENT;
   if (!holds_slots(g, x) || !holds_slots(g, d) || (grad_x && !holds_slots(g, dx))) return EP_ERR_INVALID_ARGUMENT;
-  if (N > kMaxProductSize || C > kMaxProductSize) return EP_ERR_UNSUPPORTED;
+  if (N > kMaxProductSize || C > kMaxProductSize || !short_rows(g, x) || !short_rows(g, d) || !short_weights(w))
+    return EP_ERR_UNSUPPORTED;
 
   int64_t limit = std::min(x.sizes[0], d.sizes[0]);
   if (grad_x) limit = std::min(limit, dx.sizes[0]);
