@@ -96,7 +96,7 @@ __global__ __launch_bounds__(C::NT) void along_kernel(AlongArgs a) {
 
   typename C::Acc acc = {};
   AlongSrc<C, GATED> src(a, s, n0, m0);
-  C::run(src, static_cast<int>((a.k_bytes + kPiece - 1) / kPiece), s.count - m0, acc);
+  C::run(One<AlongSrc<C, GATED>>{src}, static_cast<int>((a.k_bytes + kPiece - 1) / kPiece), s.count - m0, acc);
 
   const int l = lane_id(), w = wave_id();
   const int fa = (w % C::WA) * src.wave_span_a();
@@ -187,6 +187,15 @@ struct RowGradSrc {
 };
 
 template <class C>
+struct RowGradPlan {
+  const RowGradArgs& g;
+  const Span& s;
+  int n0, m0;
+  __device__ __forceinline__ int parts() const { return g.parts; }
+  __device__ __forceinline__ RowGradSrc<C> source(int p) const { return RowGradSrc<C>(g, s, n0, m0, p); }
+};
+
+template <class C>
 __global__ __launch_bounds__(C::NT) void row_grad_kernel(RowGradArgs g) {
   const int col_tiles = (g.N + C::BA - 1) / C::BA;
   const Span s = find_span<C::BB>(g.rows, blockIdx.x, col_tiles);
@@ -196,11 +205,7 @@ __global__ __launch_bounds__(C::NT) void row_grad_kernel(RowGradArgs g) {
   if (m0 >= s.count) return;
 
   typename C::Acc acc = {};
-  for (int part = 0; part < g.parts; ++part) {
-    if (part > 0) wait_and_meet<0>();   // the first part's LDS reads have ended
-    RowGradSrc<C> src(g, s, n0, m0, part);
-    C::run(src, (g.I + kStepRows - 1) / kStepRows, s.count - m0, acc);
-  }
+  C::run(RowGradPlan<C>{g, s, n0, m0}, (g.I + kStepRows - 1) / kStepRows, s.count - m0, acc);
 
   const int l = lane_id(), w = wave_id();
 #pragma unroll
@@ -292,7 +297,7 @@ __global__ __launch_bounds__(C::NT) void weight_grad_kernel(WeightGradArgs g) {
 
   typename C::Acc acc = {};
   WeightGradSrc<C, LIST> src(g, s, which, h0, i0);
-  C::run(src, (s.count + kStepRows - 1) / kStepRows, g.I - i0, acc);
+  C::run(One<WeightGradSrc<C, LIST>>{src}, (s.count + kStepRows - 1) / kStepRows, g.I - i0, acc);
 
   const int l = lane_id(), w = wave_id();
 #pragma unroll

@@ -164,6 +164,19 @@ __device__ __forceinline__ int row_of(const ExpertRows& r, const Span& s, int p)
 // The product of one tile
 // ---------------------------------------------------------------------------
 
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
+// A plan of one source.
+template <class Src>
+struct One {
+  const Src& src;
+  static constexpr int parts() { return 1; }
+  __device__ __forceinline__ Src source(int) const { return src; }
+};
+
 // BA x BB results from WA x WB waves; ANC / BNC: the operand lies across (else along); F8: E4M3 operands
 // with scales (both along); ST: stages of the LDS ring.
 template <int BA_, int BB_, int WA_, int WB_, bool ANC_, bool BNC_, bool F8_, int ST_>
@@ -383,8 +396,8 @@ struct Core {
   // The steps are rounded up to whole rounds (sources give zeros past the end), and the loops hold no
   // condition: with one, the compiler waits for all LDS reads where blocks join.
   template <int NJ, class Src>
-  static __device__ __forceinline__ void run(Src& src, int steps, Acc& acc, uint8_t* s0, uint8_t* s1, uint8_t* s2,
-                                             uint8_t* s3) {
+  static __device__ __forceinline__ void run_part(Src& src, int steps, Acc& acc, uint8_t* s0, uint8_t* s1, uint8_t* s2,
+                                                  uint8_t* s3) {
     const int fa = (wave_id() % WA) * Src::wave_span_a();
     issue<NJ>(src, 0, s0);
     int t = 0;
@@ -410,20 +423,28 @@ struct Core {
     }
   }
 
-  // `rows`: rows of the second operand that count.
-  template <class Src>
-  static __device__ __forceinline__ void run(Src& src, int steps, int rows, Acc& acc) {
+  // Sums over the parts of `plan` (plan.parts() sources of `steps` steps each, plan.source(p)).  `rows`:
+  // rows of the second operand that count.
+  template <class Plan>
+  static __device__ __forceinline__ void run(const Plan& plan, int steps, int rows, Acc& acc) {
     __shared__ __attribute__((aligned(1024))) uint8_t s0[STAGE];
     __shared__ __attribute__((aligned(1024))) uint8_t s1[STAGE];
     __shared__ __attribute__((aligned(1024))) uint8_t s2[ST > 2 ? STAGE : 16];
     __shared__ __attribute__((aligned(1024))) uint8_t s3[ST > 3 ? STAGE : 16];
     if (steps <= 0) return;
+    auto all = [&](auto nj) {
+      for (int p = 0; p < plan.parts(); ++p) {
+        if (p > 0) wait_and_meet<0>();   // the part before has read its last stage
+        auto src = plan.source(p);
+        run_part<decltype(nj)::value>(src, steps, acc, s0, s1, s2, s3);
+      }
+    };
     constexpr int Q = FB >= 4 ? FB / 4 : 1;   // the loop exists for one to four quarters of the fragments
     const int quarters = (rows + 16 * WB * Q - 1) / (16 * WB * Q);
-    if (Q < FB && quarters <= 1) run<Q>(src, steps, acc, s0, s1, s2, s3);
-    else if (2 * Q < FB && quarters == 2) run<(2 * Q < FB ? 2 * Q : FB)>(src, steps, acc, s0, s1, s2, s3);
-    else if (3 * Q < FB && quarters == 3) run<(3 * Q < FB ? 3 * Q : FB)>(src, steps, acc, s0, s1, s2, s3);
-    else run<FB>(src, steps, acc, s0, s1, s2, s3);
+    if (Q < FB && quarters <= 1) all(Int<Q>{});
+    else if (2 * Q < FB && quarters == 2) all(Int<(2 * Q < FB ? 2 * Q : FB)>{});
+    else if (3 * Q < FB && quarters == 3) all(Int<(3 * Q < FB ? 3 * Q : FB)>{});
+    else all(Int<FB>{});
   }
 };
 
