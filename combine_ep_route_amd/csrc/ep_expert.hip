@@ -20,7 +20,7 @@ enum Kind { kLinear, kGated, kGatedGrad };
 template <class C, bool GATED>
 struct AlongSrc {
   static constexpr int kCols = GATED ? C::BA / 2 : C::BA;
-  static_assert(!GATED || kCols % (C::NW * 8) == 0, "a load holds rows of one matrix");
+  static_assert(!GATED || kCols % (C::NW * C::ROWS) == 0, "a load holds rows of one matrix");
   const uint8_t *w0, *w1, *x, *sc;   // bases of the next step
   int offa[C::JA], offb[C::JB], offs;
   int left;                          // bytes of the contraction behind this lane's piece
@@ -37,20 +37,20 @@ struct AlongSrc {
   __device__ __forceinline__ AlongSrc(const AlongArgs& a, const Span& s, int n0, int m0) {
     const int w = wave_id(), piece = C::along_piece() * 16;
     const int row0 = first_row(a.rows, s, m0);
-    w0 = a.w[0] + s.e * a.w_expert[0] + n0 * a.ld_w[0] - kPiece;
-    w1 = GATED ? a.w[1] + s.e * a.w_expert[1] + n0 * a.ld_w[1] - kPiece : nullptr;
-    x = a.x + row0 * a.ld_x - kPiece;
-    left = static_cast<int>(a.k_bytes) - piece + kPiece;
+    w0 = a.w[0] + s.e * a.w_expert[0] + n0 * a.ld_w[0] - C::PIECE;
+    w1 = GATED ? a.w[1] + s.e * a.w_expert[1] + n0 * a.ld_w[1] - C::PIECE : nullptr;
+    x = a.x + row0 * a.ld_x - C::PIECE;
+    left = static_cast<int>(a.k_bytes) - piece + C::PIECE;
 #pragma unroll
     for (int j = 0; j < C::JA; ++j) {
-      const int r = (j * C::NW + w) * 8 + C::along_row();
+      const int r = (j * C::NW + w) * C::ROWS + C::along_row();
       const bool second = GATED && j >= C::JA / 2;
       const int n = second ? r - kCols : r;
       offa[j] = n0 + n < a.N ? n * static_cast<int>(a.ld_w[second]) + piece : kOutside;
     }
 #pragma unroll
     for (int j = 0; j < C::JB; ++j) {
-      const int p = m0 + (j * C::NW + w) * 8 + C::along_row();
+      const int p = m0 + (j * C::NW + w) * C::ROWS + C::along_row();
       offb[j] = p < s.count ? (row_of(a.rows, s, p) - row0) * static_cast<int>(a.ld_x) + piece : kOutside;
     }
     if constexpr (C::F8) {
@@ -67,11 +67,11 @@ struct AlongSrc {
       }
     }
   }
-  __device__ __forceinline__ void step(int) {
-    w0 += kPiece;
-    if (GATED) w1 += kPiece;
-    x += kPiece;
-    left -= kPiece;
+  __device__ __forceinline__ void step() {
+    w0 += C::PIECE;
+    if (GATED) w1 += C::PIECE;
+    x += C::PIECE;
+    left -= C::PIECE;
     inside = left > 0;
     if (C::F8) sc += 4;
   }
@@ -96,7 +96,7 @@ __global__ __launch_bounds__(C::NT) void along_kernel(AlongArgs a) {
 
   typename C::Acc acc = {};
   AlongSrc<C, GATED> src(a, s, n0, m0);
-  C::run(One<AlongSrc<C, GATED>>{src}, static_cast<int>((a.k_bytes + kPiece - 1) / kPiece), s.count - m0, acc);
+  C::run(One<AlongSrc<C, GATED>>{src}, static_cast<int>((a.k_bytes + C::PIECE - 1) / C::PIECE), s.count - m0, acc);
 
   const int l = lane_id(), w = wave_id();
   const int fa = (w % C::WA) * src.wave_span_a();
@@ -167,17 +167,17 @@ struct RowGradSrc {
     }
 #pragma unroll
     for (int j = 0; j < C::JB; ++j) {
-      const int p = m0 + (j * C::NW + v) * 8 + C::along_row();
+      const int p = m0 + (j * C::NW + v) * C::ROWS + C::along_row();
       offb[j] = p < s.count ? (row_of(g.rows, s, p) - row0) * static_cast<int>(ld_dy) + C::along_piece() * 16 : kOutside;
     }
-    w = g.w[part] + s.e * g.w_expert[part] - ld_w * kStepRows;
-    dy = g.dy[part] + row0 * ld_dy - kPiece;
-    left = g.I + kStepRows;
+    w = g.w[part] + s.e * g.w_expert[part] - ld_w * C::KROWS;
+    dy = g.dy[part] + row0 * ld_dy - C::PIECE;
+    left = g.I + C::KROWS;
   }
-  __device__ __forceinline__ void step(int) {
-    left -= kStepRows;
-    w += ld_w * kStepRows;
-    dy += kPiece;
+  __device__ __forceinline__ void step() {
+    left -= C::KROWS;
+    w += ld_w * C::KROWS;
+    dy += C::PIECE;
   }
   // contracted rows past the last one lie behind the extent
   __device__ __forceinline__ Rsrc a_rsrc(int) const { return rsrc(w, extent_of(left * ld_w)); }
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(C::NT) void row_grad_kernel(RowGradArgs g) {
   if (m0 >= s.count) return;
 
   typename C::Acc acc = {};
-  C::run(RowGradPlan<C>{g, s, n0, m0}, (g.I + kStepRows - 1) / kStepRows, s.count - m0, acc);
+  C::run(RowGradPlan<C>{g, s, n0, m0}, (g.I + C::KROWS - 1) / C::KROWS, s.count - m0, acc);
 
   const int l = lane_id(), w = wave_id();
 #pragma unroll
@@ -241,10 +241,10 @@ struct WeightGradSrc {
 
   __device__ __forceinline__ WeightGradSrc(const WeightGradArgs& g_, const Span& s_, int which, int h0_, int i0_)
       : g(g_), s(s_), ld_dy(g_.ld_dy[which]), h0(h0_), i0(i0_) {
-    const int v = wave_id(), back = LIST ? 0 : kStepRows;
+    const int v = wave_id(), back = LIST ? 0 : C::KROWS;
     x = g.x + (s.first - back) * g.ld_x;
     dy = g.dy[which] + (s.first - back) * ld_dy;
-    left = s.count + kStepRows;
+    left = s.count + C::KROWS;
     if constexpr (!LIST) {
 #pragma unroll
       for (int j = 0; j < C::JA; ++j) offa[j] = offset_a(j, C::template across_row<C::BA>(j * C::NW + v));
@@ -260,11 +260,11 @@ struct WeightGradSrc {
     const int i = i0 + C::template across_col<C::BB>(j * C::NW + wave_id());
     return i < g.I ? row * static_cast<int>(ld_dy) + i * 2 : kOutside;
   }
-  __device__ __forceinline__ void step(int) {
-    left -= kStepRows;
+  __device__ __forceinline__ void step() {
+    left -= C::KROWS;
     if constexpr (!LIST) {
-      x += g.ld_x * kStepRows;
-      dy += ld_dy * kStepRows;
+      x += g.ld_x * C::KROWS;
+      dy += ld_dy * C::KROWS;
     } else {
 #pragma unroll
       for (int j = 0; j < C::JA; ++j) {
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(C::NT) void weight_grad_kernel(WeightGradArgs g) {
 
   typename C::Acc acc = {};
   WeightGradSrc<C, LIST> src(g, s, which, h0, i0);
-  C::run(One<WeightGradSrc<C, LIST>>{src}, (s.count + kStepRows - 1) / kStepRows, g.I - i0, acc);
+  C::run(One<WeightGradSrc<C, LIST>>{src}, (s.count + C::KROWS - 1) / C::KROWS, g.I - i0, acc);
 
   const int l = lane_id(), w = wave_id();
 #pragma unroll
@@ -369,8 +369,8 @@ hipError_t launch_along_as(const AlongArgs& a, hipStream_t stream, bool check) {
 template <bool F8, int KIND, int ACT>
 hipError_t launch_along_kind(const AlongArgs& a, hipStream_t stream, bool check) {
   if (a.rows_max <= static_cast<int64_t>(a.rows.E) * 32)
-    return launch_along_as<Core<128, 32, 4, 1, false, false, F8, 4>, KIND, ACT>(a, stream, check);
-  return launch_along_as<Core<256, 256, 2, 4, false, false, F8, 2>, KIND, ACT>(a, stream, check);
+    return launch_along_as<Core<128, 32, 4, 1, false, false, F8, 4, 128>, KIND, ACT>(a, stream, check);
+  return launch_along_as<Core<256, 256, 2, 4, false, false, F8, F8 ? 2 : 5, F8 ? 128 : 64>, KIND, ACT>(a, stream, check);
 }
 
 template <bool F8>
@@ -402,7 +402,7 @@ hipError_t launch_gated_grad(const AlongArgs& a, int act, hipStream_t stream, bo
 }
 
 hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check) {
-  using C = Core<256, 256, 2, 4, true, false, false, 2>;
+  using C = Core<256, 256, 2, 4, true, false, false, 5, 64>;
   const int64_t tiles = row_tiles<C::BB>(g.rows, g.rows_max, g.per_expert_max) * ((g.N + C::BA - 1) / C::BA);
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
   if (tiles == 0 || check) return hipSuccess;
@@ -411,7 +411,7 @@ hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check)
 }
 
 hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check) {
-  using C = Core<256, 256, 2, 4, true, true, false, 2>;
+  using C = Core<256, 256, 2, 4, true, true, false, 5, 64>;
   const int64_t tiles = static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + C::BA - 1) / C::BA) *
                         ((g.I + C::BB - 1) / C::BB);
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;

@@ -1,10 +1,10 @@
 // Device core of the experts' products: LDS-tiled matrix products on the matrix unit, fed by loads
 // that go from global memory to LDS without passing registers.
 //
-// Every tile is held as 128-byte pieces, whatever its type and direction:
-//   "along" operands are contiguous in the contracted index: one 128-byte row per output row or
-//   column (64 bf16 or 128 FP8 values of the contraction);
-//   "across" operands are contiguous in the output index: 64 contracted rows of B bf16 values.
+// A step of the contraction brings one tile of each operand to LDS, whatever its type and direction:
+//   "along" operands are contiguous in the contracted index: PIECE bytes of each output row or column
+//   (64 bytes: 32 bf16 values; 128: 64 bf16 or 128 FP8 values);
+//   "across" operands are contiguous in the output index: PIECE/2 contracted rows of bf16 values.
 // Products are formed transposed (weights as the first operand, rows as the second), so that the
 // four results a lane holds are four consecutive columns of one output row: 8-byte stores.
 #pragma once
@@ -24,8 +24,6 @@ typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(4))) int i32x4;
 typedef __attribute__((ext_vector_type(8))) int i32x8;
 
-constexpr int kPiece = 128;    // bytes of the contraction one step holds of an "along" row
-constexpr int kStepRows = 64;  // contracted rows one step holds of an "across" operand
 
 // Loads go through buffer descriptors: 32-bit offsets from a base that all lanes share, and what lies
 // outside the descriptor's extent is read as zeros.
@@ -178,64 +176,88 @@ struct One {
 };
 
 // BA x BB results from WA x WB waves; ANC / BNC: the operand lies across (else along); F8: E4M3 operands
-// with scales (both along); ST: stages of the LDS ring.
-template <int BA_, int BB_, int WA_, int WB_, bool ANC_, bool BNC_, bool F8_, int ST_>
+// with scales (both along); ST: stages of the LDS ring; PIECE: see above.
+template <int BA_, int BB_, int WA_, int WB_, bool ANC_, bool BNC_, bool F8_, int ST_, int PIECE_>
 struct Core {
-  static constexpr int BA = BA_, BB = BB_, WA = WA_, WB = WB_, ST = ST_;
+  static constexpr int BA = BA_, BB = BB_, WA = WA_, WB = WB_, ST = ST_, PIECE = PIECE_;
   static constexpr bool ANC = ANC_, BNC = BNC_, F8 = F8_;
   static constexpr int NW = WA * WB, NT = NW * 64;
   static constexpr int TA = BA / WA, TB = BB / WB;   // a wave's part
   static constexpr int FA = TA / 16, FB = TB / 16;   // in 16 x 16 fragments
-  static constexpr int JA = BA / 8 / NW, JB = BB / 8 / NW;   // 1 KiB loads a wave issues per step
+  static constexpr int ROWS = 1024 / PIECE;          // rows of an "along" tile in a 1 KiB load
+  static constexpr int KROWS = PIECE / 2;            // contracted rows of a step of an "across" tile
+  static constexpr int JA = BA / ROWS / NW, JB = BB / ROWS / NW;   // loads a wave issues per step
   // Scales of a step: the rows' from entry 0, the weights' two at entries WS and WS + 64, each loaded by a
   // wave of its own.
   static constexpr int WS = (BB + 63) / 64 * 64;
   static constexpr int SCALES = F8 ? NT * 4 : 0;
-  static constexpr int STAGE = (BA + BB) * kPiece + SCALES;
-  static_assert(BA / 8 % NW == 0 && BB / 8 % NW == 0, "loads must divide over the waves");
+  static constexpr int STAGE = (BA + BB) * PIECE + SCALES;
+  static_assert(BA / ROWS % NW == 0 && BB / ROWS % NW == 0, "loads must divide over the waves");
   static_assert(TA % 16 == 0 && TB % 16 == 0, "whole fragments");
-  static_assert(!F8 || (!ANC && !BNC && WS + 128 <= NT), "FP8 operands lie along");
-  static_assert(ST >= 2 && ST <= 4 && (JA + JB + 1) * (ST - 2) < 64, "the wait counts at most 63 loads");
+  static_assert(PIECE == 64 || PIECE == 128, "32 or 64 contracted bf16 values");
+  static_assert(!F8 || (!ANC && !BNC && PIECE == 128 && WS + 128 <= NT), "FP8 operands lie along");
+  static_assert(ST >= 2 && ST <= 5 && (JA + JB + 1) * (ST - 1) < 64, "the wait counts at most 63 loads");
 
   typedef f32x4 Acc[FA][FB];
 
-  // The 16-byte piece of an "along" tile that this lane loads in a 1 KiB load of 8 rows: row l/8, piece
-  // (l%8) ^ (l/8).  Rows of 128 bytes put equal pieces of all rows on the same banks; the exclusive or
-  // spreads the eight rows a read takes at once over all of them.
-  static __device__ __forceinline__ int along_row() { return lane_id() >> 3; }
-  static __device__ __forceinline__ int along_piece() { return (lane_id() & 7) ^ (lane_id() >> 3); }
+  // Where a 16-byte piece of an "along" row lies: rows of 64 or 128 bytes put equal pieces of neighbouring
+  // rows on the same banks; the exclusive or spreads the eight rows a read takes at once over all of them.
+  static __device__ __forceinline__ int spread(int row) { return PIECE == 128 ? row & 7 : (row >> 1) & 3; }
+  // The row, and the piece of it, that this lane loads in a 1 KiB load.
+  static __device__ __forceinline__ int along_row() { return lane_id() / (PIECE / 16); }
+  static __device__ __forceinline__ int along_piece() { return (lane_id() % (PIECE / 16)) ^ spread(along_row()); }
   // The same for an "across" tile of B columns: contracted row and first column of load g.  32-byte chunks
   // change places by mix(k): the 16 lanes of a transposing read touch four rows k..k+3, its neighbours the
   // rows 8 further on, all at the same chunk.
   static __device__ __forceinline__ int mix(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
   template <int B>
-  static __device__ __forceinline__ int across_row(int g) { return (g * 1024 + lane_id() * 16) / (B * 2); }
+  static __device__ __forceinline__ int across_row(int g) { return (g * 1024u + lane_id() * 16u) / (B * 2u); }
   template <int B>
   static __device__ __forceinline__ int across_col(int g) {
-    const int at = (g * 1024 + lane_id() * 16) % (B * 2);
+    const int at = (g * 1024u + lane_id() * 16u) % (B * 2u);
     return ((at >> 5) ^ (mix(across_row<B>(g)) & (B / 16 - 1))) * 16 + ((at >> 4) & 1) * 8;
   }
 
   // 1 KiB loads of the second operand that NJ fragments of each wave column need, and all loads of a step.
-  static constexpr int loads_b(int nj) { return BNC ? JB : (2 * nj + WA - 1) / WA < JB ? (2 * nj + WA - 1) / WA : JB; }
+  static constexpr int loads_b(int nj) {
+    const int need = (16 * WB * nj + ROWS * NW - 1) / (ROWS * NW);
+    return BNC || need > JB ? JB : need;
+  }
   static constexpr int loads(int nj) { return JA + loads_b(nj) + (F8 ? 1 : 0); }
 
+  // Load `at` of a step (scales first).  The loads of a step are spread over the products: a burst of them
+  // fills the address unit's queue, and a wave that waits there issues no product either.
   template <int NJ, class Src>
-  static __device__ __forceinline__ void issue(Src& src, int step, uint8_t* buf) {
+  static __device__ __forceinline__ void issue_one(const Src& src, int at, uint8_t* buf) {
     const int w = wave_id();
-    src.step(step);   // every step once, in order
-    if constexpr (F8) load_lds4(src.scale_rsrc(), src.scale(), buf + (BA + BB) * kPiece + w * 256);
+    if (F8 && at == 0) {
+      if constexpr (F8) load_lds4(src.scale_rsrc(), src.scale(), buf + (BA + BB) * PIECE + w * 256);
+      return;
+    }
+    const int j = at - (F8 ? 1 : 0);
+    if (j < JA) load_lds16(src.a_rsrc(j), src.a(j), buf + (j * NW + w) * 1024);
+    else if (j < JA + loads_b(NJ)) load_lds16(src.b_rsrc(), src.b(j - JA), buf + BA * PIECE + ((j - JA) * NW + w) * 1024);
+  }
+  template <int NJ, class Src>
+  static __device__ __forceinline__ void issue(Src& src, uint8_t* buf) {
+    src.step();
 #pragma unroll
-    for (int j = 0; j < JA; ++j) load_lds16(src.a_rsrc(j), src.a(j), buf + (j * NW + w) * 1024);
+    for (int i = 0; i < loads(NJ); ++i) issue_one<NJ>(src, i, buf);
+  }
+  // The part of a step's loads that goes with fragment i of the first operand.
+  template <int NJ, class Src>
+  static __device__ __forceinline__ void issue_part(const Src& src, int i, uint8_t* buf) {
+    constexpr int per = (loads(NJ) + FA - 1) / FA;
 #pragma unroll
-    for (int j = 0; j < loads_b(NJ); ++j) load_lds16(src.b_rsrc(), src.b(j), buf + BA * kPiece + (j * NW + w) * 1024);
+    for (int k = 0; k < per; ++k)
+      if (i * per + k < loads(NJ)) issue_one<NJ>(src, i * per + k, buf);
   }
 
-  // 16 rows or columns from `from` of the step's half s, 8 contracted values a lane: lane group
+  // 16 rows or columns from `from` of the step's part s, 8 contracted values a lane: lane group
   // q = l/16 holds k = 32 s + 8 q .. + 7 of row l%16.
   static __device__ __forceinline__ i32x4 along_frag(const uint8_t* t, int from, int s) {
     const int l = lane_id(), r = from + (l & 15);
-    return *reinterpret_cast<const i32x4*>(t + r * kPiece + (((s * 4 + (l >> 4)) ^ (l & 7)) << 4));
+    return *reinterpret_cast<const i32x4*>(t + r * PIECE + (((s * 4 + (l >> 4)) ^ spread(l & 15)) << 4));
   }
   template <int B>
   static __device__ __forceinline__ i32x4 across_frag(const uint8_t* t, int from, int s) {
@@ -267,10 +289,11 @@ struct Core {
   // with about 15 bits (2.4e-4 of the largest product at worst in 4096 sums, 1.7e-5 of the result's norm on
   // quantised normal values): far below the bf16 rounding of the output, 2^-9.
   template <int NJ, class Src>
-  static __device__ __forceinline__ void compute_fp8(const Src&, const uint8_t* buf, Acc& acc, int fa) {
+  static __device__ __forceinline__ void compute_fp8(const Src& src, const uint8_t* buf, uint8_t* before, Acc& acc,
+                                                     int fa) {
     const uint8_t* ta = buf;
-    const uint8_t* tb = buf + BA * kPiece;
-    const float* sc = reinterpret_cast<const float*>(buf + (BA + BB) * kPiece);
+    const uint8_t* tb = buf + BA * PIECE;
+    const float* sc = reinterpret_cast<const float*>(buf + (BA + BB) * PIECE);
     const float w0 = sc[WS], w1 = sc[WS + 64];
     i32x8 b[NJ];
     float x[NJ], c[NJ];
@@ -289,6 +312,7 @@ struct Core {
         for (int j = 0; j < NJ; ++j) c[j] = x[j] * w;
       }
       const i32x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      issue_part<NJ>(src, i, before);
       if (i + 1 < FA) {
         lo = along_frag(ta, Src::frag_a_at(fa, i + 1), 0);
         hi = along_frag(ta, Src::frag_a_at(fa, i + 1), 1);
@@ -308,73 +332,64 @@ struct Core {
     }
   }
 
+  // A step of bf16 that reads all its fragments and then multiplies.
   template <int NJ, class Src>
-  static __device__ __forceinline__ void compute(const Src& src, const uint8_t* buf, Acc& acc, int fa) {
-    if constexpr (F8) {
-      compute_fp8<NJ>(src, buf, acc, fa);
-    } else {
+  static __device__ __forceinline__ void compute(const Src&, const uint8_t* buf, Acc& acc, int fa) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        i32x4 a[FA], b[NJ];
+    for (int s = 0; s < PIECE / 64; ++s) {
+      i32x4 a[FA], b[NJ];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) b[j] = frag_b(buf + BA * kPiece, from_b(j), s);
+      for (int j = 0; j < NJ; ++j) b[j] = frag_b(buf + BA * PIECE, from_b(j), s);
 #pragma unroll
-        for (int i = 0; i < FA; ++i) a[i] = frag_a(buf, Src::frag_a_at(fa, i), s);
+      for (int i = 0; i < FA; ++i) a[i] = frag_a(buf, Src::frag_a_at(fa, i), s);
 #pragma unroll
-        for (int i = 0; i < FA; ++i)
+      for (int i = 0; i < FA; ++i)
 #pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[i]),
-                                                                __builtin_bit_cast(bf16x8, b[j]), acc[i][j], 0, 0, 0);
-      }
+        for (int j = 0; j < NJ; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[i]),
+                                                              __builtin_bit_cast(bf16x8, b[j]), acc[i][j], 0, 0, 0);
     }
   }
 
   // Ring of ST stages, each an array of its own so that the compiler sees that the loads into one do not
-  // touch the others.  At step t: wait for stage t (the loads of LEFT later steps stay in flight), meet,
+  // touch the others.  At step t: wait for stage t (the loads of ST-2 later steps stay in flight), meet,
   // start the loads of step t+ST-1 into the stage that step t-1 read (every wave has read it: its LDS reads
   // ended before the barrier), multiply.
-  template <int NJ, int LEFT, bool MORE, class Src>
-  static __device__ __forceinline__ void ring_step(Src& src, int t, uint8_t* cur, uint8_t* next, Acc& acc, int fa) {
-    wait_and_meet<loads(NJ) * LEFT>();
-    if constexpr (MORE) issue<NJ>(src, t + ST - 1, next);
-    compute<NJ>(src, cur, acc, fa);
-  }
-  // Steps t .. t+ST-1; LAST: only the first of them has loads left to start.
-  template <int NJ, bool LAST, class Src>
-  static __device__ __forceinline__ void ring_round(Src& src, int t, Acc& acc, int fa, uint8_t* s0, uint8_t* s1,
-                                                    uint8_t* s2, uint8_t* s3) {
-    uint8_t* const last = ST == 2 ? s1 : ST == 3 ? s2 : s3;
-    ring_step<NJ, ST - 2, true>(src, t, s0, last, acc, fa);
-    ring_step<NJ, LAST && ST == 2 ? 0 : ST - 2, !LAST>(src, t + 1, s1, s0, acc, fa);
-    if constexpr (ST > 2) ring_step<NJ, LAST ? ST - 3 : ST - 2, !LAST>(src, t + 2, s2, s1, acc, fa);
-    if constexpr (ST > 3) ring_step<NJ, LAST ? ST - 4 : ST - 2, !LAST>(src, t + 3, s3, s2, acc, fa);
+  template <int NJ, class Src>
+  static __device__ __forceinline__ void ring_step(Src& src, uint8_t* cur, uint8_t* before, Acc& acc, int fa) {
+    wait_and_meet<loads(NJ) * (ST - 2)>();
+    if constexpr (F8) {
+      src.step();
+      compute_fp8<NJ>(src, cur, before, acc, fa);
+    } else {
+      issue<NJ>(src, before);
+      compute<NJ>(src, cur, acc, fa);
+    }
   }
 
-  // Two stages in bf16: a software pipeline over the first operand's fragments.  While the NJ products of
-  // fragment i run, fragment i+2 is read; with the last two run those of the next half step's first two and
-  // its second operand.  When a stage's last fragment is in registers, the stage takes the loads of two
-  // steps on; the next stage was started a whole step earlier.
-  template <int NJ, int HALF, bool MORE, bool NEXT, class Src>
-  static __device__ __forceinline__ void piped_half(Src& src, int t, uint8_t* cur, uint8_t* next, Acc& acc, int fa,
-                                                    i32x4 (&b)[NJ], i32x4 (&a)[2]) {
+  // The same as a software pipeline over the first operand's fragments (bf16, steps of 32 values).  While the
+  // NJ products of fragment i run, fragment i+2 is read and a load of step t+ST-1 is started; with the last
+  // two fragments' products run the reads of the next step's first two and its second operand.  When a
+  // stage's last fragment is in registers all waves meet: the stage is free, and the next one complete.
+  template <int NJ, class Src>
+  static __device__ __forceinline__ void piped_step(Src& src, uint8_t* before, uint8_t* cur, uint8_t* next, Acc& acc,
+                                                    int fa, i32x4 (&b)[NJ], i32x4 (&a)[2]) {
     i32x4 c[NJ];
+    src.step();
 #pragma unroll
     for (int i = 0; i < FA; ++i) {
-      i32x4 ahead = {};
+      i32x4 ahead;
       if (i + 2 < FA) {
-        ahead = frag_a(cur, Src::frag_a_at(fa, i + 2), HALF);
-      } else if (HALF == 0 || NEXT) {
-        const uint8_t* from = HALF == 0 ? cur : next;
+        ahead = frag_a(cur, Src::frag_a_at(fa, i + 2), 0);
+        static_assert(loads(NJ) <= FA - 2, "all loads of a step before its barrier");
+        issue_part<NJ>(src, i, before);
+      } else {
         if (i == FA - 2) {
-          if constexpr (HALF == 1) {
-            wait_and_meet<0>();
-            if constexpr (MORE) issue<NJ>(src, t + 2, cur);
-          }
+          wait_and_meet<loads(NJ) * (ST - 2)>();
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) c[j] = frag_b(from + BA * kPiece, from_b(j), 1 - HALF);
+          for (int j = 0; j < NJ; ++j) c[j] = frag_b(next + BA * PIECE, from_b(j), 0);
         }
-        ahead = frag_a(from, Src::frag_a_at(fa, i + 2 - FA), 1 - HALF);
+        ahead = frag_a(next, Src::frag_a_at(fa, i + 2 - FA), 0);
       }
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
@@ -386,41 +401,53 @@ struct Core {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) b[j] = c[j];
   }
-  template <int NJ, bool MORE, bool NEXT, class Src>
-  static __device__ __forceinline__ void piped_step(Src& src, int t, uint8_t* cur, uint8_t* next, Acc& acc, int fa,
-                                                    i32x4 (&b)[NJ], i32x4 (&a)[2]) {
-    piped_half<NJ, 0, false, true>(src, t, cur, next, acc, fa, b, a);
-    piped_half<NJ, 1, MORE, NEXT>(src, t, cur, next, acc, fa, b, a);
-  }
 
-  // The steps are rounded up to whole rounds (sources give zeros past the end), and the loops hold no
-  // condition: with one, the compiler waits for all LDS reads where blocks join.
+  // The main loops hold no condition: with one, the compiler waits for all LDS reads where blocks join.  So
+  // loads are started past the last step too, which sources answer with zeros, and waited for at the end.
   template <int NJ, class Src>
   static __device__ __forceinline__ void run_part(Src& src, int steps, Acc& acc, uint8_t* s0, uint8_t* s1, uint8_t* s2,
-                                                  uint8_t* s3) {
+                                                  uint8_t* s3, uint8_t* s4) {
     const int fa = (wave_id() % WA) * Src::wave_span_a();
-    issue<NJ>(src, 0, s0);
+    constexpr bool PIPED = PIECE == 64;
+    uint8_t* const last = ST == 2 ? s1 : ST == 3 ? s2 : ST == 4 ? s3 : s4;
     int t = 0;
-    if constexpr (ST == 2 && !F8) {
+    issue<NJ>(src, s0);
+    if constexpr (ST > 2) issue<NJ>(src, s1);
+    if constexpr (ST > 3) issue<NJ>(src, s2);
+    if constexpr (ST > 4) issue<NJ>(src, s3);
+    if constexpr (PIPED) {
       i32x4 b[NJ], a[2];
-      issue<NJ>(src, 1, s1);
-      wait_and_meet<loads(NJ)>();
+      wait_and_meet<loads(NJ) * (ST - 2)>();
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) b[j] = frag_b(s0 + BA * kPiece, from_b(j), 0);
+      for (int j = 0; j < NJ; ++j) b[j] = frag_b(s0 + BA * PIECE, from_b(j), 0);
       a[0] = frag_a(s0, Src::frag_a_at(fa, 0), 0);
       a[1] = frag_a(s0, Src::frag_a_at(fa, 1), 0);
-      for (; t + 2 < steps; t += 2) {
-        piped_step<NJ, true, true>(src, t, s0, s1, acc, fa, b, a);
-        piped_step<NJ, true, true>(src, t + 1, s1, s0, acc, fa, b, a);
+      for (; t + ST <= steps; t += ST) {
+        piped_step<NJ>(src, last, s0, s1, acc, fa, b, a);
+        piped_step<NJ>(src, s0, s1, ST == 2 ? s0 : s2, acc, fa, b, a);
+        if constexpr (ST > 2) piped_step<NJ>(src, s1, s2, ST == 3 ? s0 : s3, acc, fa, b, a);
+        if constexpr (ST > 3) piped_step<NJ>(src, s2, s3, ST == 4 ? s0 : s4, acc, fa, b, a);
+        if constexpr (ST > 4) piped_step<NJ>(src, s3, s4, s0, acc, fa, b, a);
       }
-      piped_step<NJ, false, true>(src, t, s0, s1, acc, fa, b, a);
-      piped_step<NJ, false, false>(src, t + 1, s1, s0, acc, fa, b, a);
+      if (t < steps) piped_step<NJ>(src, last, s0, s1, acc, fa, b, a);
+      if (ST > 2 && t + 1 < steps) piped_step<NJ>(src, s0, s1, s2, acc, fa, b, a);
+      if (ST > 3 && t + 2 < steps) piped_step<NJ>(src, s1, s2, s3, acc, fa, b, a);
+      if (ST > 4 && t + 3 < steps) piped_step<NJ>(src, s2, s3, s4, acc, fa, b, a);
     } else {
-      if constexpr (ST > 2) issue<NJ>(src, 1, s1);
-      if constexpr (ST > 3) issue<NJ>(src, 2, s2);
-      for (; t + ST < steps; t += ST) ring_round<NJ, false>(src, t, acc, fa, s0, s1, s2, s3);
-      ring_round<NJ, true>(src, t, acc, fa, s0, s1, s2, s3);
+      for (; t + ST <= steps; t += ST) {
+        ring_step<NJ>(src, s0, last, acc, fa);
+        ring_step<NJ>(src, s1, s0, acc, fa);
+        if constexpr (ST > 2) ring_step<NJ>(src, s2, s1, acc, fa);
+        if constexpr (ST > 3) ring_step<NJ>(src, s3, s2, acc, fa);
+        if constexpr (ST > 4) ring_step<NJ>(src, s4, s3, acc, fa);
+      }
+      if (t < steps) ring_step<NJ>(src, s0, last, acc, fa);
+      if (ST > 2 && t + 1 < steps) ring_step<NJ>(src, s1, s0, acc, fa);
+      if (ST > 3 && t + 2 < steps) ring_step<NJ>(src, s2, s1, acc, fa);
+      if (ST > 4 && t + 3 < steps) ring_step<NJ>(src, s3, s2, acc, fa);
     }
+    // no load into LDS may outlive the workgroup, and the next part starts with all stages free
+    wait_and_meet<0>();
   }
 
   // Sums over the parts of `plan` (plan.parts() sources of `steps` steps each, plan.source(p)).  `rows`:
@@ -431,12 +458,12 @@ struct Core {
     __shared__ __attribute__((aligned(1024))) uint8_t s1[STAGE];
     __shared__ __attribute__((aligned(1024))) uint8_t s2[ST > 2 ? STAGE : 16];
     __shared__ __attribute__((aligned(1024))) uint8_t s3[ST > 3 ? STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t s4[ST > 4 ? STAGE : 16];
     if (steps <= 0) return;
     auto all = [&](auto nj) {
       for (int p = 0; p < plan.parts(); ++p) {
-        if (p > 0) wait_and_meet<0>();   // the part before has read its last stage
         auto src = plan.source(p);
-        run_part<decltype(nj)::value>(src, steps, acc, s0, s1, s2, s3);
+        run_part<decltype(nj)::value>(src, steps, acc, s0, s1, s2, s3, s4);
       }
     };
     constexpr int Q = FB >= 4 ? FB / 4 : 1;   // the loop exists for one to four quarters of the fragments
