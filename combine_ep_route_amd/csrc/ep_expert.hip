@@ -98,44 +98,75 @@ __global__ __launch_bounds__(C::NT) void along_kernel(AlongArgs a) {
   AlongSrc<C, GATED> src(a, s, n0, m0);
   C::run(One<AlongSrc<C, GATED>>{src}, static_cast<int>((a.k_bytes + C::PIECE - 1) / C::PIECE), s.count - m0, acc);
 
-  const int l = lane_id(), w = wave_id();
-  const int fa = (w % C::WA) * src.wave_span_a();
+  constexpr int CF = GATED ? C::FA / 2 : C::FA;
+  const int l = lane_id(), first = n0 + (wave_id() % C::WA) * src.wave_span_a();   // the wave's first column
+  const int bytes = (a.N - first) * 2;
+  auto row = [&](int r) {
+    const int p = m0 + C::wave_row(r);
+    return p < s.count ? static_cast<int64_t>(row_of(a.rows, s, p)) : -1;
+  };
+  if constexpr (KIND == kGatedGrad) {
+    uint2 d[CF][C::FB];
+    auto grad_row = [&](int r) {
+      const int64_t at = row(r);
+      return at < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.grad + at * a.ld_grad + first);
+    };
+    if constexpr (C::kThroughLds) {
+      C::template load_rows<CF>(d, bytes, grad_row);
+    } else {
 #pragma unroll
-  for (int j = 0; j < C::FB; ++j) {
-    const int p = m0 + C::from_b(j) + (l & 15);
-    if (p >= s.count) continue;
-    const int64_t r = row_of(a.rows, s, p);
+      for (int j = 0; j < C::FB; ++j) {
+        const uint8_t* from = grad_row(j * 16 + (l & 15));
 #pragma unroll
-    for (int i = 0; i < (GATED ? C::FA / 2 : C::FA); ++i) {
-      const int n = n0 + fa + i * 16 + (l >> 4) * 4;
-      if (n >= a.N) continue;
-      if constexpr (KIND == kLinear) {
-        *reinterpret_cast<uint2*>(a.out[0] + r * a.ld_out[0] + n) = bf16x4(acc[i][j]);
-      } else {
-        const f32x4 g = acc[i][j], u = acc[i + C::FA / 2][j];
-        f32x4 f, df;
+        for (int i = 0; i < CF; ++i) {
+          const int byte = (i * 16 + (l >> 4) * 4) * 2;
+          d[i][j] = from && byte < bytes ? *reinterpret_cast<const uint2*>(from + byte) : uint2{0, 0};
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < CF; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FB; ++j) {
+        const uint2 b = d[i][j];
+        const f32x4 dh = {from_bf16(b.x & 0xffff), from_bf16(b.x >> 16), from_bf16(b.y & 0xffff), from_bf16(b.y >> 16)};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          float v, d;
-          activate<ACT>(g[k], &v, &d);
-          f[k] = v;
-          df[k] = d;
+          float f, df;
+          activate<ACT>(acc[i][j][k], &f, &df);
+          acc[i][j][k] = df * dh[k] * acc[i + CF][j][k];
+          acc[i + CF][j][k] = f * dh[k];
         }
-        if constexpr (KIND == kGated) {
+      }
+  } else if constexpr (KIND == kGated) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) f[k] *= u[k];
-          *reinterpret_cast<uint2*>(a.out[0] + r * a.ld_out[0] + n) = bf16x4(f);
-        } else {
-          // The gradients of the two products are kept in bf16: they are operands of the matrix unit next.
-          const uint2 d = *reinterpret_cast<const uint2*>(a.grad + r * a.ld_grad + n);
-          const f32x4 dh = {from_bf16(d.x & 0xffff), from_bf16(d.x >> 16), from_bf16(d.y & 0xffff), from_bf16(d.y >> 16)};
+    for (int i = 0; i < CF; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            df[k] *= dh[k] * u[k];
-            f[k] *= dh[k];
-          }
-          *reinterpret_cast<uint2*>(a.out[0] + r * a.ld_out[0] + n) = bf16x4(df);
-          *reinterpret_cast<uint2*>(a.out[1] + r * a.ld_out[1] + n) = bf16x4(f);
+      for (int j = 0; j < C::FB; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float f, df;
+          activate<ACT>(acc[i][j][k], &f, &df);
+          acc[i][j][k] = f * acc[i + CF][j][k];
+        }
+  }
+  // The gradients of the two products are kept in bf16: they are operands of the matrix unit next.
+#pragma unroll
+  for (int o = 0; o < (KIND == kGatedGrad ? 2 : 1); ++o) {
+    auto out_row = [&](int r) {
+      const int64_t at = row(r);
+      return at < 0 ? nullptr : reinterpret_cast<uint8_t*>(a.out[o] + at * a.ld_out[o] + first);
+    };
+    if constexpr (C::kThroughLds) {
+      C::template store_rows<CF, 2>(acc, o * CF, bytes, out_row);
+    } else {
+#pragma unroll
+      for (int j = 0; j < C::FB; ++j) {
+        uint8_t* to = out_row(j * 16 + (l & 15));
+#pragma unroll
+        for (int i = 0; i < CF; ++i) {
+          const int byte = (i * 16 + (l >> 4) * 4) * 2;
+          if (to && byte < bytes) *reinterpret_cast<uint2*>(to + byte) = bf16x4(acc[o * CF + i][j]);
         }
       }
     }
@@ -207,18 +238,12 @@ __global__ __launch_bounds__(C::NT) void row_grad_kernel(RowGradArgs g) {
   typename C::Acc acc = {};
   C::run(RowGradPlan<C>{g, s, n0, m0}, (g.I + C::KROWS - 1) / C::KROWS, s.count - m0, acc);
 
-  const int l = lane_id(), w = wave_id();
-#pragma unroll
-  for (int j = 0; j < C::FB; ++j) {
-    const int p = m0 + C::from_b(j) + (l & 15);
-    if (p >= s.count) continue;
-    const int64_t r = row_of(g.rows, s, p);
-#pragma unroll
-    for (int i = 0; i < C::FA; ++i) {
-      const int n = n0 + (w % C::WA) * C::TA + i * 16 + (l >> 4) * 4;
-      if (n < g.N) *reinterpret_cast<uint2*>(g.dx + r * g.ld_dx + n) = bf16x4(acc[i][j]);
-    }
-  }
+  const int first = n0 + (wave_id() % C::WA) * C::TA;
+  C::template store_rows<C::FA, 2>(acc, 0, (g.N - first) * 2, [&](int r) -> uint8_t* {
+    const int p = m0 + C::wave_row(r);
+    if (p >= s.count) return nullptr;
+    return reinterpret_cast<uint8_t*>(g.dx + row_of(g.rows, s, p) * g.ld_dx + first);
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -299,20 +324,12 @@ __global__ __launch_bounds__(C::NT) void weight_grad_kernel(WeightGradArgs g) {
   WeightGradSrc<C, LIST> src(g, s, which, h0, i0);
   C::run(One<WeightGradSrc<C, LIST>>{src}, (s.count + C::KROWS - 1) / C::KROWS, g.I - i0, acc);
 
-  const int l = lane_id(), w = wave_id();
-#pragma unroll
-  for (int j = 0; j < C::FB; ++j) {
-    const int i = i0 + C::from_b(j) + (l & 15);
-    if (i >= g.I) continue;
-#pragma unroll
-    for (int f = 0; f < C::FA; ++f) {
-      const int h = h0 + (w % C::WA) * C::TA + f * 16 + (l >> 4) * 4;
-      if (h >= g.H) continue;
-      uint8_t* p = g.dw[which] + e * g.dw_expert[which] + i * g.ld_dw[which];
-      if constexpr (F32) *reinterpret_cast<f32x4*>(p + h * 4) = acc[f][j];
-      else *reinterpret_cast<uint2*>(p + h * 2) = bf16x4(acc[f][j]);
-    }
-  }
+  constexpr int ES = F32 ? 4 : 2;
+  const int first = h0 + (wave_id() % C::WA) * C::TA;
+  C::template store_rows<C::FA, ES>(acc, 0, (g.H - first) * ES, [&](int r) -> uint8_t* {
+    const int i = i0 + C::wave_row(r);
+    return i < g.I ? g.dw[which] + e * g.dw_expert[which] + i * g.ld_dw[which] + first * ES : nullptr;
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -370,7 +387,7 @@ template <bool F8, int KIND, int ACT>
 hipError_t launch_along_kind(const AlongArgs& a, hipStream_t stream, bool check) {
   if (a.rows_max <= static_cast<int64_t>(a.rows.E) * 32)
     return launch_along_as<Core<128, 32, 4, 1, false, false, F8, 4, 128>, KIND, ACT>(a, stream, check);
-  return launch_along_as<Core<256, 256, 2, 4, false, false, F8, F8 ? 2 : 5, F8 ? 128 : 64>, KIND, ACT>(a, stream, check);
+  return launch_along_as<Core<256, 256, 2, 4, false, false, F8, 2, 128>, KIND, ACT>(a, stream, check);
 }
 
 template <bool F8>
@@ -402,7 +419,7 @@ hipError_t launch_gated_grad(const AlongArgs& a, int act, hipStream_t stream, bo
 }
 
 hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check) {
-  using C = Core<256, 256, 2, 4, true, false, false, 5, 64>;
+  using C = Core<256, 256, 2, 4, true, false, false, 2, 128>;
   const int64_t tiles = row_tiles<C::BB>(g.rows, g.rows_max, g.per_expert_max) * ((g.N + C::BA - 1) / C::BA);
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
   if (tiles == 0 || check) return hipSuccess;
@@ -411,7 +428,7 @@ hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check)
 }
 
 hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check) {
-  using C = Core<256, 256, 2, 4, true, true, false, 5, 64>;
+  using C = Core<256, 256, 2, 4, true, true, false, 2, 128>;
   const int64_t tiles = static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + C::BA - 1) / C::BA) *
                         ((g.I + C::BB - 1) / C::BB);
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;

@@ -162,6 +162,14 @@ __device__ __forceinline__ int row_of(const ExpertRows& r, const Span& s, int p)
 // The product of one tile
 // ---------------------------------------------------------------------------
 
+__device__ __forceinline__ uint32_t bf16_bits(float v) {
+  return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(v)));
+}
+__device__ __forceinline__ uint2 bf16x4(f32x4 v) {
+  return {bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16};
+}
+__device__ __forceinline__ float from_bf16(uint32_t b) { return __builtin_bit_cast(float, b << 16); }
+
 template <int N>
 struct Int {
   static constexpr int value = N;
@@ -199,6 +207,27 @@ struct Core {
   static_assert(ST >= 2 && ST <= 5 && (JA + JB + 1) * (ST - 1) < 64, "the wait counts at most 63 loads");
 
   typedef f32x4 Acc[FA][FB];
+
+  static __device__ __forceinline__ uint8_t* stage0() {
+    __shared__ __attribute__((aligned(1024))) uint8_t s[STAGE];
+    return s;
+  }
+  static __device__ __forceinline__ uint8_t* stage1() {
+    __shared__ __attribute__((aligned(1024))) uint8_t s[STAGE];
+    return s;
+  }
+  static __device__ __forceinline__ uint8_t* stage2() {
+    __shared__ __attribute__((aligned(1024))) uint8_t s[ST > 2 ? STAGE : 16];
+    return s;
+  }
+  static __device__ __forceinline__ uint8_t* stage3() {
+    __shared__ __attribute__((aligned(1024))) uint8_t s[ST > 3 ? STAGE : 16];
+    return s;
+  }
+  static __device__ __forceinline__ uint8_t* stage4() {
+    __shared__ __attribute__((aligned(1024))) uint8_t s[ST > 4 ? STAGE : 16];
+    return s;
+  }
 
   // Where a 16-byte piece of an "along" row lies: rows of 64 or 128 bytes put equal pieces of neighbouring
   // rows on the same banks; the exclusive or spreads the eight rows a read takes at once over all of them.
@@ -367,39 +396,48 @@ struct Core {
     }
   }
 
-  // The same as a software pipeline over the first operand's fragments (bf16, steps of 32 values).  While the
-  // NJ products of fragment i run, fragment i+2 is read and a load of step t+ST-1 is started; with the last
-  // two fragments' products run the reads of the next step's first two and its second operand.  When a
-  // stage's last fragment is in registers all waves meet: the stage is free, and the next one complete.
+  // The same as a software pipeline over the first operand's fragments (bf16).  While the NJ products of a
+  // fragment run, the one after the next is read; with the last two run the reads of the next step's first
+  // two and its second operand.  When a stage's last fragment is in registers all waves meet: the next stage
+  // is complete, and this one takes the loads of step t+ST, kEarly of them at once and the others with the
+  // next step's first fragments.
+  static constexpr int kEarly = 4;
   template <int NJ, class Src>
   static __device__ __forceinline__ void piped_step(Src& src, uint8_t* before, uint8_t* cur, uint8_t* next, Acc& acc,
                                                     int fa, i32x4 (&b)[NJ], i32x4 (&a)[2]) {
+    constexpr int H = PIECE / 64, N = H * FA;
     i32x4 c[NJ];
-    src.step();
 #pragma unroll
-    for (int i = 0; i < FA; ++i) {
-      i32x4 ahead;
-      if (i + 2 < FA) {
-        ahead = frag_a(cur, Src::frag_a_at(fa, i + 2), 0);
-        static_assert(loads(NJ) <= FA - 2, "all loads of a step before its barrier");
-        issue_part<NJ>(src, i, before);
-      } else {
-        if (i == FA - 2) {
-          wait_and_meet<loads(NJ) * (ST - 2)>();
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) c[j] = frag_b(next + BA * PIECE, from_b(j), 0);
-        }
-        ahead = frag_a(next, Src::frag_a_at(fa, i + 2 - FA), 0);
+    for (int n = 0; n < N; ++n) {
+      const int i = n % FA, s = n / FA, m = n + 2;
+      if (kEarly + 2 * n < loads(NJ)) issue_one<NJ>(src, kEarly + 2 * n, before);
+      if (kEarly + 2 * n + 1 < loads(NJ)) issue_one<NJ>(src, kEarly + 2 * n + 1, before);
+      if (n == N - 2) {
+        wait_and_meet<loads(NJ) * (ST - 2)>();
+        src.step();
       }
+      if (n >= N - 2) {
+        const int from = (n - (N - 2)) * 2;
+        if (from < loads(NJ) && from < kEarly) issue_one<NJ>(src, from, cur);
+        if (from + 1 < loads(NJ) && from + 1 < kEarly) issue_one<NJ>(src, from + 1, cur);
+      }
+      if (i == FA - 2) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) c[j] = frag_b((s + 1 < H ? cur : next) + BA * PIECE, from_b(j), s + 1 < H ? s + 1 : 0);
+      }
+      const i32x4 ahead = m < N ? frag_a(cur, Src::frag_a_at(fa, m % FA), m / FA)
+                                : frag_a(next, Src::frag_a_at(fa, m - N), 0);
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[i & 1]),
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[n & 1]),
                                                             __builtin_bit_cast(bf16x8, b[j]), acc[i][j], 0, 0, 0);
-      a[i & 1] = ahead;
+      a[n & 1] = ahead;
+      if (i == FA - 1) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) b[j] = c[j];
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) b[j] = c[j];
   }
 
   // The main loops hold no condition: with one, the compiler waits for all LDS reads where blocks join.  So
@@ -408,7 +446,7 @@ struct Core {
   static __device__ __forceinline__ void run_part(Src& src, int steps, Acc& acc, uint8_t* s0, uint8_t* s1, uint8_t* s2,
                                                   uint8_t* s3, uint8_t* s4) {
     const int fa = (wave_id() % WA) * Src::wave_span_a();
-    constexpr bool PIPED = PIECE == 64;
+    constexpr bool PIPED = !F8 && FA >= 4;
     uint8_t* const last = ST == 2 ? s1 : ST == 3 ? s2 : ST == 4 ? s3 : s4;
     int t = 0;
     issue<NJ>(src, s0);
@@ -417,7 +455,10 @@ struct Core {
     if constexpr (ST > 4) issue<NJ>(src, s3);
     if constexpr (PIPED) {
       i32x4 b[NJ], a[2];
-      wait_and_meet<loads(NJ) * (ST - 2)>();
+      src.step();
+#pragma unroll
+      for (int i = 0; i < kEarly && i < loads(NJ); ++i) issue_one<NJ>(src, i, last);
+      wait_and_meet<loads(NJ) * (ST - 2) + (kEarly < loads(NJ) ? kEarly : loads(NJ))>();
 #pragma unroll
       for (int j = 0; j < NJ; ++j) b[j] = frag_b(s0 + BA * PIECE, from_b(j), 0);
       a[0] = frag_a(s0, Src::frag_a_at(fa, 0), 0);
@@ -454,11 +495,11 @@ struct Core {
   // rows of the second operand that count.
   template <class Plan>
   static __device__ __forceinline__ void run(const Plan& plan, int steps, int rows, Acc& acc) {
-    __shared__ __attribute__((aligned(1024))) uint8_t s0[STAGE];
-    __shared__ __attribute__((aligned(1024))) uint8_t s1[STAGE];
-    __shared__ __attribute__((aligned(1024))) uint8_t s2[ST > 2 ? STAGE : 16];
-    __shared__ __attribute__((aligned(1024))) uint8_t s3[ST > 3 ? STAGE : 16];
-    __shared__ __attribute__((aligned(1024))) uint8_t s4[ST > 4 ? STAGE : 16];
+    uint8_t* const s0 = stage0();
+    uint8_t* const s1 = stage1();
+    uint8_t* const s2 = stage2();
+    uint8_t* const s3 = stage3();
+    uint8_t* const s4 = stage4();
     if (steps <= 0) return;
     auto all = [&](auto nj) {
       for (int p = 0; p < plan.parts(); ++p) {
@@ -473,15 +514,93 @@ struct Core {
     else if (3 * Q < FB && quarters == 3) all(Int<(3 * Q < FB ? 3 * Q : FB)>{});
     else all(Int<FB>{});
   }
-};
 
-__device__ __forceinline__ uint32_t bf16_bits(float v) {
-  return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(v)));
-}
-__device__ __forceinline__ uint2 bf16x4(f32x4 v) {
-  return {bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16};
-}
-__device__ __forceinline__ float from_bf16(uint32_t b) { return __builtin_bit_cast(float, b << 16); }
+  // -------------------------------------------------------------------------
+  // A wave's part of the results between its registers and rows in memory
+  // -------------------------------------------------------------------------
+  // A lane holds four columns of 16 rows' fragments: stored as they lie, 32 bytes of a row at a time.  Through
+  // LDS (the stages are free behind run()) whole rows of the wave's CF*16 columns are moved, 16 bytes a lane.
+  // Each wave has kRegion bytes of its own; a row's 16-byte pieces are spread over the banks by the row.
+  static constexpr int kRegion = 2 * (STAGE - SCALES) / NW / 1024 * 1024;
+  static constexpr bool kThroughLds = kRegion >= 8192;
+  static __device__ __forceinline__ uint8_t* region() {
+    const int w = wave_id();
+    return (w < NW / 2 ? stage0() : stage1()) + w % (NW / 2) * kRegion;
+  }
+  template <int CF, int ES>
+  struct Tile {
+    static constexpr int ROW = CF * 16 * ES, PIECES = ROW / 16, MASK = (PIECES < 16 ? PIECES : 16) - 1;
+    static constexpr int ROUND = kRegion / ROW < TB ? kRegion / ROW : TB;   // rows that fit the region
+    static __device__ __forceinline__ int at(int row, int byte) {
+      return row * ROW + ((((byte >> 4) ^ row) & MASK) << 4 | (byte & ~(16 * MASK + 15)) | (byte & 15));
+    }
+    // 16 bytes a lane, whole rows at a time: f(row of the wave's part, byte in the row, place in the region)
+    template <class F>
+    static __device__ __forceinline__ void pieces(int round, F f) {
+#pragma unroll
+      for (int k = 0; k < ROUND * PIECES / 64; ++k) {
+        const int n = k * 64 + lane_id(), row = n / PIECES, byte = n % PIECES * 16;
+        f(round * ROUND + row, byte, region() + at(row, byte));
+      }
+    }
+  };
+  // Between the lanes' writes to the region and their reads of each other's: LDS takes a wave's accesses in
+  // order, so only the compiler has to keep them apart.
+  static __device__ __forceinline__ void turn() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+  }
+  // Row r of the wave's part is row wave_row(r) of the tile.
+  static __device__ __forceinline__ int wave_row(int r) { return from_b(0) + r / 16 * (16 * WB) + r % 16; }
+
+  // Stores acc[i0 .. i0+CF-1][..] as bf16 (ES 2) or fp32 (ES 4).  row(r): where the wave's first column of row
+  // wave_row(r) goes, or null; bytes: of the wave's columns that are stored, in multiples of 16.
+  template <int CF, int ES, class Row>
+  static __device__ __forceinline__ void store_rows(const Acc& acc, int i0, int bytes, Row row) {
+    using T = Tile<CF, ES>;
+    const int l = lane_id();
+#pragma unroll
+    for (int round = 0; round < TB / T::ROUND; ++round) {
+#pragma unroll
+      for (int j = 0; j < T::ROUND / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < CF; ++i) {
+          const f32x4 v = acc[i0 + i][round * (T::ROUND / 16) + j];
+          uint8_t* p = region() + T::at(j * 16 + (l & 15), (i * 16 + (l >> 4) * 4) * ES);
+          if constexpr (ES == 2) *reinterpret_cast<uint2*>(p) = bf16x4(v);
+          else *reinterpret_cast<f32x4*>(p) = v;
+        }
+      turn();
+      T::pieces(round, [&](int r, int byte, const uint8_t* from) {
+        const uint4 v = *reinterpret_cast<const uint4*>(from);
+        uint8_t* to = row(r);
+        if (to && byte < bytes) *reinterpret_cast<uint4*>(to + byte) = v;
+      });
+      turn();
+    }
+  }
+  // The other way: bf16 rows to the lanes' places, v[i][j] four columns as bits.
+  template <int CF, class Row>
+  static __device__ __forceinline__ void load_rows(uint2 (&v)[CF][FB], int bytes, Row row) {
+    using T = Tile<CF, 2>;
+    const int l = lane_id();
+#pragma unroll
+    for (int round = 0; round < TB / T::ROUND; ++round) {
+      T::pieces(round, [&](int r, int byte, uint8_t* to) {
+        const uint8_t* from = row(r);
+        *reinterpret_cast<uint4*>(to) = from && byte < bytes ? *reinterpret_cast<const uint4*>(from + byte) : uint4{0, 0, 0, 0};
+      });
+      turn();
+#pragma unroll
+      for (int j = 0; j < T::ROUND / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < CF; ++i)
+          v[i][round * (T::ROUND / 16) + j] =
+              *reinterpret_cast<const uint2*>(region() + T::at(j * 16 + (l & 15), (i * 16 + (l >> 4) * 4) * 2));
+      turn();
+    }
+  }
+};
 
 // The activation and its derivative.  silu(g) = g s(g) with s the logistic function; the tanh form of
 // gelu is g s(2z), z = sqrt(2/pi) (g + 0.044715 g^3), since (1 + tanh z)/2 = s(2z).
