@@ -227,7 +227,7 @@ struct RowGradPlan {
 };
 
 template <class C>
-__global__ __launch_bounds__(C::NT) void row_grad_kernel(RowGradArgs g) {
+__global__ __launch_bounds__(C::NT, 2) void row_grad_kernel(RowGradArgs g) {
   const int col_tiles = (g.N + C::BA - 1) / C::BA;
   const Span s = find_span<C::BB>(g.rows, blockIdx.x, col_tiles);
   if (s.e < 0) return;
@@ -310,7 +310,7 @@ struct WeightGradSrc {
 };
 
 template <class C, bool F32, bool LIST>
-__global__ __launch_bounds__(C::NT) void weight_grad_kernel(WeightGradArgs g) {
+__global__ __launch_bounds__(C::NT, 2) void weight_grad_kernel(WeightGradArgs g) {
   const int ht = (g.H + C::BA - 1) / C::BA, it = (g.I + C::BB - 1) / C::BB;
   const int per = ht * it * g.parts;
   const int tile = xcd_tile(blockIdx.x, per * g.rows.E);
@@ -419,7 +419,7 @@ hipError_t launch_gated_grad(const AlongArgs& a, int act, hipStream_t stream, bo
 }
 
 hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check) {
-  using C = Core<256, 256, 2, 4, true, false, false, 2, 128>;
+  using C = Core<256, 256, 2, 4, true, false, false, 4, 64>;
   const int64_t tiles = row_tiles<C::BB>(g.rows, g.rows_max, g.per_expert_max) * ((g.N + C::BA - 1) / C::BA);
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
   if (tiles == 0 || check) return hipSuccess;
@@ -428,7 +428,7 @@ hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check)
 }
 
 hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check) {
-  using C = Core<256, 256, 2, 4, true, true, false, 2, 128>;
+  using C = Core<256, 256, 2, 4, true, true, false, 4, 64>;
   const int64_t tiles = static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + C::BA - 1) / C::BA) *
                         ((g.I + C::BB - 1) / C::BB);
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;

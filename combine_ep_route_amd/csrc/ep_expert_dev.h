@@ -530,7 +530,8 @@ struct Core {
   template <int CF, int ES>
   struct Tile {
     static constexpr int ROW = CF * 16 * ES, PIECES = ROW / 16, MASK = (PIECES < 16 ? PIECES : 16) - 1;
-    static constexpr int ROUND = kRegion / ROW < TB ? kRegion / ROW : TB;   // rows that fit the region
+    static constexpr int fit(int rows) { return rows * ROW <= kRegion ? rows : fit(rows / 2); }
+    static constexpr int ROUND = fit(TB);   // rows that fit the region
     static __device__ __forceinline__ int at(int row, int byte) {
       return row * ROW + ((((byte >> 4) ^ row) & MASK) << 4 | (byte & ~(16 * MASK + 15)) | (byte & 15));
     }
