@@ -48,29 +48,27 @@ def desc(t: Optional[torch.Tensor], tag: int = A.EP_TAG_NONE):
     if not t.is_cuda and not (tag == A.EP_TAG_RECV_EXPERT_COUNTER_HOST and t.is_pinned()):
         raise ValueError(f"ep tensors must be on the GPU (or, for a host receive counter, pinned), "
                          f"got a {t.device} tensor")
-    if t.dim() < 1 or t.dim() > 3:
+    shape = t.shape
+    n = len(shape)
+    if n < 1 or n > 3:
         raise ValueError("ep tensors have 1 to 3 dimensions")
-    d = A.EpTensor()
-    d.data = t.data_ptr()
-    d.dtype = _DTYPES[t.dtype]
-    d.ndim = t.dim()
     # an empty tensor may report any strides (numpy's give 0s): describe it
     # as the contiguous tensor it trivially is
-    strides = t.stride() if t.numel() > 0 else torch.empty(t.shape, device="meta").stride()
-    for i in range(t.dim()):
-        d.sizes[i] = t.shape[i]
-        d.strides[i] = strides[i]
-    d.tag = tag
-    return d
+    strides = t.stride() if t.numel() > 0 else torch.empty(shape, device="meta").stride()
+    pad = _PAD[n]
+    return A.EpTensor(t.data_ptr(), _DTYPES[t.dtype], n, (*shape, *pad), (*strides, *pad), tag)
+
+
+_PAD = {1: (0, 0), 2: (0,), 3: ()}   # up to the three entries of a descriptor
 
 
 def _ref(d):
-    return None if d is None else ctypes.byref(d)
+    return d   # ctypes passes a structure where a pointer to it is declared
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the current stream's handle, without making a Stream object for it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
