@@ -380,7 +380,7 @@ hipError_t launch_list_rows(const int32_t* counts, int E, int S, int slots, int3
 
 namespace norm {
 
-constexpr int kGradBlocks = 512;   // workgroups of the backward pass, each with a share of the column sums
+constexpr int kNormCus = 256;   // CUs the backward pass plans for
 
 // Strides in elements.
 struct NormArgs {
@@ -431,9 +431,9 @@ struct NormGradArgs {
   float* dw_pre;
   float* dw_post;
   float* dgate_channel;
-  float* work;               // up to 3 x grad_blocks(n) x H
+  float* work;               // up to 2 x grad_blocks x H
 };
-int grad_blocks(int64_t n);
+int grad_blocks(int64_t n, int H);   // its workgroups, each with a share of the column sums
 hipError_t launch_residual_norm_backward(const NormGradArgs& a, hipStream_t stream);
 
 }  // namespace norm

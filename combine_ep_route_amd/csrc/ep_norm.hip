@@ -1,5 +1,7 @@
 // The norms around the block, fused with its gate and the residual stream: what stands between a
 // combine and the next router.  One pass over the rows; every sum in fp32.
+#include <algorithm>
+
 #include "ep_internal.h"
 
 namespace ep {
@@ -12,26 +14,50 @@ enum Gate { kNone, kChannel, kToken };
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
 
-// Sums of N values over the workgroup, in a fixed order; all threads get them.  `part` holds 16 N floats
-// and is free again once every thread has passed the second barrier of the next call.
-template <int N>
-__device__ __forceinline__ void sum_block(float (&v)[N], float* part) {
-  const int w = threadIdx.x >> 6, waves = blockDim.x >> 6;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v[i] += __shfl_xor(v[i], d);
-    if (lane_id() == 0) part[i * 16 + w] = v[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float s = 0.0f;
-    for (int q = 0; q < waves; ++q) s += part[i * 16 + q];
-    v[i] = s;
-  }
-  __syncthreads();
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
 }
+// The sum over a wave, in lane 63: pairs, quads, halves and whole rows of 16 lanes, then the rows.
+__device__ __forceinline__ float add_wave(float v) {
+  v = add_dpp<0xb1, 0xf>(v);    // lanes 1 0 3 2 of each quad
+  v = add_dpp<0x4e, 0xf>(v);    // lanes 2 3 0 1
+  v = add_dpp<0x141, 0xf>(v);   // half rows mirrored
+  v = add_dpp<0x140, 0xf>(v);   // rows mirrored
+  v = add_dpp<0x142, 0xa>(v);   // each row's last lane to the next row
+  return add_dpp<0x143, 0xc>(v);   // lane 31 to the upper rows
+}
+
+// Sums over the workgroup's waves, in a fixed order.  Consecutive calls take turns between two buffers: a wave
+// that writes one again has passed the barrier of the call between, before which all waves have read it.
+struct BlockSum {
+  float (*part)[3 * 16];
+  int turn = 0;
+
+  // once per workgroup: entries of waves that it does not have stay zeros
+  __device__ __forceinline__ BlockSum(float (*p)[3 * 16]) : part(p) {
+    for (int i = threadIdx.x; i < 2 * 3 * 16; i += blockDim.x) part[i / 48][i % 48] = 0.0f;
+    __syncthreads();
+  }
+  template <int N>
+  __device__ __forceinline__ void add(float (&v)[N]) {
+    float* p = part[turn];
+    turn ^= 1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = add_wave(v[i]);
+      if (lane_id() == 63) p[i * 16 + (threadIdx.x >> 6)] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float4* q = reinterpret_cast<const float4*>(p + i * 16);
+      const float4 a = q[0], b = q[1], c = q[2], d = q[3];
+      v[i] = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w)) + ((c.x + c.y) + (c.z + c.w)) +
+             ((d.x + d.y) + (d.z + d.w));
+    }
+  }
+};
 
 struct V8 {
   float v[8];
@@ -65,8 +91,9 @@ __device__ __forceinline__ void store8(float* p, const V8& a) {
 // One workgroup a row, CPT pieces of 8 columns a thread: a row is read once, both norms' sums are formed
 // from registers.
 template <int CPT, bool POST, int GATE>
-__global__ void residual_norm_kernel(NormArgs a) {
-  __shared__ float part[16];
+__global__ __launch_bounds__(kMaxThreads) void residual_norm_kernel(NormArgs a) {
+  __shared__ __attribute__((aligned(16))) float part[2][3 * 16];
+  BlockSum sum(part);
   const int64_t r = blockIdx.x;
   V8 y[CPT], x[CPT];
   float ss[1] = {0.0f};
@@ -83,7 +110,7 @@ __global__ void residual_norm_kernel(NormArgs a) {
     for (int p = 0; p < CPT; ++p)
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss[0] += y[p].v[i] * y[p].v[i];
-    sum_block<1>(ss, part);
+    sum.add<1>(ss);
     ry = 1.0f / sqrtf(ss[0] / a.H + a.eps);
     ss[0] = 0.0f;
   }
@@ -109,7 +136,7 @@ __global__ void residual_norm_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss[0] += x[p].v[i] * x[p].v[i];
   }
-  sum_block<1>(ss, part);
+  sum.add<1>(ss);
   const float rx = 1.0f / sqrtf(ss[0] / a.H + a.eps);
 #pragma unroll
   for (int p = 0; p < CPT; ++p) {
@@ -123,115 +150,156 @@ __global__ void residual_norm_kernel(NormArgs a) {
 }
 
 // With xh = x r, r = (mean x^2 + eps)^-1/2 and v = g_norm w_pre:
-//   dx = g_res + r (v - xh mean(v xh));  residual: a dx;  dt = b gate dx;  gate: b dx t;
-//   y: with q = dt w_post, yh = y ry: ry (q - yh mean(q yh)); without a post norm dt itself.
-// A workgroup takes rows blockIdx, blockIdx + blocks, ... and keeps its share of the column sums in
-// registers; the workgroups' shares are added in order by sum_columns_kernel.
+//   d = g_res + r (v - xh mean(v xh));  residual: a d;  gate: b d t;
+//   y: with q = b gate d w_post, yh = y ry: ry (q - yh mean(q yh)); without a post norm b gate d itself.
+// Column sums: w_pre of g_norm xh; and one more, of s = b d yh (yh = y without a post norm; times a token's
+// gate): w_post's is gate times it, a channel gate's is w_post times it.
+// A workgroup takes rows blockIdx, blockIdx + blocks, ... and keeps the weights and its share of the column
+// sums in registers; the workgroups' shares are added in order by sum_columns_kernel.  What a row waits for is
+// the loads and two sums over the workgroup, one after the other: the next row's loads are started first.
 template <int CPT, bool POST, int GATE>
-__global__ void residual_norm_backward_kernel(NormGradArgs a) {
-  __shared__ float part[3 * 16];
-  V8 s_pre[CPT] = {}, s_post[CPT] = {}, s_gate[CPT] = {};
+__global__ __launch_bounds__(kMaxThreads) void residual_norm_backward_kernel(NormGradArgs a) {
+  __shared__ __attribute__((aligned(16))) float part[2][3 * 16];
+  BlockSum sum(part);
+  constexpr bool Y = POST || GATE != kNone;
+  struct Row {
+    uint4 x[CPT], g[CPT], r[CPT], y[CPT], t[CPT];
+  };
+  auto column = [&](int p) { return static_cast<int>(p * blockDim.x + threadIdx.x) * 8; };
+  auto load = [&](int64_t r, Row& v) {
+#pragma unroll
+    for (int p = 0; p < CPT; ++p) {
+      const int c = column(p);
+      v.x[p] = v.g[p] = v.r[p] = v.y[p] = v.t[p] = uint4{0, 0, 0, 0};
+      if (c >= a.H || r >= a.n) continue;
+      v.x[p] = *reinterpret_cast<const uint4*>(a.x + r * a.ld_x + c);
+      v.g[p] = *reinterpret_cast<const uint4*>(a.g_norm + r * a.ld_g_norm + c);
+      if (Y) v.y[p] = *reinterpret_cast<const uint4*>(a.y + r * a.ld_y + c);
+      if (a.g_res) v.r[p] = *reinterpret_cast<const uint4*>(a.g_res + r * a.ld_g_res + c);
+      if (GATE == kToken) v.t[p] = *reinterpret_cast<const uint4*>(a.gate + r * a.ld_gate + c);
+    }
+  };
+  // scale: b, times a channel's gate, times w_post
+  V8 w_pre[CPT] = {}, scale[CPT], s_pre[CPT] = {}, s_two[CPT] = {};
+#pragma unroll
+  for (int p = 0; p < CPT; ++p) {
+    const int c = column(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) scale[p].v[i] = a.b;
+    if (c >= a.H) continue;
+    w_pre[p] = weights8(a.w_pre, a.pre_f32, c);
+    V8 w, g;
+    if constexpr (POST) w = weights8(a.w_post, a.post_f32, c);
+    if constexpr (GATE == kChannel) g = load8(a.gate + c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (POST) scale[p].v[i] *= w.v[i];
+      if constexpr (GATE == kChannel) scale[p].v[i] *= g.v[i];
+    }
+  }
   const float inv = 1.0f / a.H;
+  constexpr bool AHEAD = CPT == 1;   // two pieces a thread leave no registers for another row
+  Row now, next;
+  if (AHEAD) load(blockIdx.x, now);
   for (int64_t r = blockIdx.x; r < a.n; r += gridDim.x) {
-    V8 x[CPT], g[CPT], y[CPT];
+    if constexpr (AHEAD) load(r + gridDim.x, next);
+    else load(r, now);
     float v[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int p = 0; p < CPT; ++p) {
-      const int c = (p * blockDim.x + threadIdx.x) * 8;
-      const bool in = c < a.H;
-      x[p] = in ? load8(a.x + r * a.ld_x + c) : V8{};
-      g[p] = in ? load8(a.g_norm + r * a.ld_g_norm + c) : V8{};
-      if (POST || GATE != kNone) y[p] = in ? load8(a.y + r * a.ld_y + c) : V8{};
-      const V8 w = in ? weights8(a.w_pre, a.pre_f32, c) : V8{};
+      const V8 x = unpack(now.x[p]), g = unpack(now.g[p]), y = unpack(now.y[p]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[0] += x[p].v[i] * x[p].v[i];
-        v[1] += g[p].v[i] * w.v[i] * x[p].v[i];
-        if constexpr (POST) v[2] += y[p].v[i] * y[p].v[i];
+        v[0] += x.v[i] * x.v[i];
+        v[1] += g.v[i] * w_pre[p].v[i] * x.v[i];
+        if constexpr (POST) v[2] += y.v[i] * y.v[i];
       }
     }
-    sum_block<3>(v, part);
+    sum.add<3>(v);
     const float rx = 1.0f / sqrtf(v[0] * inv + a.eps);
-    const float mx = v[1] * rx * inv;   // mean of v xh
+    const float kx = v[1] * rx * inv * rx * rx;   // r^2 mean(v xh)
     const float ry = POST ? 1.0f / sqrtf(v[2] * inv + a.eps) : 1.0f;
-    float q[1] = {0.0f};
+    float m[1] = {0.0f};
+    V8 q[CPT];
 #pragma unroll
     for (int p = 0; p < CPT; ++p) {
-      const int c = (p * blockDim.x + threadIdx.x) * 8;
-      if (c >= a.H) continue;
-      const V8 w = weights8(a.w_pre, a.pre_f32, c);
-      V8 gr{}, wp, gt, dx, dg;
-      if (a.g_res) gr = load8(a.g_res + r * a.ld_g_res + c);
-      if constexpr (POST) wp = weights8(a.w_post, a.post_f32, c);
-      if constexpr (GATE != kNone) gt = load8(a.gate + (GATE == kToken ? r * a.ld_gate : 0) + c);
+      const V8 x = unpack(now.x[p]), g = unpack(now.g[p]), y = unpack(now.y[p]), gr = unpack(now.r[p]);
+      const V8 gt = unpack(now.t[p]);
+      V8 dx, dg;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float xh = x[p].v[i] * rx, yh = POST ? y[p].v[i] * ry : 0.0f;
-        const float d = gr.v[i] + rx * (g[p].v[i] * w.v[i] - xh * mx);
-        s_pre[p].v[i] += g[p].v[i] * xh;
+        const float d = gr.v[i] + rx * (g.v[i] * w_pre[p].v[i]) - kx * x.v[i];
+        s_pre[p].v[i] += g.v[i] * x.v[i] * rx;
         dx.v[i] = a.a * d;
-        float dt = a.b * d;
-        if constexpr (GATE != kNone) {
-          const float t = POST ? yh * wp.v[i] : y[p].v[i];
-          dg.v[i] = dt * t;
-          if constexpr (GATE == kChannel) s_gate[p].v[i] += dg.v[i];
-          dt *= gt.v[i];
+        q[p].v[i] = d * scale[p].v[i];
+        const float yh = POST ? y.v[i] * ry : y.v[i];
+        if constexpr (GATE == kToken) {
+          dg.v[i] = q[p].v[i] * yh;
+          q[p].v[i] *= gt.v[i];
         }
-        if constexpr (POST) {
-          s_post[p].v[i] += dt * yh;
-          dt *= wp.v[i];
-          q[0] += dt * yh;
+        if constexpr (Y && (POST || GATE == kChannel)) {
+          const float e = a.b * d * (GATE == kToken ? gt.v[i] : 1.0f);
+          s_two[p].v[i] += e * yh;
         }
-        g[p].v[i] = dt;
+        if constexpr (POST) m[0] += q[p].v[i] * yh;
       }
+      const int c = column(p);
+      if (c >= a.H) continue;
       *reinterpret_cast<uint4*>(a.dres + r * a.ld_dres + c) = pack(dx);
       if constexpr (GATE == kToken) {
         if (a.dgate_token) *reinterpret_cast<uint4*>(a.dgate_token + r * a.ld_dgate + c) = pack(dg);
       }
     }
-    float my = 0.0f;
-    if constexpr (POST) {
-      sum_block<1>(q, part);
-      my = q[0] * inv;
-    }
+    if constexpr (POST) sum.add<1>(m);
+    const float ky = m[0] * inv * ry * ry;
 #pragma unroll
     for (int p = 0; p < CPT; ++p) {
-      const int c = (p * blockDim.x + threadIdx.x) * 8;
+      const int c = column(p);
       if (c >= a.H) continue;
-      V8 dy;
+      if constexpr (POST) {
+        const V8 y = unpack(now.y[p]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dy.v[i] = POST ? ry * (g[p].v[i] - y[p].v[i] * ry * my) : g[p].v[i];
-      *reinterpret_cast<uint4*>(a.dy + r * a.ld_dy + c) = pack(dy);
+        for (int i = 0; i < 8; ++i) q[p].v[i] = ry * q[p].v[i] - ky * y.v[i];
+      }
+      *reinterpret_cast<uint4*>(a.dy + r * a.ld_dy + c) = pack(q[p]);
     }
+    if constexpr (AHEAD) now = next;
   }
 #pragma unroll
   for (int p = 0; p < CPT; ++p) {
-    const int c = (p * blockDim.x + threadIdx.x) * 8;
+    const int c = column(p);
     if (c >= a.H) continue;
     float* at = a.work + static_cast<int64_t>(blockIdx.x) * a.H + c;
-    const int64_t next = static_cast<int64_t>(gridDim.x) * a.H;
     store8(at, s_pre[p]);
-    if (POST) store8(at += next, s_post[p]);
-    if (GATE == kChannel) store8(at += next, s_gate[p]);
+    if (POST || GATE == kChannel) store8(at + static_cast<int64_t>(gridDim.x) * a.H, s_two[p]);
   }
 }
 
-// Column sums of `blocks` rows: 64 columns a workgroup, 16 threads a column; blockIdx.y picks the sum.
-__global__ __launch_bounds__(1024) void sum_columns_kernel(const float* work, int blocks, int H, float* o0, float* o1,
-                                                           float* o2) {
+__device__ __forceinline__ float weight_at(const void* w, bool f32, int c) {
+  return f32 ? static_cast<const float*>(w)[c] : lo(static_cast<const uint16_t*>(w)[c]);
+}
+
+// Column sums of the workgroups' shares: 64 columns a workgroup, 16 threads a column.  blockIdx.y 0: w_pre's;
+// 1: the second sum, of which w_post's and a channel gate's are multiples.
+__global__ __launch_bounds__(1024) void sum_columns_kernel(NormGradArgs a, int blocks) {
   __shared__ float part[16][64];
-  float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
   const int c = blockIdx.x * 64 + lane_id(), q = threadIdx.x >> 6;
-  const float* w = work + static_cast<int64_t>(blockIdx.y) * blocks * H;
+  const float* w = a.work + static_cast<int64_t>(blockIdx.y) * blocks * a.H;
   float s = 0.0f;
-  if (c < H)
-    for (int b = q; b < blocks; b += 16) s += w[static_cast<int64_t>(b) * H + c];
+  if (c < a.H)
+    for (int b = q; b < blocks; b += 16) s += w[static_cast<int64_t>(b) * a.H + c];
   part[q][lane_id()] = s;
   __syncthreads();
-  if (q != 0 || c >= H || !out) return;
+  if (q != 0 || c >= a.H) return;
 #pragma unroll
   for (int i = 1; i < 16; ++i) s += part[i][lane_id()];
-  out[c] = s;
+  if (blockIdx.y == 0) {
+    a.dw_pre[c] = s;
+    return;
+  }
+  const bool channel = a.gate && !a.gate_rows;
+  if (a.dw_post) a.dw_post[c] = channel ? s * lo(a.gate[c]) : s;
+  if (a.dgate_channel) a.dgate_channel[c] = a.w_post ? s * weight_at(a.w_post, a.post_f32, c) : s;
 }
 
 inline int pieces(int H) { return H / 8 > kMaxThreads ? 2 : 1; }
@@ -255,7 +323,12 @@ void run_backward(const NormGradArgs& a, int gate, int blocks, hipStream_t s) {
 
 }  // namespace
 
-int grad_blocks(int64_t n) { return static_cast<int>(n < kGradBlocks ? n : kGradBlocks); }
+// One workgroup per CU when it fills one (16 waves at 128 registers); of smaller ones as many as fit, while
+// each has eight rows for its share of the column sums (4096 x 7168: 256 workgroups).
+int grad_blocks(int64_t n, int H) {
+  const int64_t fit = kNormCus * std::max(1, 16 / (threads(H) / 64));
+  return static_cast<int>(std::min(n, std::max<int64_t>(kNormCus, std::min(fit, n / 8))));
+}
 
 hipError_t launch_residual_norm(const NormArgs& a, hipStream_t s) {
   if (a.n == 0) return hipSuccess;
@@ -266,7 +339,7 @@ hipError_t launch_residual_norm(const NormArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_residual_norm_backward(const NormGradArgs& a, hipStream_t s) {
-  const int gate = !a.gate ? kNone : a.gate_rows ? kToken : kChannel, blocks = grad_blocks(a.n);
+  const int gate = !a.gate ? kNone : a.gate_rows ? kToken : kChannel, blocks = grad_blocks(a.n, a.H);
   if (blocks > 0) {
     if (pieces(a.H) == 1)
       a.w_post ? run_backward<1, true>(a, gate, blocks, s) : run_backward<1, false>(a, gate, blocks, s);
@@ -274,11 +347,8 @@ hipError_t launch_residual_norm_backward(const NormGradArgs& a, hipStream_t s) {
       a.w_post ? run_backward<2, true>(a, gate, blocks, s) : run_backward<2, false>(a, gate, blocks, s);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  float* sums[3] = {a.dw_pre, nullptr, nullptr};
-  int count = 1;
-  if (a.w_post) sums[count++] = a.dw_post;
-  if (gate == kChannel) sums[count++] = a.dgate_channel;
-  sum_columns_kernel<<<dim3((a.H + 63) / 64, count), 1024, 0, s>>>(a.work, blocks, a.H, sums[0], sums[1], sums[2]);
+  const int sums = a.dw_post || a.dgate_channel ? 2 : 1;
+  sum_columns_kernel<<<dim3((a.H + 63) / 64, sums), 1024, 0, s>>>(a, blocks);
   return hipGetLastError();
 }
 

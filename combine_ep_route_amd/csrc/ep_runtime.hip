@@ -1531,7 +1531,7 @@ EP_API ep_status_t ep_residual_norm(ep_group_t group, const ep_tensor_t* y, cons
 EP_API ep_status_t ep_residual_norm_workspace(ep_group_t group, int64_t n, int64_t* bytes) {
   Group* g = reinterpret_cast<Group*>(group);
   if (!group_ok(g) || n < 0 || !bytes) return EP_ERR_INVALID_ARGUMENT;
-  *bytes = static_cast<int64_t>(3) * norm::grad_blocks(n) * g->cfg.hidden * 4;
+  *bytes = static_cast<int64_t>(2) * norm::grad_blocks(n, g->cfg.hidden) * g->cfg.hidden * 4;
   return EP_OK;
 }
 
@@ -1559,7 +1559,7 @@ EP_API ep_status_t ep_residual_norm_backward(ep_group_t group, const ep_tensor_t
   if (grad_gate && !(per_token ? rows_bf16(grad_gate, n, H) : check_vector(grad_gate, H, true)))
     return EP_ERR_INVALID_ARGUMENT;
   if (n > kMaxNormRows) return EP_ERR_UNSUPPORTED;
-  const int64_t need = static_cast<int64_t>(3) * norm::grad_blocks(n) * H * 4;
+  const int64_t need = static_cast<int64_t>(2) * norm::grad_blocks(n, static_cast<int>(H)) * H * 4;
   if (n > 0 && (!workspace || workspace->dtype != EP_DTYPE_U8 || workspace->ndim != 1 || workspace->strides[0] != 1 ||
                 workspace->sizes[0] < need || !workspace->data ||
                 (reinterpret_cast<uintptr_t>(workspace->data) & 15) != 0))
