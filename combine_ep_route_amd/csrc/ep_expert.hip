@@ -383,11 +383,23 @@ hipError_t launch_along_as(const AlongArgs& a, hipStream_t stream, bool check) {
   return hipGetLastError();
 }
 
+// Which tile a product over the rows takes, by the average rows of an expert (the counts themselves are only
+// on the device) and by how many 256 x 256 tiles there are for the 256 CUs.
+enum Size { kSmall, kMiddle, kBig };
+Size tile_size(const ExpertRows& r, int64_t rows, int64_t col_tiles) {
+  const int64_t each = rows / r.E;
+  if (each <= 24) return kSmall;
+  return each <= 128 || r.E * ((each + 255) / 256) * col_tiles < 256 ? kMiddle : kBig;
+}
+
 template <bool F8, int KIND, int ACT>
 hipError_t launch_along_kind(const AlongArgs& a, hipStream_t stream, bool check) {
-  if (a.rows_max <= static_cast<int64_t>(a.rows.E) * 32)
-    return launch_along_as<Core<128, 32, 4, 1, false, false, F8, 4, 128>, KIND, ACT>(a, stream, check);
-  return launch_along_as<Core<256, 256, 2, 4, false, false, F8, 2, 128>, KIND, ACT>(a, stream, check);
+  const int cols = KIND == kLinear ? 256 : 128;
+  switch (tile_size(a.rows, a.rows_max, (a.N + cols - 1) / cols)) {
+    case kSmall: return launch_along_as<Core<128, 32, 4, 1, false, false, F8, 4, 128>, KIND, ACT>(a, stream, check);
+    case kMiddle: return launch_along_as<Core<128, 128, 2, 2, false, false, F8, 2, 128>, KIND, ACT>(a, stream, check);
+    default: return launch_along_as<Core<256, 256, 2, 4, false, false, F8, 2, 128>, KIND, ACT>(a, stream, check);
+  }
 }
 
 template <bool F8>
@@ -418,8 +430,10 @@ hipError_t launch_gated_grad(const AlongArgs& a, int act, hipStream_t stream, bo
                       : launch_along_kind<false, kGatedGrad, kGeluTanh>(a, stream, check);
 }
 
-hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check) {
-  using C = Core<256, 256, 2, 4, true, false, false, 4, 64>;
+namespace {
+
+template <class C>
+hipError_t launch_row_grad_as(const RowGradArgs& g, hipStream_t stream, bool check) {
   const int64_t tiles = row_tiles<C::BB>(g.rows, g.rows_max, g.per_expert_max) * ((g.N + C::BA - 1) / C::BA);
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
   if (tiles == 0 || check) return hipSuccess;
@@ -427,8 +441,8 @@ hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check)
   return hipGetLastError();
 }
 
-hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check) {
-  using C = Core<256, 256, 2, 4, true, true, false, 4, 64>;
+template <class C>
+hipError_t launch_weight_grad_as(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check) {
   const int64_t tiles = static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + C::BA - 1) / C::BA) *
                         ((g.I + C::BB - 1) / C::BB);
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
@@ -442,6 +456,22 @@ hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t str
     else weight_grad_kernel<C, false, false><<<blocks, C::NT, 0, stream>>>(g);
   }
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check) {
+  switch (tile_size(g.rows, g.rows_max, (g.N + 255) / 256)) {
+    case kSmall: return launch_row_grad_as<Core<128, 32, 4, 1, true, false, false, 4, 128>>(g, stream, check);
+    case kMiddle: return launch_row_grad_as<Core<128, 128, 2, 2, true, false, false, 4, 64>>(g, stream, check);
+    default: return launch_row_grad_as<Core<256, 256, 2, 4, true, false, false, 4, 64>>(g, stream, check);
+  }
+}
+
+hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check) {
+  if (static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + 255) / 256) * ((g.I + 255) / 256) < 512)
+    return launch_weight_grad_as<Core<128, 128, 2, 2, true, true, false, 4, 64>>(g, f32, stream, check);
+  return launch_weight_grad_as<Core<256, 256, 2, 4, true, true, false, 4, 64>>(g, f32, stream, check);
 }
 
 }  // namespace expert

@@ -45,6 +45,8 @@ SHAPES = [
     ("ht", 1, 700, 4, 2, 256, 712, ()),       # several row tiles per expert
     ("ll", 2, 300, 2, 2, 336, 512, ()),
     ("ht", 1, 300, 3, 1, 640, 1000, (0, 2)),  # all rows on one expert
+    ("ht", 1, 2400, 32, 2, 2064, 2072, (7,)),  # the largest tiles, filled by every number of quarters
+    ("ll", 4, 600, 32, 2, 2064, 2072, (7,)),
 ]
 
 
@@ -68,7 +70,8 @@ def test_gated(shape, act):
 
 
 @pytest.mark.parametrize("shape", [s[:5] + (h, i, s[7]) for s, h, i in
-                                   zip(SHAPES, (128, 384, 512, 1152, 256, 640, 896), (8, 136, 256, 520, 712, 128, 1000))],
+                                   zip(SHAPES, (128, 384, 512, 1152, 256, 640, 896, 384, 384),
+                                       (8, 136, 256, 520, 712, 128, 1000, 2072, 2072))],
                          ids=str)
 def test_gated_fp8(shape):
     """Rows as the dispatch packed them, in the group's own buffer."""
@@ -117,7 +120,7 @@ def test_linear(shape):
         untouched(r, out)
 
 
-@pytest.mark.parametrize("shape", [s[:6] + (i, s[7]) for s, i in zip(SHAPES, (128, 256, 384, 128, 640, 512, 1024))],
+@pytest.mark.parametrize("shape", [s[:6] + (i, s[7]) for s, i in zip(SHAPES, (128, 256, 384, 128, 640, 512, 1024, 384, 384))],
                          ids=str)
 def test_linear_fp8(shape):
     mode, S, T, E, K, H, I, skip = shape
