@@ -389,7 +389,7 @@ enum Size { kSmall, kMiddle, kBig };
 Size tile_size(const ExpertRows& r, int64_t rows, int64_t col_tiles) {
   const int64_t each = rows / r.E;
   if (each <= 24) return kSmall;
-  return each <= 128 || r.E * ((each + 255) / 256) * col_tiles < 256 ? kMiddle : kBig;
+  return each <= 96 || r.E * ((each + 255) / 256) * col_tiles < 256 ? kMiddle : kBig;
 }
 
 template <bool F8, int KIND, int ACT>

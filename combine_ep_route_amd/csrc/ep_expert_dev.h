@@ -333,30 +333,36 @@ struct Core {
       x[j] = sc[from_b(j) + (lane_id() & 15)];
     }
     i32x4 lo = along_frag(ta, Src::frag_a_at(fa, 0), 0), hi = along_frag(ta, Src::frag_a_at(fa, 0), 1);
+    // The sums of a fragment's results follow while the next one's products run.
+    f32x4 p[2][NJ];
 #pragma unroll
-    for (int i = 0; i < FA; ++i) {
-      if (i == 0 || i == FA / 2) {
-        const float w = Src::second_scale(fa, i) ? w1 : w0;
+    for (int i = 0; i <= FA; ++i) {
+      if (i < FA) {
+        const i32x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        issue_part<NJ>(src, i, before);
+        if (i + 1 < FA) {
+          lo = along_frag(ta, Src::frag_a_at(fa, i + 1), 0);
+          hi = along_frag(ta, Src::frag_a_at(fa, i + 1), 1);
+        }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) c[j] = x[j] * w;
+        for (int j = 0; j < NJ; ++j)
+          p[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[j], f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
       }
-      const i32x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      issue_part<NJ>(src, i, before);
-      if (i + 1 < FA) {
-        lo = along_frag(ta, Src::frag_a_at(fa, i + 1), 0);
-        hi = along_frag(ta, Src::frag_a_at(fa, i + 1), 1);
+      if (i > 0) {
+        if (i - 1 == 0 || i - 1 == FA / 2) {
+          const float w = Src::second_scale(fa, i - 1) ? w1 : w0;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) c[j] = x[j] * w;
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            acc[i - 1][j][k] = __builtin_fmaf(p[(i - 1) & 1][j][k], c[j], acc[i - 1][j][k]);
+        // Without these the compiler reads all fragments ahead, puts off all sums and spills them.
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(acc[i - 1][j]));
       }
-      f32x4 p[NJ];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        p[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[j], f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][j][k] = __builtin_fmaf(p[j][k], c[j], acc[i][j][k]);
-      // Without these the compiler reads all fragments ahead, puts off all sums and spills them.
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(acc[i][j]));
       __builtin_amdgcn_sched_barrier(0);
     }
   }
