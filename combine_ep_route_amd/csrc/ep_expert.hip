@@ -250,13 +250,13 @@ __global__ __launch_bounds__(C::NT, 2) void row_grad_kernel(RowGradArgs g) {
 // Gradient of the weights: dw[e][i][h] = sum over the expert's rows r of dy[r][i] x[r][h]
 // ---------------------------------------------------------------------------
 
-// LIST: the rows are looked up step by step (LL, many sources); else they follow each other.  Rows past the
+// LIST: the rows are looked up step by step (LL, several sources); else they follow each other.  Rows past the
 // expert's last one are zeros in both operands.
 template <class C, bool LIST>
 struct WeightGradSrc {
   const WeightGradArgs& g;
   const Span& s;
-  const uint8_t *x, *dy;      // bases of the step; with a list the expert's first slot
+  const uint8_t *x, *dy;      // bases of the step; else the expert's first slot
   int64_t ld_dy;
   int offa[C::JA], offb[C::JB];
   int h0, i0, left;
@@ -396,7 +396,7 @@ template <bool F8, int KIND, int ACT>
 hipError_t launch_along_kind(const AlongArgs& a, hipStream_t stream, bool check) {
   const int cols = KIND == kLinear ? 256 : 128;
   switch (tile_size(a.rows, a.rows_max, (a.N + cols - 1) / cols)) {
-    case kSmall: return launch_along_as<Core<128, 32, 4, 1, false, false, F8, 4, 128>, KIND, ACT>(a, stream, check);
+    case kSmall: return launch_along_as<Core<128, 32, 4, 1, false, false, F8, F8 ? 3 : 4, 128>, KIND, ACT>(a, stream, check);
     case kMiddle: return launch_along_as<Core<128, 128, 2, 2, false, false, F8, 2, 128>, KIND, ACT>(a, stream, check);
     default: return launch_along_as<Core<256, 256, 2, 4, false, false, F8, 2, 128>, KIND, ACT>(a, stream, check);
   }
@@ -448,7 +448,7 @@ hipError_t launch_weight_grad_as(const WeightGradArgs& g, bool f32, hipStream_t 
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
   if (check) return hipSuccess;
   const int blocks = static_cast<int>((tiles + 7) / 8 * 8);
-  if (g.rows.list) {
+  if (scattered(g.rows)) {
     if (f32) weight_grad_kernel<C, true, true><<<blocks, C::NT, 0, stream>>>(g);
     else weight_grad_kernel<C, false, true><<<blocks, C::NT, 0, stream>>>(g);
   } else {

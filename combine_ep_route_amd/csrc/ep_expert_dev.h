@@ -66,6 +66,9 @@ __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane
 // Which rows an expert holds
 // ---------------------------------------------------------------------------
 
+// Whether an expert's rows lie in several runs.
+__host__ __device__ inline bool scattered(const ExpertRows& r) { return r.list != nullptr || r.sources > 1; }
+
 struct Span {
   int e = -1;             // expert, or -1: none
   int count = 0;          // its rows within the limit
@@ -75,13 +78,18 @@ struct Span {
   int m = 0, n = 0;       // row tile and column tile in it
 };
 
+// Inclusive sum over the lanes: shifts by 1, 2, 4 and 8 inside rows of 16, then the rows' last lanes.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int add_dpp(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
 __device__ __forceinline__ int scan64(int v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    v += lane_id() >= d ? o : 0;
-  }
-  return v;
+  v = add_dpp<0x111, 0xf>(v);
+  v = add_dpp<0x112, 0xf>(v);
+  v = add_dpp<0x114, 0xf>(v);
+  v = add_dpp<0x118, 0xf>(v);
+  v = add_dpp<0x142, 0xa>(v);
+  return add_dpp<0x143, 0xc>(v);
 }
 
 // Workgroups go to the 8 XCDs in turn: XCD x takes the x-th eighth of the tiles, so that tiles that share
@@ -102,7 +110,18 @@ __device__ __forceinline__ Span find_span(const ExpertRows& r, int which, int co
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     // all loads at once: what lies outside is read in bounds and counts nothing
-    if (i < per) c[i] = r.count[e0 + i < r.E ? e0 + i : r.E - 1];
+    if (i < per) {
+      const int32_t* p = r.count + (e0 + i < r.E ? e0 + i : r.E - 1) * r.sources;
+      if (r.sources == 1) {
+        c[i] = p[0];
+      } else {
+        int v[kFewSources];
+#pragma unroll
+        for (int k = 0; k < kFewSources; ++k) v[k] = p[k < r.sources ? k : 0];
+#pragma unroll
+        for (int k = 0; k < kFewSources; ++k) c[i] += k < r.sources ? v[k] : 0;
+      }
+    }
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -145,17 +164,30 @@ __device__ __forceinline__ Span find_span(const ExpertRows& r, int which, int co
     s.n = local / t;
     s.m = local - s.n * t;
   }
-  if (r.list == nullptr && s.first + static_cast<int64_t>(s.count) > r.limit)
+  if (!scattered(r) && s.first + static_cast<int64_t>(s.count) > r.limit)
     s.count = r.limit > s.first ? static_cast<int>(r.limit - s.first) : 0;
   return s;
 }
 
 // The row that offsets in a tile from its row m0 on count from.
 __device__ __forceinline__ int64_t first_row(const ExpertRows& r, const Span& s, int m0) {
-  return r.list ? s.first : s.first + m0;
+  return scattered(r) ? s.first : s.first + m0;
 }
 __device__ __forceinline__ int row_of(const ExpertRows& r, const Span& s, int p) {
-  return r.list ? r.list[s.before + p] : s.first + p;
+  if (r.list) return r.list[s.before + p];
+  if (r.sources == 1) return s.first + p;
+  const int32_t* c = r.count + s.e * r.sources;
+  int v[kFewSources], at = s.first;
+#pragma unroll
+  for (int k = 0; k < kFewSources; ++k) v[k] = c[k < r.sources ? k : 0];
+  bool on = true;   // p lies behind the sources so far
+#pragma unroll
+  for (int k = 0; k + 1 < kFewSources; ++k) {
+    on = on && k + 1 < r.sources && p >= v[k];
+    p -= on ? v[k] : 0;
+    at += on ? r.slots : 0;
+  }
+  return at + p;
 }
 
 // ---------------------------------------------------------------------------

@@ -303,17 +303,20 @@ hipError_t launch_dequant(const DequantArgs& a, hipStream_t stream);
 
 namespace expert {
 
-// Rows of expert e, p = 0 .. count[e]-1, in the receive layout: list[before(e) + p] with a list (LL, many
-// sources: slots are filled per source); else e*stride + p with a stride (LL, one source); else
-// before(e) + p (HT).  before(e) is the sum of the counts of the experts before e; in LL the slots of
-// expert e are e*stride .. (e+1)*stride - 1.
-// In a tile, offsets are 32-bit: 256 rows of any operand, and with a list an expert's slots, span less than
-// 2^31 bytes.
+// Rows of expert e, p = 0 .. n(e)-1, in the receive layout; before(e) is the sum of the n of the experts
+// before e.
+//   HT:              row before(e) + p;  n(e) = count[e].
+//   LL, one source:  row e*stride + p;   n(e) = count[e].
+//   LL, few sources: source s fills slots e*stride + s*slots ..; n(e) is the sum of count[e*sources + s].
+//   LL, many:        row list[before(e) + p];  n(e) = count[e] (launch_list_rows makes both).
+// In a tile, offsets are 32-bit: 256 rows of any operand, and with several sources an expert's slots, span
+// less than 2^31 bytes.
+constexpr int kFewSources = 8;
 struct ExpertRows {
-  const int32_t* count;   // [E]
+  const int32_t* count;
   const int32_t* list;
   int64_t limit;          // rows that the caller's tensors hold
-  int32_t E, stride;
+  int32_t E, stride, sources, slots;
   int32_t* err;           // device error word: rows beyond the limit are left out and reported
 };
 

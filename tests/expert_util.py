@@ -36,8 +36,11 @@ class Routing:
             topk = np.argsort(-score, axis=1)[:, :K].astype(np.int32)
         self.topk = topk
         self.E, self.S, self.T, self.K, self.H, self.mode = E, S, T, K, H, mode
-        ranks = max(r for r in (1, 2, 4, 8) if E % r == 0)
-        cfg = dict(mode=mode, num_nodes=1, ranks_per_node=ranks, num_experts=E, top_k=K, max_nodes_per_token=0,
+        ranks = max(r for r in (1, 2, 4, 8, 16) if E % r == 0)
+        nodes = 2 if S > ranks and E % (2 * ranks) == 0 else 1
+        ranks = E if S > nodes * ranks else ranks
+        nodes = 1 if ranks == E else nodes
+        cfg = dict(mode=mode, num_nodes=nodes, ranks_per_node=ranks, num_experts=E, top_k=K, max_nodes_per_token=0,
                    hidden=H, max_tokens_per_rank=T, num_src_ranks=S, payload=payload)
         cfg.update(over)
         self.slots = cfg["max_tokens_per_rank"]

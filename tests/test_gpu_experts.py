@@ -40,13 +40,15 @@ def weights_fp8(E, N, K, seed):
 SHAPES = [
     ("ht", 1, 1, 8, 1, 16, 8, ()),            # one token, sizes below one piece
     ("ht", 3, 37, 16, 2, 272, 136, (0, 5)),   # contracted tails, empty experts
-    ("ll", 4, 33, 16, 3, 512, 264, (15,)),    # a list of slots from several sources
+    ("ll", 4, 33, 16, 3, 512, 264, (15,)),    # slots of several sources
+    ("ll", 16, 9, 32, 3, 256, 136, (31,)),    # a list: more sources than are looked up in the counts
     ("ll", 1, 50, 8, 2, 1040, 520, ()),       # one source: slots in place
     ("ht", 1, 700, 4, 2, 256, 712, ()),       # several row tiles per expert
     ("ll", 2, 300, 2, 2, 336, 512, ()),
     ("ht", 1, 300, 3, 1, 640, 1000, (0, 2)),  # all rows on one expert
     ("ht", 1, 2400, 32, 2, 2064, 2072, (7,)),  # the largest tiles, filled by every number of quarters
     ("ll", 4, 600, 32, 2, 2064, 2072, (7,)),
+    ("ll", 24, 100, 48, 2, 2064, 1040, (7,)),
 ]
 
 
@@ -70,8 +72,8 @@ def test_gated(shape, act):
 
 
 @pytest.mark.parametrize("shape", [s[:5] + (h, i, s[7]) for s, h, i in
-                                   zip(SHAPES, (128, 384, 512, 1152, 256, 640, 896, 384, 384),
-                                       (8, 136, 256, 520, 712, 128, 1000, 2072, 2072))],
+                                   zip(SHAPES, (128, 384, 512, 256, 1152, 256, 640, 896, 384, 384, 256),
+                                       (8, 136, 256, 136, 520, 712, 128, 1000, 2072, 2072, 1040))],
                          ids=str)
 def test_gated_fp8(shape):
     """Rows as the dispatch packed them, in the group's own buffer."""
@@ -120,7 +122,7 @@ def test_linear(shape):
         untouched(r, out)
 
 
-@pytest.mark.parametrize("shape", [s[:6] + (i, s[7]) for s, i in zip(SHAPES, (128, 256, 384, 128, 640, 512, 1024, 384, 384))],
+@pytest.mark.parametrize("shape", [s[:6] + (i, s[7]) for s, i in zip(SHAPES, (128, 256, 384, 256, 128, 640, 512, 1024, 384, 384, 256))],
                          ids=str)
 def test_linear_fp8(shape):
     mode, S, T, E, K, H, I, skip = shape
