@@ -147,6 +147,7 @@ SIGNATURES = {
     "ep_dispatch_backward": (_S, [_P, _PT, _PT, _P]),
     "ep_expert_gated": (_S, [_P, _PT, _PT, _PT, _PT, _PT, ctypes.c_int32, _PT, _P]),
     "ep_expert_gated_backward": (_S, [_P, _PT, _PT, _PT, _PT, ctypes.c_int32, _PT, _PT, _PT, _PT, _PT, _P]),
+    "ep_expert_quantize": (_S, [_P, _PT, _PT, _PT, _P]),
     "ep_expert_linear": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _P]),
     "ep_expert_linear_backward": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _P]),
     "ep_residual_norm": (_S, [_P, _PT, _PT, _PT, _PT, _PT, ctypes.c_float, ctypes.c_float, ctypes.c_float, _PT, _PT,

@@ -527,15 +527,24 @@ __global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs p, int W_) {
 // pre-quantised: the same chunk mapping and quantize() as the dispatch, so
 // the codes and scales are the ones the dispatch would write.  Codes go out as 16-byte stores; each block's scale is stored by
 // the first lane of its 8.
-template <int NV>
+// With a row map the rows are the ones its entries name (a.n entries).
+template <int NV, bool MAP>
 __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a, int W) {
   const int lane = threadIdx.x & 63;
   const int C = a.H / 16;
   const int64_t waves = static_cast<int64_t>(gridDim.x) * 4;
   const int64_t total = a.n * W;
   for (int64_t gw = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); gw < total; gw += waves) {
-    const int64_t i = gw / W;
+    int64_t i = gw / W;
     const int part = static_cast<int>(gw - i * W);
+    if constexpr (MAP) {
+      i = a.map[i];
+      if (i < 0) continue;
+      if (i >= a.rows) {
+        if (lane == 0 && part == 0) atomicOr(a.err, EP_DEVERR_ROW_RANGE);
+        continue;
+      }
+    }
     const int c0 = part * NV * 64 + lane;
     Raw raw[NV];
     const u32x4 zero{0, 0, 0, 0};
@@ -600,7 +609,9 @@ hipError_t launch_quantize(const QuantArgs& a, hipStream_t stream) {
   const int W = (C + 64 * kChunksPerLane - 1) / (64 * kChunksPerLane);
   int64_t blocks = (a.n * W + 3) / 4;
   if (blocks > 0x7FFFFFFF) blocks = 0x7FFFFFFF;
-  quantize_kernel<kChunksPerLane><<<dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream>>>(a, W);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(256);
+  if (a.map) quantize_kernel<kChunksPerLane, true><<<grid, block, 0, stream>>>(a, W);
+  else quantize_kernel<kChunksPerLane, false><<<grid, block, 0, stream>>>(a, W);
   return hipGetLastError();
 }
 

@@ -263,6 +263,10 @@ struct QuantArgs {
   int64_t ld_s;           // elements
   int64_t n;
   int H;
+  // With a row map (null: rows 0 .. n-1): n entries that name a row or -1; rows beyond `rows` are reported.
+  const int32_t* map;
+  int64_t rows;
+  int32_t* err;
 };
 hipError_t launch_quantize(const QuantArgs& a, hipStream_t stream);
 

@@ -1387,6 +1387,41 @@ EP_API ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_
   return EP_OK;
 }
 
+EP_API ep_status_t ep_expert_quantize(ep_handle_t handle, const ep_tensor_t* x_in, ep_tensor_t* q, ep_tensor_t* scales,
+                                      ep_stream_t stream) {
+  Handle* h = reinterpret_cast<Handle*>(handle);
+  if (!handle_ok(h) || !x_in || x_in->ndim < 2 || x_in->ndim > 3) return EP_ERR_INVALID_ARGUMENT;
+  Group* g = h->g;
+  if (const ep_status_t st = expert_ready(h); st != EP_OK) return st;
+  const int64_t C = x_in->sizes[x_in->ndim - 1];
+  ep_tensor_t x, qd, sd;
+  if (C <= 0 || C % 128 != 0 || !geometry_rows(g, x_in, EP_DTYPE_BF16, C, EP_TAG_TOKENS, true, &x) ||
+      !geometry_rows(g, q, EP_DTYPE_FP8_E4M3, C, EP_TAG_TOKENS, true, &qd) ||
+      !geometry_rows(g, scales, EP_DTYPE_F32, C / 128, EP_TAG_SCALES, false, &sd) ||
+      (reinterpret_cast<uintptr_t>(sd.data) & 3) || !holds_slots(g, x) || !holds_slots(g, qd) || !holds_slots(g, sd))
+    return EP_ERR_INVALID_ARGUMENT;
+  if (C > kMaxProductSize) return EP_ERR_UNSUPPORTED;
+  const hipStream_t s = as_stream(stream);
+  if (const ep_status_t st = ensure_device(g, s); st != EP_OK) return st;
+  h->stream = s;
+  if (const ep_status_t st = ensure_maps(h, s); st != EP_OK) return st;
+  QuantArgs a{};
+  a.x = static_cast<const uint16_t*>(x.data);
+  a.ld_x = x.strides[0];
+  a.q = static_cast<uint8_t*>(qd.data);
+  a.ld_q = qd.strides[0];
+  a.scales = static_cast<float*>(sd.data);
+  a.ld_s = sd.strides[0];
+  a.n = h->n * g->cfg.top_k;
+  a.H = static_cast<int>(C);
+  a.map = g->cfg.mode == EP_MODE_LL ? h->slot_map : h->row2;
+  a.rows = std::min({x.sizes[0], qd.sizes[0], sd.sizes[0]});
+  a.err = g->err;
+  const ep_status_t st = from_hip(launch_quantize(a, s));
+  if (st == EP_OK) trace(g, "expert_quantize", h->n);
+  return st;
+}
+
 EP_API ep_status_t ep_expert_linear(ep_handle_t handle, const ep_tensor_t* x_in, const ep_tensor_t* x_scales,
                                     const ep_tensor_t* w, const ep_tensor_t* w_scales, ep_tensor_t* out,
                                     ep_stream_t stream) {

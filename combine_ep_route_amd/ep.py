@@ -278,6 +278,11 @@ def ep_expert_gated_backward(handle: Handle, rows: torch.Tensor, w_gate: torch.T
         _ref(wg), _ref(wu), _stream(stream)))
 
 
+def ep_expert_quantize(handle: Handle, x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    xd, qd, sd = desc(x, A.EP_TAG_TOKENS), desc(q, A.EP_TAG_TOKENS), desc(scales, A.EP_TAG_SCALES)
+    _check("ep_expert_quantize", A.lib().ep_expert_quantize(handle.ptr, _ref(xd), _ref(qd), _ref(sd), _stream(stream)))
+
+
 def ep_expert_linear(handle: Handle, x: torch.Tensor, w: torch.Tensor, out: torch.Tensor,
                      x_scales: Optional[torch.Tensor] = None, w_scales: Optional[torch.Tensor] = None,
                      stream=None) -> None:

@@ -609,6 +609,17 @@ ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_t *rows
                                      ep_tensor_t *grad_rows, ep_tensor_t *grad_w_gate,
                                      ep_tensor_t *grad_w_up, ep_stream_t stream);
 
+/* FP8 quantisation of the experts' rows, for an FP8 product behind ep_expert_gated:
+ * every row that holds a message, with ep_quantize's arithmetic (scale = amax/448
+ * per 128 elements, codes the nearest-even, saturating E4M3 of x/scale).  Needs
+ * the handle's row map (written by its dispatch, or computed on first use).
+ *   x      : BF16 [rows, C] at the dispatch geometry, C a multiple of 128.
+ *   q      : FP8_E4M3 [rows, C] out, rows 16-byte aligned.
+ *   scales : F32 [rows, C/128] out.
+ * The group's payload does not matter. */
+ep_status_t ep_expert_quantize(ep_handle_t handle, const ep_tensor_t *x, ep_tensor_t *q,
+                               ep_tensor_t *scales, ep_stream_t stream);
+
 /* The linear product of every received row: out[r][n] = sum_k x[r][k] w[e][n][k].
  *   x   : BF16 [rows, C] at the dispatch geometry, or FP8_E4M3 [rows, C] with
  *   x_scales : F32 [rows, C/128] (or LL [E, S*T_max, C/128]), contiguous in the

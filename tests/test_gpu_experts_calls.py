@@ -267,6 +267,38 @@ def test_repeated_and_on_another_stream(tokens):
         ep.ep_destroy_handle(h2)
 
 
+@pytest.mark.parametrize("mode,S", [("ht", 2), ("ll", 1), ("ll", 3)])
+def test_quantize_rows(mode, S):
+    """Codes and scales are ep_quantize's bit for bit; rows that hold nothing stay; short tensors are reported."""
+    say(f"quantised rows, {mode} {S}")
+    E, C = 6, 640
+    with Routing(mode, S, 40, E, 2, 256, seed=9) as r, Routing("ht", 1, 1, 1, 1, C, payload="fp8") as f:
+        x = row_tensor(r, C, 2, 3.0, pad=8)
+        x[~r.unused] *= torch.logspace(-30, 20, int((~r.unused).sum()), device="cuda")[:, None]
+        x[r.expert_rows[1][0], 128:256] = 0
+        used = x[~r.unused].contiguous()
+        q0 = torch.empty(used.shape, dtype=FP8, device="cuda")
+        s0 = torch.empty((used.shape[0], C // 128), device="cuda")
+        ep.ep_quantize(f.group, used, q0, s0)
+        q = torch.full((r.rows, C + 16), 7, dtype=torch.uint8, device="cuda").view(FP8)[:, :C]
+        s = torch.full((r.rows, C // 128 + 1), -7.25, device="cuda")[:, :C // 128]
+        ep.ep_expert_quantize(r.handle, x, q, s)
+        assert torch.equal(q[~r.unused].view(torch.uint8), q0.view(torch.uint8)) and torch.equal(s[~r.unused], s0)
+        assert bool((q[r.unused].view(torch.uint8) == 7).all()) and bool((s[r.unused] == -7.25).all())
+        assert ep.ep_get_device_error(r.group) == 0
+        bad = A.EP_ERR_INVALID_ARGUMENT
+        refused(bad, ep.ep_expert_quantize, r.handle, x[:, :C - 64], q[:, :C - 64], s)
+        refused(bad, ep.ep_expert_quantize, r.handle, x, q[:, :C - 128], s)
+        refused(bad, ep.ep_expert_quantize, r.handle, x, q, s[:, :-1])
+        refused(bad, ep.ep_expert_quantize, r.handle, x.float(), q, s)
+        refused(bad, ep.ep_expert_quantize, r.handle, x, q.view(torch.uint8), s)
+        if mode == "ht":
+            ep.ep_expert_quantize(r.handle, x, q[:-1], s)
+            assert ep.ep_get_device_error(r.group) == A.EP_DEVERR_ROW_RANGE
+        else:
+            refused(bad, ep.ep_expert_quantize, r.handle, x, q[:-1], s)
+
+
 def block_reference(r, x, wn, wg, wu, wd, topk, tw, eps=1e-6):
     """The block in 64 bits with gradients: norm, experts, weighted sum, residual, norm."""
     out = []
@@ -398,6 +430,7 @@ def test_decode_step_in_a_graph(form):
         sc = dict(w_gate_scales=torch.full((E, 2, H // 128), 0.01, device="cuda"),
                   w_up_scales=torch.full((E, 2, H // 128), 0.02, device="cuda"))
         wg, wu = (wg / 0.01).clamp(-448, 448).to(FP8), (wu / 0.02).clamp(-448, 448).to(FP8)
+        wd, sd = (wd / 0.01).clamp(-448, 448).to(FP8), torch.full((E, H // 128, I // 128), 0.01, device="cuda")
     x, topk, tw = (torch.empty((n, H), dtype=BF16, device="cuda"), torch.empty((n, K), dtype=torch.int32, device="cuda"),
                    torch.empty((n, K), device="cuda"))
 
@@ -406,7 +439,13 @@ def test_decode_step_in_a_graph(form):
         ep.ep_dispatch(h, x)
         rows = ep.ep_handle_get_buffer(h, A.EP_BUF_LL_RECV)
         ep.ep_expert_gated(h, rows, wg, wu, a, **sc)
-        ep.ep_expert_linear(h, a, wd, y)
+        if form == "fp8":
+            q = torch.zeros((E * S * T, I), dtype=torch.uint8, device="cuda").view(FP8)
+            qs = torch.zeros((E * S * T, I // 128), device="cuda")
+            ep.ep_expert_quantize(h, a, q, qs)
+            ep.ep_expert_linear(h, q, wd, y, x_scales=qs, w_scales=sd)
+        else:
+            ep.ep_expert_linear(h, a, wd, y)
         ep.ep_combine(h, y, tw, out)
         return h
 

@@ -127,5 +127,6 @@ def test_products_reject_what_is_no_handle():
         assert lib.ep_expert_gated(h, _ref(r), _ref(w), _ref(w), None, None, 0, _ref(r), None) == BAD
         assert lib.ep_expert_gated_backward(h, _ref(r), _ref(w), _ref(w), _ref(r), 0, _ref(r), _ref(r), None, None, None,
                                             None) == BAD
+        assert lib.ep_expert_quantize(h, _ref(r), _ref(r), _ref(r), None) == BAD
         assert lib.ep_expert_linear(h, _ref(r), None, _ref(w), None, _ref(r), None) == BAD
         assert lib.ep_expert_linear_backward(h, _ref(r), _ref(w), _ref(r), None, None, None) == BAD
