@@ -565,8 +565,12 @@ ep_status_t ep_dispatch_backward(ep_handle_t handle, const ep_tensor_t *grad_exp
  * Errors of all of them: EP_ERR_INVALID_ARGUMENT (handle, descriptors, shapes,
  * alignment, an unknown activation, or a staged operation pending on the
  * handle); EP_ERR_UNSUPPORTED with the PER_RANK stage 2 (its rows belong to
- * several experts), for sizes above 2^20 and for more tiles than one grid
- * holds (about four million). */
+ * several experts), for sizes above 2^20, for strides that put 256 rows of a
+ * tensor (LL with several sources: the slots of one expert) or of a weight
+ * matrix 2^31 bytes or more apart, and for more tiles than one grid holds
+ * (about four million).  What a call needs of the handle is written by the
+ * handle's own work: calls on one handle from several streams are fine while
+ * no new routing or dispatch of that handle runs beside them. */
 typedef enum {
     EP_ACT_SILU = 0,     /* act(g) = g / (1 + exp(-g))                           */
     EP_ACT_GELU_TANH = 1 /* act(g) = g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
@@ -616,7 +620,7 @@ ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_t *rows
  *   x      : BF16 [rows, C] at the dispatch geometry, C a multiple of 128.
  *   q      : FP8_E4M3 [rows, C] out, rows 16-byte aligned.
  *   scales : F32 [rows, C/128] out.
- * The group's payload does not matter. */
+ * The group's payload does not matter.  Short tensors as for the products. */
 ep_status_t ep_expert_quantize(ep_handle_t handle, const ep_tensor_t *x, ep_tensor_t *q,
                                ep_tensor_t *scales, ep_stream_t stream);
 
