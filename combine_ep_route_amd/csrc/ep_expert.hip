@@ -83,6 +83,14 @@ struct AlongSrc {
   __device__ __forceinline__ int scale() const { return inside ? offs : kOutside; }
 };
 
+// Rounded to bf16: the results, and of kGatedGrad the gradients of both products, which are operands of the
+// matrix unit next; all else stays fp32.
+// Measured, 256 experts of 7168 x 2048:
+//   32768 rows, none to several hundred an expert: gated bf16 2.36 ms, 815 TFLOP/s, 11.1 GB read beyond the L2 (8.1
+//   needed: an expert's row tiles drift apart); gated FP8 1.36 ms, 1410 TFLOP/s; linear bf16 1.23 ms, 780 TFLOP/s.
+//   Half of the tiles hold less than half of their rows: the weights' bytes and the products bound them in turn.
+//   4 rows each, FP8: gated 1.19 ms, 6.3 TB/s, bound by the weights' bytes.  Two workgroups a CU need
+//   FP8 stages of 21 KiB, three each: linear of 8 rows each in 64 experts 170 us so, 200 with one and four stages.
 template <class C, int KIND, int ACT>
 __global__ __launch_bounds__(C::NT) void along_kernel(AlongArgs a) {
   constexpr bool GATED = KIND != kLinear;
@@ -99,7 +107,7 @@ __global__ __launch_bounds__(C::NT) void along_kernel(AlongArgs a) {
   C::run(One<AlongSrc<C, GATED>>{src}, static_cast<int>((a.k_bytes + C::PIECE - 1) / C::PIECE), s.count - m0, acc);
 
   constexpr int CF = GATED ? C::FA / 2 : C::FA;
-  const int l = lane_id(), first = n0 + (wave_id() % C::WA) * src.wave_span_a();   // the wave's first column
+  const int first = n0 + (wave_id() % C::WA) * src.wave_span_a();   // the wave's first column
   const int bytes = (a.N - first) * 2;
   auto row = [&](int r) {
     const int p = m0 + C::wave_row(r);
@@ -111,19 +119,7 @@ __global__ __launch_bounds__(C::NT) void along_kernel(AlongArgs a) {
       const int64_t at = row(r);
       return at < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.grad + at * a.ld_grad + first);
     };
-    if constexpr (C::kThroughLds) {
-      C::template load_rows<CF>(d, bytes, grad_row);
-    } else {
-#pragma unroll
-      for (int j = 0; j < C::FB; ++j) {
-        const uint8_t* from = grad_row(j * 16 + (l & 15));
-#pragma unroll
-        for (int i = 0; i < CF; ++i) {
-          const int byte = (i * 16 + (l >> 4) * 4) * 2;
-          d[i][j] = from && byte < bytes ? *reinterpret_cast<const uint2*>(from + byte) : uint2{0, 0};
-        }
-      }
-    }
+    C::template load_rows<CF>(d, bytes, grad_row);
 #pragma unroll
     for (int i = 0; i < CF; ++i)
 #pragma unroll
@@ -157,19 +153,7 @@ __global__ __launch_bounds__(C::NT) void along_kernel(AlongArgs a) {
       const int64_t at = row(r);
       return at < 0 ? nullptr : reinterpret_cast<uint8_t*>(a.out[o] + at * a.ld_out[o] + first);
     };
-    if constexpr (C::kThroughLds) {
-      C::template store_rows<CF, 2>(acc, o * CF, bytes, out_row);
-    } else {
-#pragma unroll
-      for (int j = 0; j < C::FB; ++j) {
-        uint8_t* to = out_row(j * 16 + (l & 15));
-#pragma unroll
-        for (int i = 0; i < CF; ++i) {
-          const int byte = (i * 16 + (l >> 4) * 4) * 2;
-          if (to && byte < bytes) *reinterpret_cast<uint2*>(to + byte) = bf16x4(acc[o * CF + i][j]);
-        }
-      }
-    }
+    C::template store_rows<CF, 2>(acc, o * CF, bytes, out_row);
   }
 }
 
@@ -226,6 +210,10 @@ struct RowGradPlan {
   __device__ __forceinline__ RowGradSrc<C> source(int p) const { return RowGradSrc<C>(g, s, n0, m0, p); }
 };
 
+// The parts are summed in the same registers: one rounding, one write.  Two waves a SIMD at least: without the
+// bound the compiler takes over 256 registers where four waves make a workgroup.
+// 64 experts of 7168 x 2048, 512 rows each: gated 2.1 ms, 910 TFLOP/s; one part, 256 rows each: 0.82 ms, of which
+// the weights' 1.9 GB alone take 0.31.  Bound by the matrix unit (59% busy) and by the loads of its tiles.
 template <class C>
 __global__ __launch_bounds__(C::NT, 2) void row_grad_kernel(RowGradArgs g) {
   const int col_tiles = (g.N + C::BA - 1) / C::BA;
@@ -250,8 +238,8 @@ __global__ __launch_bounds__(C::NT, 2) void row_grad_kernel(RowGradArgs g) {
 // Gradient of the weights: dw[e][i][h] = sum over the expert's rows r of dy[r][i] x[r][h]
 // ---------------------------------------------------------------------------
 
-// LIST: the rows are looked up step by step (LL, several sources); else they follow each other.  Rows past the
-// expert's last one are zeros in both operands.
+// LIST: the rows are looked up step by step (an expert's rows in several runs: LL, several sources); else they
+// follow each other.  Rows past the expert's last one are zeros in both operands.
 template <class C, bool LIST>
 struct WeightGradSrc {
   const WeightGradArgs& g;
@@ -309,6 +297,13 @@ struct WeightGradSrc {
   __device__ __forceinline__ int b(int j) const { return offb[j]; }
 };
 
+// An expert without rows gets zeros.  Both operands lie across the contraction: they reach the matrix unit by
+// transposing LDS reads.
+// 64 experts of 7168 x 2048: bf16, 512 rows each, both gated gradients 2.5 ms, 760 TFLOP/s; F32, 256 rows each,
+// 1.2 ms, 3.7 TB/s of 4.5 GB.  The contraction is short (8 to 16 steps), so a tile's first loads and its stores,
+// 256 KiB in F32, are not covered by products: two workgroups a CU of 256 x 128 or 128 x 128 would cover them, but take
+// more loads and lose more (1.9 and 2.2 ms of the whole backward where this takes 1.7).  Another order of the
+// tiles that reads a quarter of the bytes beyond the L2 changes nothing.
 template <class C, bool F32, bool LIST>
 __global__ __launch_bounds__(C::NT, 2) void weight_grad_kernel(WeightGradArgs g) {
   const int ht = (g.H + C::BA - 1) / C::BA, it = (g.I + C::BB - 1) / C::BB;
@@ -337,7 +332,8 @@ __global__ __launch_bounds__(C::NT, 2) void weight_grad_kernel(WeightGradArgs g)
 // ---------------------------------------------------------------------------
 
 // One workgroup per expert: its rows (e*S + s)*T_max + slot for all sources in order, at the sum of the
-// counts before it.  Each workgroup sums those counts itself: E*S of them at most, from the L2.
+// counts before it.  Each workgroup sums those counts itself: E*S of them at most, from the L2.  64 experts with 4
+// sources: 3 us, the launch.
 __global__ __launch_bounds__(256) void list_rows_kernel(const int32_t* counts, int S, int slots, int32_t* total,
                                                         int32_t* list) {
   __shared__ int part[4];
@@ -384,7 +380,17 @@ hipError_t launch_along_as(const AlongArgs& a, hipStream_t stream, bool check) {
 }
 
 // Which tile a product over the rows takes, by the average rows of an expert (the counts themselves are only
-// on the device) and by how many 256 x 256 tiles there are for the 256 CUs.
+// on the device) and by how many 256 x 256 tiles there are for the 256 CUs.  Measured, 64 experts of 2048 x 1408,
+// gated, us:
+//   rows an expert   bf16: small  middle  big    FP8: small  middle  big
+//         32               147     158     -           102     85     -
+//         48                -      148    178            -     90    101
+//         96                -      164    181            -    107    112
+//        384                -      401    345            -    277    242
+// From 24 rows on the small tile's 32 rows are often two tiles, which read the weights twice.  Rows spread over
+// the experts as a router leaves them make many tiles of the average's multiple: at 128 rows on average (256
+// experts of 7168 x 2048, bf16) the big tile takes 2.35 ms, the middle one 2.67.
+// Few big tiles leave CUs idle: 88 of them (8 experts, 256 rows each) take 48 us, middle ones 37.
 enum Size { kSmall, kMiddle, kBig };
 Size tile_size(const ExpertRows& r, int64_t rows, int64_t col_tiles) {
   const int64_t each = rows / r.E;
@@ -468,6 +474,9 @@ hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check)
   }
 }
 
+// With fewer than two 256 x 256 tiles a CU the smaller ones fill the chip: the whole linear backward of 8 experts
+// of 1024 x 768 takes 63 us with them, 103 with big ones; with 2816 tiles (64 experts of 2048 x 1408) the gated
+// backward of 24 rows each takes 494 us with big ones, 553 with small.
 hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check) {
   if (static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + 255) / 256) * ((g.I + 255) / 256) < 512)
     return launch_weight_grad_as<Core<128, 128, 2, 2, true, true, false, 4, 64>>(g, f32, stream, check);

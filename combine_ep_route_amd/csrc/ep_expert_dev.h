@@ -1,6 +1,15 @@
 // Device core of the experts' products: LDS-tiled matrix products on the matrix unit, fed by loads
 // that go from global memory to LDS without passing registers.
 //
+// What bounds it: with many rows an expert, the matrix unit's power and the loads in turn.  A dense product
+// (64 experts of 7168 x 2048, 512 rows each, bf16) runs at 1110 to 1125 TFLOP/s (a plain library product of its
+// size: 1440), the same product of zeros, which draws less power, at 1304; the clock falls to about 1.6 GHz
+// under it.  A workgroup's tile of 256 x 256 takes 32 KiB from the L2 for each 32 contracted bf16 values, half
+// of what tiles of 128 x 128 take; the L2 gives a CU 64 bytes a cycle.  With few rows an expert the weights'
+// bytes bound it (6.3 TB/s reached of 6.1 to 6.8 for pure reads and writes of large arrays).
+// Tried, without gain: five stages of 64 bytes, prefetches three and four steps ahead, 32 x 32 x 16
+// instructions, waves of 128 x 128, two workgroups of 256 x 128 a CU, waves' priorities.
+//
 // A step of the contraction brings one tile of each operand to LDS, whatever its type and direction:
 //   "along" operands are contiguous in the contracted index: PIECE bytes of each output row or column
 //   (64 bytes: 32 bf16 values; 128: 64 bf16 or 128 FP8 values);
@@ -236,7 +245,7 @@ struct Core {
   static_assert(TA % 16 == 0 && TB % 16 == 0, "whole fragments");
   static_assert(PIECE == 64 || PIECE == 128, "32 or 64 contracted bf16 values");
   static_assert(!F8 || (!ANC && !BNC && PIECE == 128 && WS + 128 <= NT), "FP8 operands lie along");
-  static_assert(ST >= 2 && ST <= 5 && (JA + JB + 1) * (ST - 1) < 64, "the wait counts at most 63 loads");
+  static_assert(ST >= 2 && ST <= 4 && (JA + JB + 1) * (ST - 1) < 64, "the wait counts at most 63 loads");
 
   typedef f32x4 Acc[FA][FB];
 
@@ -254,10 +263,6 @@ struct Core {
   }
   static __device__ __forceinline__ uint8_t* stage3() {
     __shared__ __attribute__((aligned(1024))) uint8_t s[ST > 3 ? STAGE : 16];
-    return s;
-  }
-  static __device__ __forceinline__ uint8_t* stage4() {
-    __shared__ __attribute__((aligned(1024))) uint8_t s[ST > 4 ? STAGE : 16];
     return s;
   }
 
@@ -482,15 +487,14 @@ struct Core {
   // loads are started past the last step too, which sources answer with zeros, and waited for at the end.
   template <int NJ, class Src>
   static __device__ __forceinline__ void run_part(Src& src, int steps, Acc& acc, uint8_t* s0, uint8_t* s1, uint8_t* s2,
-                                                  uint8_t* s3, uint8_t* s4) {
+                                                  uint8_t* s3) {
     const int fa = (wave_id() % WA) * Src::wave_span_a();
     constexpr bool PIPED = !F8 && FA >= 4;
-    uint8_t* const last = ST == 2 ? s1 : ST == 3 ? s2 : ST == 4 ? s3 : s4;
+    uint8_t* const last = ST == 2 ? s1 : ST == 3 ? s2 : s3;
     int t = 0;
     issue<NJ>(src, s0);
     if constexpr (ST > 2) issue<NJ>(src, s1);
     if constexpr (ST > 3) issue<NJ>(src, s2);
-    if constexpr (ST > 4) issue<NJ>(src, s3);
     if constexpr (PIPED) {
       i32x4 b[NJ], a[2];
       src.step();
@@ -505,25 +509,21 @@ struct Core {
         piped_step<NJ>(src, last, s0, s1, acc, fa, b, a);
         piped_step<NJ>(src, s0, s1, ST == 2 ? s0 : s2, acc, fa, b, a);
         if constexpr (ST > 2) piped_step<NJ>(src, s1, s2, ST == 3 ? s0 : s3, acc, fa, b, a);
-        if constexpr (ST > 3) piped_step<NJ>(src, s2, s3, ST == 4 ? s0 : s4, acc, fa, b, a);
-        if constexpr (ST > 4) piped_step<NJ>(src, s3, s4, s0, acc, fa, b, a);
+        if constexpr (ST > 3) piped_step<NJ>(src, s2, s3, s0, acc, fa, b, a);
       }
       if (t < steps) piped_step<NJ>(src, last, s0, s1, acc, fa, b, a);
       if (ST > 2 && t + 1 < steps) piped_step<NJ>(src, s0, s1, s2, acc, fa, b, a);
       if (ST > 3 && t + 2 < steps) piped_step<NJ>(src, s1, s2, s3, acc, fa, b, a);
-      if (ST > 4 && t + 3 < steps) piped_step<NJ>(src, s2, s3, s4, acc, fa, b, a);
     } else {
       for (; t + ST <= steps; t += ST) {
         ring_step<NJ>(src, s0, last, acc, fa);
         ring_step<NJ>(src, s1, s0, acc, fa);
         if constexpr (ST > 2) ring_step<NJ>(src, s2, s1, acc, fa);
         if constexpr (ST > 3) ring_step<NJ>(src, s3, s2, acc, fa);
-        if constexpr (ST > 4) ring_step<NJ>(src, s4, s3, acc, fa);
       }
       if (t < steps) ring_step<NJ>(src, s0, last, acc, fa);
       if (ST > 2 && t + 1 < steps) ring_step<NJ>(src, s1, s0, acc, fa);
       if (ST > 3 && t + 2 < steps) ring_step<NJ>(src, s2, s1, acc, fa);
-      if (ST > 4 && t + 3 < steps) ring_step<NJ>(src, s3, s2, acc, fa);
     }
     // no load into LDS may outlive the workgroup, and the next part starts with all stages free
     wait_and_meet<0>();
@@ -537,12 +537,11 @@ struct Core {
     uint8_t* const s1 = stage1();
     uint8_t* const s2 = stage2();
     uint8_t* const s3 = stage3();
-    uint8_t* const s4 = stage4();
     if (steps <= 0) return;
     auto all = [&](auto nj) {
       for (int p = 0; p < plan.parts(); ++p) {
         auto src = plan.source(p);
-        run_part<decltype(nj)::value>(src, steps, acc, s0, s1, s2, s3, s4);
+        run_part<decltype(nj)::value>(src, steps, acc, s0, s1, s2, s3);
       }
     };
     constexpr int Q = FB >= 4 ? FB / 4 : 1;   // the loop exists for one to four quarters of the fragments
@@ -556,11 +555,12 @@ struct Core {
   // -------------------------------------------------------------------------
   // A wave's part of the results between its registers and rows in memory
   // -------------------------------------------------------------------------
-  // A lane holds four columns of 16 rows' fragments: stored as they lie, 32 bytes of a row at a time.  Through
-  // LDS (the stages are free behind run()) whole rows of the wave's CF*16 columns are moved, 16 bytes a lane.
+  // A lane holds four columns of 16 rows' fragments: stored as they lie, 32 bytes of a row at a time.  Instead
+  // they go through LDS (the stages are free behind run()): whole rows of the wave's CF*16 columns, 16 bytes a
+  // lane.  64 experts of 2048 x 7168, 512 rows each, gated backward: 7.05 ms with stores as they lie, 6.52 so.
   // Each wave has kRegion bytes of its own; a row's 16-byte pieces are spread over the banks by the row.
   static constexpr int kRegion = 2 * (STAGE - SCALES) / NW / 1024 * 1024;
-  static constexpr bool kThroughLds = kRegion >= 8192;
+  static_assert(kRegion >= 8192, "16 rows of 128 fp32 values");
   static __device__ __forceinline__ uint8_t* region() {
     const int w = wave_id();
     return (w < NW / 2 ? stage0() : stage1()) + w % (NW / 2) * kRegion;
