@@ -300,10 +300,11 @@ struct WeightGradSrc {
 // An expert without rows gets zeros.  Both operands lie across the contraction: they reach the matrix unit by
 // transposing LDS reads.
 // 64 experts of 7168 x 2048: bf16, 512 rows each, both gated gradients 2.5 ms, 760 TFLOP/s; F32, 256 rows each,
-// 1.2 ms, 3.7 TB/s of 4.5 GB.  The contraction is short (8 to 16 steps), so a tile's first loads and its stores,
-// 256 KiB in F32, are not covered by products: two workgroups a CU of 256 x 128 or 128 x 128 would cover them, but take
-// more loads and lose more (1.9 and 2.2 ms of the whole backward where this takes 1.7).  Another order of the
-// tiles that reads a quarter of the bytes beyond the L2 changes nothing.
+// 1.1 ms, 3.5 TB/s written.  The two bounds add up: the stores of a tile (256 KiB in F32; without rows 0.62 ms in
+// all, 6.0 TB/s) and the short contraction (256 rows more: 0.335 ms, the library's 1440 TFLOP/s).  Two workgroups
+// a CU of 256 x 128 or 128 x 128 gain no overlap and take more loads (a linear backward of 1.7 ms takes 1.9 and
+// 2.2), nor do staggered starts.  Another order of the tiles that reads a quarter of the bytes beyond the L2
+// changes nothing.
 template <class C, bool F32, bool LIST>
 __global__ __launch_bounds__(C::NT, 2) void weight_grad_kernel(WeightGradArgs g) {
   const int ht = (g.H + C::BA - 1) / C::BA, it = (g.I + C::BB - 1) / C::BB;
