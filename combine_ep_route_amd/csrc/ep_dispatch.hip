@@ -526,24 +526,59 @@ __global__ __launch_bounds__(256) void dispatch_kernel(DispatchArgs p, int W_) {
 // A3 on its own, for callers that keep FP8 tokens and dispatch them
 // pre-quantised: the same chunk mapping and quantize() as the dispatch, so
 // the codes and scales are the ones the dispatch would write.  Codes go out as 16-byte stores; each
-// block's scale is stored by the first lane of its 8.  With a row map (MAP) the rows are the ones its a.n entries
-// name: 65536 rows of 2048 in 76 us, 5.4 TB/s, bound by memory; 1024 in 4.4 us.
-template <int NV, bool MAP>
+// block's scale is stored by the first lane of its 8.
+//
+// kFirst and kEntries take the experts' rows that hold a message, found from what the handle's creation has written,
+// so that a call depends on no other one.  HT: they are the first ones; every wave adds up the experts' counts.
+// LL: entry by entry, its tile's prefix and its rank in the tile, one round trip more than a map of them would take.
+// Rows of 2048, bound by memory: HT 65536 in 64 us, 6.3 TB/s, 1024 in 4.1 us; LL 65536 in 75 us, 1024 in 4.3 us
+// (by a map 62, 4.0, 74 and 4.1 us).  The tile's whole prefix loaded ahead of the entry's expert: LL 80 and 4.5 us.
+enum QuantRows { kAll, kFirst, kEntries };
+
+// The counts' sum.
+__device__ __forceinline__ int64_t rows_in_use(const QuantArgs& a) {
+  int sum = 0;
+  const int lane = threadIdx.x & 63;
+  for (int e0 = 0; e0 < a.E; e0 += 256) {
+#pragma unroll
+    for (int e = 0; e < 256; e += 64) sum += e0 + e + lane < a.E ? a.count[e0 + e + lane] : 0;
+  }
+  // over the lanes: rows of 16 lanes, then the rows
+  sum += __builtin_amdgcn_update_dpp(0, sum, 0x111, 0xf, 0xf, false);
+  sum += __builtin_amdgcn_update_dpp(0, sum, 0x112, 0xf, 0xf, false);
+  sum += __builtin_amdgcn_update_dpp(0, sum, 0x114, 0xf, 0xf, false);
+  sum += __builtin_amdgcn_update_dpp(0, sum, 0x118, 0xf, 0xf, false);
+  sum += __builtin_amdgcn_update_dpp(0, sum, 0x142, 0xa, 0xf, false);
+  sum += __builtin_amdgcn_update_dpp(0, sum, 0x143, 0xc, 0xf, false);
+  return __builtin_amdgcn_readlane(sum, 63);
+}
+
+template <int NV, int ROWS>
 __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a, int W) {
   const int lane = threadIdx.x & 63;
   const int C = a.H / 16;
   const int64_t waves = static_cast<int64_t>(gridDim.x) * 4;
-  const int64_t total = a.n * W;
-  for (int64_t gw = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); gw < total; gw += waves) {
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t total = a.n * W;
+  if constexpr (ROWS == kFirst) {
+    int64_t n = rows_in_use(a);
+    if (n > a.rows) {
+      n = a.rows;
+      if (first == 0 && lane == 0) atomicOr(a.err, EP_DEVERR_ROW_RANGE);
+    }
+    total = n * W;
+  }
+  for (int64_t gw = first; gw < total; gw += waves) {
     int64_t i = gw / W;
     const int part = static_cast<int>(gw - i * W);
-    if constexpr (MAP) {
-      i = a.map[i];
-      if (i < 0) continue;
-      if (i >= a.rows) {
-        if (lane == 0 && part == 0) atomicOr(a.err, EP_DEVERR_ROW_RANGE);
-        continue;
-      }
+    if constexpr (ROWS == kEntries) {
+      const uint32_t token = static_cast<uint32_t>(i) / static_cast<uint32_t>(a.K);
+      const uint32_t s = token / static_cast<uint32_t>(a.T), t = token - s * static_cast<uint32_t>(a.T);
+      const int e = a.topk[i], rank = a.rank_e[i];
+      if (rank < 0 || static_cast<uint32_t>(e) >= static_cast<uint32_t>(a.E)) continue;
+      const int at = a.hist_e[(static_cast<int64_t>(s) * a.tps + t / kTile) * a.E + e] + rank;
+      if (static_cast<uint32_t>(at) >= static_cast<uint32_t>(a.slots)) continue;
+      i = (static_cast<int64_t>(e) * a.S + s) * a.slots + at;
     }
     const int c0 = part * NV * 64 + lane;
     Raw raw[NV];
@@ -610,8 +645,9 @@ hipError_t launch_quantize(const QuantArgs& a, hipStream_t stream) {
   int64_t blocks = (a.n * W + 3) / 4;
   if (blocks > 0x7FFFFFFF) blocks = 0x7FFFFFFF;
   const dim3 grid(static_cast<unsigned>(blocks)), block(256);
-  if (a.map) quantize_kernel<kChunksPerLane, true><<<grid, block, 0, stream>>>(a, W);
-  else quantize_kernel<kChunksPerLane, false><<<grid, block, 0, stream>>>(a, W);
+  if (a.count) quantize_kernel<kChunksPerLane, kFirst><<<grid, block, 0, stream>>>(a, W);
+  else if (a.topk) quantize_kernel<kChunksPerLane, kEntries><<<grid, block, 0, stream>>>(a, W);
+  else quantize_kernel<kChunksPerLane, kAll><<<grid, block, 0, stream>>>(a, W);
   return hipGetLastError();
 }
 

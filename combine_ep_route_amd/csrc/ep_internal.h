@@ -263,8 +263,12 @@ struct QuantArgs {
   int64_t ld_s;           // elements
   int64_t n;
   int H;
-  // With a row map (null: rows 0 .. n-1): n entries that name a row or -1; rows beyond `rows` are reported.
-  const int32_t* map;
+  // Of the experts' rows those that hold a message, from what a handle's creation has written:
+  //   count (HT): the first ones, as many as the E counts' sum, n at most; those beyond `rows` are reported.
+  //   topk, rank_e, hist_e (LL): the slots of the n entries, as the dispatch works them out.
+  const int32_t* count;
+  const int32_t *topk, *rank_e, *hist_e;
+  int32_t E, K, S, T, tps, slots;
   int64_t rows;
   int32_t* err;
 };

@@ -1404,7 +1404,6 @@ EP_API ep_status_t ep_expert_quantize(ep_handle_t handle, const ep_tensor_t* x_i
   const hipStream_t s = as_stream(stream);
   if (const ep_status_t st = ensure_device(g, s); st != EP_OK) return st;
   h->stream = s;
-  if (const ep_status_t st = ensure_maps(h, s); st != EP_OK) return st;
   QuantArgs a{};
   a.x = static_cast<const uint16_t*>(x.data);
   a.ld_x = x.strides[0];
@@ -1412,9 +1411,22 @@ EP_API ep_status_t ep_expert_quantize(ep_handle_t handle, const ep_tensor_t* x_i
   a.ld_q = qd.strides[0];
   a.scales = static_cast<float*>(sd.data);
   a.ld_s = sd.strides[0];
+  // The rows in use follow from what the handle's creation has written; the maps may not have been.
   a.n = h->n * g->cfg.top_k;
+  a.E = g->cfg.num_experts;
+  if (g->cfg.mode == EP_MODE_LL) {
+    a.topk = h->topk;
+    a.rank_e = h->rank_e;
+    a.hist_e = h->hist_e;
+    a.K = g->cfg.top_k;
+    a.S = g->cfg.num_src_ranks;
+    a.T = h->T;
+    a.tps = h->tps;
+    a.slots = g->cfg.max_tokens_per_rank;
+  } else {
+    a.count = h->c2;
+  }
   a.H = static_cast<int>(C);
-  a.map = g->cfg.mode == EP_MODE_LL ? h->slot_map : h->row2;
   a.rows = std::min({x.sizes[0], qd.sizes[0], sd.sizes[0]});
   a.err = g->err;
   const ep_status_t st = from_hip(launch_quantize(a, s));

@@ -615,8 +615,7 @@ ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_t *rows
 
 /* FP8 quantisation of the experts' rows, for an FP8 product behind ep_expert_gated:
  * every row that holds a message, with ep_quantize's arithmetic (scale = amax/448
- * per 128 elements, codes the nearest-even, saturating E4M3 of x/scale).  Needs
- * the handle's row map (written by its dispatch, or computed on first use).
+ * per 128 elements, codes the nearest-even, saturating E4M3 of x/scale).
  *   x      : BF16 [rows, C] at the dispatch geometry, C a multiple of 128.
  *   q      : FP8_E4M3 [rows, C] out, rows 16-byte aligned.
  *   scales : F32 [rows, C/128] out.
