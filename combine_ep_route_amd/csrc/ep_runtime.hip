@@ -239,14 +239,21 @@ bool expert_rows(const Group* g, const ep_tensor_t* t, ep_tensor_t* out) {
 }
 
 // Make sure the slot / row maps and the HT key offsets exist (dispatch
-// writes them; without a dispatch, a maps-only pass computes them).
+// writes them; without a dispatch, a maps-only pass computes them).  A pass
+// that is captured runs when its graph is replayed: until an eager one or a
+// dispatch has written the maps, every call brings its own.
 ep_status_t ensure_maps(Handle* h, hipStream_t stream) {
   if (h->maps_ready) return EP_OK;
+  hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(stream, &capture) != hipSuccess) {
+    (void)hipGetLastError();
+    capture = hipStreamCaptureStatusNone;
+  }
   DispatchArgs p = dispatch_base(h);
   p.payload = 0;
   p.max_blocks = 0;
   const ep_status_t st = from_hip(launch_dispatch(p, stream));
-  if (st == EP_OK) h->maps_ready = true;
+  if (st == EP_OK && capture == hipStreamCaptureStatusNone) h->maps_ready = true;
   return st;
 }
 

@@ -282,7 +282,10 @@ typedef enum {
 /* The counts are written when the handle is made.  The slot / row maps and
  * the HT offsets are written by the handle's dispatch; asked for before a
  * dispatch has run, they are computed by a maps-only pass that this call
- * enqueues on the handle's stream (no rows are written). */
+ * enqueues on the handle's stream (no rows are written).  The same pass goes
+ * before the combine or an adjoint of a handle without a dispatch; in a call
+ * that is captured it becomes part of the graph, and calls outside of the
+ * graph do not rely on it. */
 ep_status_t ep_handle_get_map(ep_handle_t handle, int32_t which, ep_tensor_t *view);
 
 /* The handle's maps and counts without a group and without allocating:
