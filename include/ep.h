@@ -22,7 +22,9 @@
  *    ep_stream_t, i.e. a hipStream_t; NULL is the default stream) and returns
  *    without waiting, except the functions documented as blocking.
  *  - A group, and every handle made from it, is used from one stream at a
- *    time; the library takes no locks.
+ *    time, except where a function says otherwise (the experts' products and
+ *    ep_expert_quantize); the library takes no locks, so host threads that
+ *    share a group take turns.
  *  - Arguments are validated on the host before any HIP call; a rejected call
  *    enqueues nothing.  Routing entries are checked on the device and
  *    reported through the group's device error word (ep_get_device_error).
@@ -571,9 +573,10 @@ ep_status_t ep_dispatch_backward(ep_handle_t handle, const ep_tensor_t *grad_exp
  * several experts), for sizes above 2^20, for strides that put 256 rows of a
  * tensor (LL with several sources: the slots of one expert) or of a weight
  * matrix 2^31 bytes or more apart, and for more tiles than one grid holds
- * (about four million).  What a call needs of the handle is written by the
- * handle's own work: calls on one handle from several streams are fine while
- * no new routing or dispatch of that handle runs beside them. */
+ * (about four million).  What a call needs of the handle is written when the
+ * handle is made: once that work has run, calls on one handle may run on
+ * several streams at the same time, each with outputs of its own.  The handle's
+ * destruction, and a new handle in its place, wait for them. */
 typedef enum {
     EP_ACT_SILU = 0,     /* act(g) = g / (1 + exp(-g))                           */
     EP_ACT_GELU_TANH = 1 /* act(g) = g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
