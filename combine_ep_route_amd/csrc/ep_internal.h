@@ -140,8 +140,8 @@ struct Handle {
   int32_t* off1 = nullptr;       // HT [R]
   int32_t* c2 = nullptr;         // HT [E]
   int32_t* off2 = nullptr;       // HT [E]
-  int32_t* rows_total = nullptr; // LL, several sources [E]: rows per expert, for the experts' products
-  int32_t* rows_list = nullptr;  // LL, several sources [n_max * K]: their message indices, expert after expert
+  int32_t* rows_total = nullptr; // LL, many sources or runs [E]: rows per expert, for the experts' products
+  int32_t* rows_list = nullptr;  // the same [n_max * K]: their message indices, expert after expert
   int32_t* hist_e = nullptr;     // [tiles_max, E] tile counts -> prefixes
   int32_t* hist_n = nullptr;     // [tiles_max, N]
   int buf_half = -1;             // receive buffer / stage set of the last dispatch

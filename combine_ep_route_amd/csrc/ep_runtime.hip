@@ -238,6 +238,17 @@ bool expert_rows(const Group* g, const ep_tensor_t* t, ep_tensor_t* out) {
   return geometry_rows(g, t, EP_DTYPE_BF16, g->cfg.hidden, EP_TAG_TOKENS, true, out);
 }
 
+// Whether the experts' products read their rows from a list (LL, several
+// sources).  Few sources and experts: they look rows up in the counts
+// themselves, a launch less (4 x 32 tokens, 16 experts: 13.4 us with the list,
+// 9.6 us without).  Else the rows come from a list made once a call: where
+// many workgroups look up, a list read costs less (4 x 16 tokens, 64 experts:
+// 190 us with it, 200 us without).
+bool makes_list(const ep_config_t& cfg) {
+  const int S = cfg.num_src_ranks;
+  return cfg.mode == EP_MODE_LL && S > 1 && (S > expert::kFewSources || S * cfg.num_experts > 128);
+}
+
 // Make sure the slot / row maps and the HT key offsets exist (dispatch
 // writes them; without a dispatch, a maps-only pass computes them).  A pass
 // that is captured runs when its graph is replayed: until an eager one or a
@@ -426,7 +437,7 @@ EP_API ep_status_t ep_create_group(const ep_config_t* cfg_in, ep_stream_t stream
     size_t bytes = align_up(nm * K * 4) * 2 + align_up(nm * N * 4);   // topk copy, ranks
     if (cfg.mode == EP_MODE_LL) {
       bytes += align_up(nm * K * 4) + align_up(static_cast<size_t>(E) * S * 4);
-      if (S > 1) bytes += align_up(E * 4) + align_up(nm * K * 4);   // rows per expert and their list
+      if (makes_list(cfg)) bytes += align_up(E * 4) + align_up(nm * K * 4);   // rows per expert and their list
     } else {
       bytes += align_up(nm * N * 4) + align_up(nm * K * 4) + align_up(R * 4) * 2 + align_up(E * 4) * 2;
     }
@@ -444,7 +455,7 @@ EP_API ep_status_t ep_create_group(const ep_config_t* cfg_in, ep_stream_t stream
     if (cfg.mode == EP_MODE_LL) {
       h->slot_map = cv.take<int32_t>(nm * K);
       h->ll_count = cv.take<int32_t>(static_cast<size_t>(E) * S);
-      if (S > 1) {
+      if (makes_list(cfg)) {
         h->rows_total = cv.take<int32_t>(E);
         h->rows_list = cv.take<int32_t>(nm * K);
       }
@@ -1168,14 +1179,6 @@ ep_status_t expert_ready(const Handle* h) {
   return h->pend == Handle::kPendNone ? EP_OK : EP_ERR_INVALID_ARGUMENT;
 }
 
-// Few sources and experts: the products look rows up in the counts themselves, a launch less (4 x 32 tokens,
-// 16 experts: 13.4 us with the list, 9.6 us without).  Else the rows come from a list made once a call: where
-// many workgroups look up, a list read costs less (4 x 16 tokens, 64 experts: 190 us with it, 200 us without).
-bool makes_list(const Group* g) {
-  const int S = g->cfg.num_src_ranks;
-  return g->cfg.mode == EP_MODE_LL && S > 1 && (S > expert::kFewSources || S * g->cfg.num_experts > 128);
-}
-
 ExpertRows rows_of_experts(const Handle* h, int64_t limit) {
   const Group* g = h->g;
   ExpertRows r{};
@@ -1187,7 +1190,7 @@ ExpertRows rows_of_experts(const Handle* h, int64_t limit) {
   if (g->cfg.mode == EP_MODE_LL) {
     r.stride = g->cfg.num_src_ranks * g->cfg.max_tokens_per_rank;
     r.slots = g->cfg.max_tokens_per_rank;
-    if (makes_list(g)) {
+    if (makes_list(g->cfg)) {
       r.count = h->rows_total;
       r.list = h->rows_list;
     } else {
@@ -1205,7 +1208,7 @@ ep_status_t start_products(Handle* h, hipStream_t s) {
   Group* g = h->g;
   if (const ep_status_t st = ensure_device(g, s); st != EP_OK) return st;
   h->stream = s;
-  if (makes_list(g))
+  if (makes_list(g->cfg))
     EP_HIP(expert::launch_list_rows(h->ll_count, g->cfg.num_experts, g->cfg.num_src_ranks,
                                     g->cfg.max_tokens_per_rank, h->rows_total, h->rows_list, s));
   return EP_OK;
