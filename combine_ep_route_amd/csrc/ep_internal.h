@@ -22,6 +22,12 @@ constexpr int kMaxRanks = 1024;
 constexpr int kMaxHidden = 16384;
 constexpr int kLayoutTile = 16;    // tokens per layout tile (one workgroup of the count kernel)
 
+// Workgroups of `threads` that one launch takes of `blocks`: a grid dimension counts its threads in 32 bits.
+inline unsigned grid_blocks(int64_t blocks, int threads) {
+  const int64_t most = UINT32_MAX / static_cast<uint32_t>(threads);
+  return static_cast<unsigned>(blocks < most ? blocks : most);
+}
+
 constexpr uint32_t kGroupMagic = 0x45504752u;   // "EPGR"
 constexpr uint32_t kHandleMagic = 0x4550484Eu;  // "EPHN"
 constexpr uint32_t kDeadMagic = 0xDEADDEADu;

@@ -350,12 +350,22 @@ int grad_blocks(int64_t n, int H) {
   return static_cast<int>(std::min(n, std::max<int64_t>(kNormCus, std::min(fit, n / 8))));
 }
 
-hipError_t launch_residual_norm(const NormArgs& a, hipStream_t s) {
-  if (a.n == 0) return hipSuccess;
-  const int gate = !a.gate ? kNone : a.gate_rows ? kToken : kChannel;
-  if (pieces(a.H) == 1) a.w_post ? run_forward<1, true>(a, gate, s) : run_forward<1, false>(a, gate, s);
-  else a.w_post ? run_forward<2, true>(a, gate, s) : run_forward<2, false>(a, gate, s);
-  return hipGetLastError();
+// One workgroup a row: more rows than a grid holds take several launches.
+hipError_t launch_residual_norm(const NormArgs& args, hipStream_t s) {
+  const int gate = !args.gate ? kNone : args.gate_rows ? kToken : kChannel;
+  NormArgs a = args;
+  for (int64_t left = args.n; left > 0; left -= a.n) {
+    a.n = grid_blocks(left, threads(a.H));
+    if (pieces(a.H) == 1) a.w_post ? run_forward<1, true>(a, gate, s) : run_forward<1, false>(a, gate, s);
+    else a.w_post ? run_forward<2, true>(a, gate, s) : run_forward<2, false>(a, gate, s);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    a.y += a.n * a.ld_y;
+    a.x += a.n * a.ld_x;
+    if (gate == kToken) a.gate += a.n * a.ld_gate;
+    a.out_x += a.n * a.ld_out_x;
+    a.out_n += a.n * a.ld_out_n;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_residual_norm_backward(const NormGradArgs& a, hipStream_t s) {
