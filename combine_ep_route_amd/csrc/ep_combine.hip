@@ -240,8 +240,7 @@ hipError_t launch_combine_backward(const CombineBwdArgs& a, hipStream_t stream) 
   if (C < threads) threads = ((C + 63) / 64) * 64;
   int64_t blocks = a.n;
   if (a.max_blocks > 0 && blocks > a.max_blocks) blocks = a.max_blocks;
-  if (blocks > 0x7FFFFFFF) blocks = 0x7FFFFFFF;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(threads);
+  const dim3 grid(grid_blocks(blocks, threads)), block(threads);
   if (a.K <= 8) combine_backward_kernel<8><<<grid, block, 0, stream>>>(a);
   else combine_backward_kernel<32><<<grid, block, 0, stream>>>(a);
   return hipGetLastError();
@@ -251,8 +250,7 @@ hipError_t launch_dequant(const DequantArgs& a, hipStream_t stream) {
   if (a.n == 0) return hipSuccess;
   const int C = a.H / 16;
   const int threads = ((C + 63) / 64) * 64;
-  int64_t blocks = a.n > 0x7FFFFFFF ? 0x7FFFFFFF : a.n;
-  dequant_kernel<<<dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, stream>>>(a);
+  dequant_kernel<<<dim3(grid_blocks(a.n, threads)), dim3(threads), 0, stream>>>(a);
   return hipGetLastError();
 }
 

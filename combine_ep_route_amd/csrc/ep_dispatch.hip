@@ -617,8 +617,7 @@ void launch_nv(const DispatchArgs& p, hipStream_t stream) {
   // The CU cap counts 4-wave workgroups: smaller ones get as many waves.
   const int64_t cap = static_cast<int64_t>(p.max_blocks) * 4 / wpb;
   if (cap > 0 && blocks > cap) blocks = cap;
-  if (blocks > 0x7FFFFFFF) blocks = 0x7FFFFFFF;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(64 * wpb);
+  const dim3 grid(grid_blocks(blocks, 64 * wpb)), block(64 * wpb);
   const size_t lds = static_cast<size_t>(p.E2 + p.N * p.G) * sizeof(int32_t);   // HT key offsets
   if (p.ht) dispatch_kernel<IN, true, PAYLOAD, KMAX, NV><<<grid, block, lds, stream>>>(p, W);
   else dispatch_kernel<IN, false, PAYLOAD, KMAX, NV><<<grid, block, 0, stream>>>(p, W);
@@ -642,9 +641,7 @@ hipError_t launch_quantize(const QuantArgs& a, hipStream_t stream) {
   if (a.n == 0) return hipSuccess;
   const int C = a.H / 16;
   const int W = (C + 64 * kChunksPerLane - 1) / (64 * kChunksPerLane);
-  int64_t blocks = (a.n * W + 3) / 4;
-  if (blocks > 0x7FFFFFFF) blocks = 0x7FFFFFFF;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(256);
+  const dim3 grid(grid_blocks((a.n * W + 3) / 4, 256)), block(256);
   if (a.count) quantize_kernel<kChunksPerLane, kFirst><<<grid, block, 0, stream>>>(a, W);
   else if (a.topk) quantize_kernel<kChunksPerLane, kEntries><<<grid, block, 0, stream>>>(a, W);
   else quantize_kernel<kChunksPerLane, kAll><<<grid, block, 0, stream>>>(a, W);

@@ -22,7 +22,8 @@ constexpr int kMaxRanks = 1024;
 constexpr int kMaxHidden = 16384;
 constexpr int kLayoutTile = 16;    // tokens per layout tile (one workgroup of the count kernel)
 
-// Workgroups of `threads` that one launch takes of `blocks`: a grid dimension counts its threads in 32 bits.
+// Workgroups of `threads` that one launch takes of `blocks`: a grid dimension counts its threads in 32 bits.  What
+// is left is for the kernel's loop, or for another launch.
 inline unsigned grid_blocks(int64_t blocks, int threads) {
   const int64_t most = UINT32_MAX / static_cast<uint32_t>(threads);
   return static_cast<unsigned>(blocks < most ? blocks : most);

@@ -57,3 +57,40 @@ def test_norm_of_the_most_rows(gate):
     for at, (res, out) in zip(parts, want):
         assert torch.equal(x[at], res) and torch.equal(y[at], out), at
     ep.ep_destroy_group(g)
+
+
+def test_quantize_and_dequantize_more_rows_than_a_grid_holds():
+    """Over 2^26 rows of 128 values: ep_quantize gives every row a wave, ep_dequantize_rows a workgroup of one."""
+    H, part, parts, rest = 128, 1 << 20, 64, 5
+    n = parts * part + rest
+    say(f"quantise and dequantise {n} rows")
+    room(60)
+    g = one_expert(H, "fp8")
+    base = normal((part, H), 3, 4.0)
+    q0, s0 = torch.empty((part, H), dtype=torch.float8_e4m3fn, device="cuda"), torch.empty((part, 1), device="cuda")
+    ep.ep_quantize(g, base, q0, s0)
+    x = torch.empty((n, H), dtype=BF16, device="cuda")
+    x[:parts * part].view(parts, part, H).copy_(base)
+    x[parts * part:] = base[:rest]
+    q, s = torch.empty((n, H), dtype=torch.float8_e4m3fn, device="cuda"), torch.empty((n, 1), device="cuda")
+    ep.ep_quantize(g, x, q, s)
+    torch.cuda.synchronize()
+    codes = q.view(torch.uint8)
+    for i in range(parts + 1):
+        at = slice(i * part, min(n, (i + 1) * part))
+        m = at.stop - at.start
+        assert torch.equal(codes[at], q0[:m].view(torch.uint8)) and torch.equal(s[at], s0[:m]), i
+
+    rows = torch.zeros((n, H + 16), dtype=torch.uint8, device="cuda")   # codes, one scale, padding
+    rows[:, :H] = codes
+    rows[:, H:H + 4] = s.view(torch.uint8)
+    y0 = torch.empty((part, H), dtype=BF16, device="cuda")
+    ep.ep_dequantize_rows(g, rows[:part], y0)
+    del x, q, s, codes
+    y = torch.empty((n, H), dtype=BF16, device="cuda")
+    ep.ep_dequantize_rows(g, rows, y)
+    torch.cuda.synchronize()
+    for i in range(parts + 1):
+        at = slice(i * part, min(n, (i + 1) * part))
+        assert torch.equal(y[at], y0[:at.stop - at.start]), i
+    ep.ep_destroy_group(g)
