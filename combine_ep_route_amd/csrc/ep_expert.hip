@@ -84,11 +84,16 @@ struct AlongSrc {
 };
 
 // Rounded to bf16: the results, and of kGatedGrad the gradients of both products, which are operands of the
-// matrix unit next; all else stays fp32.
+// matrix unit next (all gradients together are then 0.0023 off in norm, 0.0017 with fp32 ones in between, of
+// which the results' own rounding makes the most); all else stays fp32.
+// The 256 x 256 tile of kGatedGrad does not fit its registers: load_rows holds the gradients of all the wave's rows
+// beside 128 accumulators, and 32 registers a lane go to scratch behind the main loop (438 MB written where the
+// results are 268).  The FP8 gated one spills one.
 // Measured, 256 experts of 7168 x 2048:
-//   32768 rows, none to several hundred an expert: gated bf16 2.36 ms, 815 TFLOP/s, 11.1 GB read beyond the L2 (8.1
-//   needed: an expert's row tiles drift apart); gated FP8 1.36 ms, 1410 TFLOP/s; linear bf16 1.23 ms, 780 TFLOP/s.
-//   Half of the tiles hold less than half of their rows: the weights' bytes and the products bound them in turn.
+//   32768 rows, none to several hundred an expert: gated bf16 2.28 ms, 840 TFLOP/s, 11.1 GB read beyond the L2 (8.1
+//   needed: an expert's row tiles drift apart); gated FP8 1.34 ms, 1440 TFLOP/s; linear bf16 1.21 ms, 800 TFLOP/s.
+//   13 % of the multiplied fragments are padding (37568 rows of them); the rest of the distance is the kernels' own
+//   rate without padding.
 //   4 rows each, FP8: gated 1.19 ms, 6.3 TB/s, bound by the weights' bytes.  Two workgroups a CU need
 //   FP8 stages of 21 KiB, three each: linear of 8 rows each in 64 experts 170 us so, 200 with one and four stages.
 template <class C, int KIND, int ACT>
@@ -382,12 +387,17 @@ hipError_t launch_along_as(const AlongArgs& a, hipStream_t stream, bool check) {
 
 // Which tile a product over the rows takes, by the average rows of an expert (the counts themselves are only
 // on the device) and by how many 256 x 256 tiles there are for the 256 CUs.  Measured, 64 experts of 2048 x 1408,
-// gated, us:
-//   rows an expert   bf16: small  middle  big    FP8: small  middle  big
-//         32               147     158     -           102     85     -
-//         48                -      148    178            -     90    101
-//         96                -      164    181            -    107    112
-//        384                -      401    345            -    277    242
+// rows spread evenly at random, us (small / middle / big):
+//   rows an expert    linear bf16         gradient of the rows    gated FP8
+//         16          74 /  78 /  87       74 /  80 /  85          78 /  82 /  99
+//         24          80 /  78 /  87       74 /  75 /  86          79 /  82 / 101
+//         32          83 /  79 /  88       85 /  77 /  87          91 /  86 / 101
+//         48          96 /  81 /  90       90 /  80 /  91         107 /  91 / 104
+//         96         128 /  90 /  96      124 / 114 / 101         153 / 111 / 112
+//        128         153 / 114 / 101      148 / 121 / 110         184 / 141 / 123
+// Both borders lie where the forward products' times cross; the gradient of the rows would take the big tile from
+// 64 rows on (98 / 94).  The gated bf16 product's times move by a tenth from run to run: 24: 146 / 157 / 177, 32: 157
+// / 150 to 171 / 181, 48: 177 / 153 to 182 / 170 to 198, 96: 243 / 170 / 182 to 202, 128: 290 / 220 / 190 to 220.
 // From 24 rows on the small tile's 32 rows are often two tiles, which read the weights twice.  Rows spread over
 // the experts as a router leaves them make many tiles of the average's multiple: at 128 rows on average (256
 // experts of 7168 x 2048, bf16) the big tile takes 2.35 ms, the middle one 2.67.
@@ -475,9 +485,13 @@ hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check)
   }
 }
 
-// With fewer than two 256 x 256 tiles a CU the smaller ones fill the chip: the whole linear backward of 8 experts
-// of 1024 x 768 takes 63 us with them, 103 with big ones; with 2816 tiles (64 experts of 2048 x 1408) the gated
-// backward of 24 rows each takes 494 us with big ones, 553 with small.
+// With fewer than two 256 x 256 tiles a CU the smaller ones fill the chip.  128 rows an expert, F32 / bf16 gradients,
+// us, small tiles and big ones, by the number of big ones:
+//     96 (8 experts of 1024 x 768)     16 / 14   21 / 17       640 (40 of 1024 x 1024)    50 / 42    53 / 40
+//    256 (16 of 1024 x 1024)           26 / 21   25 / 19      1024 (64 of 1024 x 1024)    77 / 64    72 / 52
+//    384 (24 of 1024 x 1024)           34 / 29   37 / 29      1536 (96 of 1024 x 1024)   117 / 92   102 / 79
+//    512 (32 of 1024 x 1024)           42 / 37   40 / 30      2048 (128 of 1024 x 1024)  163 / 121  145 / 100
+// Near the border the big ones win where they fill the CUs a whole number of times (256, 512).
 hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check) {
   if (static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + 255) / 256) * ((g.I + 255) / 256) < 512)
     return launch_weight_grad_as<Core<128, 128, 2, 2, true, true, false, 4, 64>>(g, f32, stream, check);

@@ -171,11 +171,16 @@ __global__ __launch_bounds__(kMaxThreads) void residual_norm_kernel(NormArgs a) 
 // Column sums: w_pre of g_norm xh; and one more, of s = b d yh (yh = y without a post norm; times a token's
 // gate): w_post's is gate times it, a channel gate's is w_post times it.
 // A workgroup takes rows blockIdx, blockIdx + blocks, ... and keeps the weights and its share of the column
-// sums in registers; the workgroups' shares are added in order by sum_columns_kernel.  What a row waits for is
-// the loads and two sums over the workgroup, one after the other: the next row's loads are started first.
-// 4096 x 7168 with a channel gate: 84 us with the column sums, 4.2 TB/s of 352 MB (this kernel 77 us, 4.6 TB/s;
+// sums in registers, of which 1024 threads have 128 each; the workgroups' shares are added in order by
+// sum_columns_kernel.  What a row waits for is the loads and two sums over the workgroup, one after the other: the
+// next row's loads are started first.
+// 4096 x 7168 with a channel gate: 84 us with the column sums, 4.2 TB/s of 352 MB (this kernel 72 us, 4.9 TB/s;
 // with separate sums for w_post and the gate, wave sums by shuffles and no loads ahead 142 us).
 // Streaming stores gain 2.5 us, streaming loads lose 6.
+// One piece a thread (up to 8192 columns) keeps all of that in registers but for the token gate with a post norm
+// (21 a lane go to scratch: 118 us, 4.0 TB/s at 4096 x 7168).  Two pieces do not: 123 to 139 go to scratch with a post
+// norm (4096 x 16384: 400 us, 2.0 TB/s; token gate 580, 1.9), 76 with a channel gate alone (223 us, 3.6 TB/s), 16
+// with a token gate alone (209 us, 5.1 TB/s).
 template <int CPT, bool POST, int GATE>
 __global__ __launch_bounds__(kMaxThreads) void residual_norm_backward_kernel(NormGradArgs a) {
   __shared__ __attribute__((aligned(16))) float part[2][3 * 16];
@@ -300,7 +305,7 @@ __device__ __forceinline__ float weight_at(const void* w, bool f32, int c) {
 
 // Column sums of the workgroups' shares: 64 columns a workgroup, 16 threads a column.  blockIdx.y 0: w_pre's;
 // 1: the second sum, of which w_post's and a channel gate's are multiples.  The order is fixed, so the sums are the
-// same bits every time.  256 x 2 x 7168: 8 us, 15 MB of reads and the launch.
+// same bits every time.  256 x 2 x 7168: 7 us, 15 MB of reads and the launch.
 __global__ __launch_bounds__(1024) void sum_columns_kernel(NormGradArgs a, int blocks) {
   __shared__ float part[16][64];
   const int c = blockIdx.x * 64 + lane_id(), q = threadIdx.x >> 6;
