@@ -66,10 +66,16 @@ def _ref(d):
     return d   # ctypes passes a structure where a pointer to it is declared
 
 
+# the current stream's handle without making a Stream object for it; not part of torch's public interface
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
-    if stream is None:   # the current stream's handle, without making a Stream object for it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 class Group:
