@@ -23,6 +23,7 @@ EP_MODE_LL = 0
 EP_MODE_HT = 1
 EP_HT_STAGE2_PER_EXPERT = 0
 EP_HT_STAGE2_PER_RANK = 1
+EP_HT_STAGE2_PER_RANK_SORTED = 3
 
 EP_DTYPE_F32 = 0
 EP_DTYPE_BF16 = 1
@@ -52,6 +53,8 @@ EP_MAP_HT_RANK_COUNT = 4
 EP_MAP_HT_RANK_OFFSET = 5
 EP_MAP_HT_EXPERT_COUNT = 6
 EP_MAP_HT_EXPERT_OFFSET = 7
+EP_MAP_HT_SORTED_ROW = 8
+EP_MAP_HT_SORTED_COUNT = 9
 
 EP_ACT_SILU = 0
 EP_ACT_GELU_TANH = 1
@@ -145,6 +148,10 @@ SIGNATURES = {
     "ep_complete": (_S, [_P, _P]),
     "ep_combine_backward": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _P]),
     "ep_dispatch_backward": (_S, [_P, _PT, _PT, _P]),
+    "ep_expert_sort": (_S, [_P, _PT, _PT, _P]),
+    "ep_expert_sort_backward": (_S, [_P, _PT, _PT, _P]),
+    "ep_expert_unsort": (_S, [_P, _PT, _PT, _PT, _P]),
+    "ep_expert_unsort_backward": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _P]),
     "ep_expert_gated": (_S, [_P, _PT, _PT, _PT, _PT, _PT, ctypes.c_int32, _PT, _P]),
     "ep_expert_gated_backward": (_S, [_P, _PT, _PT, _PT, _PT, ctypes.c_int32, _PT, _PT, _PT, _PT, _PT, _P]),
     "ep_expert_quantize": (_S, [_P, _PT, _PT, _PT, _P]),

@@ -61,7 +61,7 @@ inline int log2_exact(int v) {
 // creation and the group-free layout.  Checks mode, topology, K, M, T_max,
 // S and the stage-2 kind (not the payload, hidden size or buffers).
 struct Topology {
-  int R, L, P, M, J, E2, s2_rank;
+  int R, L, P, M, J, E2, s2_rank, sorted;
 };
 ep_status_t check_topology(const ep_config_t& cfg, Topology* t);
 
@@ -82,6 +82,7 @@ struct Group {
   int64_t rows1_max = 0;   // HT stage-1 rows, worst case
   int64_t rows2_max = 0;   // HT stage-2 rows, worst case (n_max * K)
   int s2_rank = 0;         // HT stage 2 per (token, rank)
+  int sorted = 0;          // the same, with the places of the ranks' rows in expert order
   int E2 = 0;              // stage-2 keys: E, or R per rank
   int tiles_max = 0;       // layout tiles, worst case
 
@@ -147,6 +148,11 @@ struct Handle {
   int32_t* off1 = nullptr;       // HT [R]
   int32_t* c2 = nullptr;         // HT [E]
   int32_t* off2 = nullptr;       // HT [E]
+  int32_t* rank_x = nullptr;     // sorted [n_max, K]: rank of (token, k) inside its tile and expert, or -1
+  int32_t* place = nullptr;      // sorted [n_max, K]: the entry's row in expert order, or -1
+  int32_t* entry_row = nullptr;  // sorted [n_max, K]: the stage-2 row of the entry's rank, or -1
+  int32_t* cx = nullptr;         // sorted [E]: rows per expert
+  int32_t* hist_x = nullptr;     // sorted [tiles_max, E] tile counts -> prefixes
   int32_t* rows_total = nullptr; // LL, many sources or runs [E]: rows per expert, for the experts' products
   int32_t* rows_list = nullptr;  // the same [n_max * K]: their message indices, expert after expert
   int32_t* hist_e = nullptr;     // [tiles_max, E] tile counts -> prefixes
@@ -200,6 +206,12 @@ struct LayoutArgs {
   int32_t* ll_count;     // LL out: slots used per (expert, source) [E, S]
   int32_t* c1;           // HT out: stage-1 rows per rank [R]
   int32_t* c2;           // HT out: stage-2 rows per key [E2]
+  // With the per-rank stage 2, optionally (hist_x not null) the entries' places in expert order:
+  int32_t* rank_x;       // [n, K] out: in-tile ranks per expert
+  int32_t* hist_x;       // [tiles, E] per-tile expert counts, rewritten as prefixes
+  int32_t* cx;           // [E] out: rows per expert
+  int32_t* place;        // [n, K] out: rows in expert order
+  int32_t* entry_row;    // [n, K] out: the rank's row of every valid entry
   int32_t* err;          // device error word (bad or repeated entries)
 };
 hipError_t launch_layout(const LayoutArgs& a, hipStream_t stream);
@@ -300,6 +312,63 @@ struct CombineBwdArgs {
   int32_t* err;
 };
 hipError_t launch_combine_backward(const CombineBwdArgs& a, hipStream_t stream);
+
+// Between the ranks' stage-2 rows and rows in expert order.  Every entry (i, k) of a token has a place, the row
+// in expert order, and a row, the one of its rank; entries of a token on the same rank share it.
+struct SortArgs {
+  const uint8_t* x;       // the ranks' rows
+  int64_t ld_x;           // bytes
+  int64_t rows_x;
+  uint8_t* out;           // rows in expert order
+  int64_t ld_out;         // bytes
+  int64_t rows_out;
+  int32_t bytes;          // of a row, a multiple of 4
+  int32_t pad;            // bytes behind them that are written as zeros: the row's last line whole, or 0
+  const int32_t* row;     // [n, K]
+  const int32_t* place;   // [n, K]
+  int64_t n;
+  int K;
+  int max_blocks;         // 0 = no cap
+  int32_t* err;
+};
+hipError_t launch_sort(const SortArgs& a, hipStream_t stream);
+
+struct UnsortArgs {
+  const uint16_t* y;      // BF16 rows in expert order
+  int64_t ld_y;           // elements
+  int64_t rows_y;
+  const float* w;         // [n, K], or null for unit weights (the sort's adjoint)
+  uint16_t* out;          // BF16 rows of the ranks
+  int64_t ld_out;
+  int64_t rows_out;
+  const int32_t* row;
+  const int32_t* place;
+  int64_t n;
+  int K, H;
+  int max_blocks;
+  int32_t* err;
+};
+hipError_t launch_unsort(const UnsortArgs& a, hipStream_t stream);
+
+struct UnsortBwdArgs {
+  const uint16_t* g;      // BF16 gradient of the ranks' rows
+  int64_t ld_g;
+  int64_t rows_g;
+  const uint16_t* y;      // BF16 rows in expert order, or null (no dw)
+  int64_t ld_y;
+  uint16_t* dy;           // their gradient
+  int64_t ld_dy;
+  int64_t rows_y;         // rows valid in dy (and y)
+  const float* w;         // [n, K]
+  float* dw;              // [n, K] or null
+  const int32_t* row;
+  const int32_t* place;
+  int64_t n;
+  int K, H;
+  int max_blocks;
+  int32_t* err;
+};
+hipError_t launch_unsort_backward(const UnsortBwdArgs& a, hipStream_t stream);
 
 struct DequantArgs {
   const uint8_t* rows;

@@ -24,7 +24,10 @@
 //   * the dispatch kernel adds key offset + tile prefix + in-tile rank; in
 //     HT each of its workgroups first scans the key totals into the key
 //     offsets in LDS (a few hundred values, read while its tokens load), so
-//     that no step of the scan waits for the other workgroups.
+//     that no step of the scan waits for the other workgroups;
+//   * places_kernel (per-rank stage 2 with expert order): the first two parts
+//     also count and rank every entry by its expert; this adds the same three
+//     terms up for the entry's place in expert order and for its rank's row.
 // No atomics decide a position, so every map is bit-reproducible.
 #include "ep_route_dev.h"
 
@@ -58,9 +61,9 @@ __device__ __forceinline__ int chunk_prefix(int32_t* base, int p0, int p1, int r
 
 template <bool ROUTE, int V, int LPN>
 __global__ __launch_bounds__(kTileThreads) void tile_count_kernel(LayoutArgs a) {
-  extern __shared__ uint32_t s_mask[];            // [E2 + N] lane masks of the tile's tokens
+  extern __shared__ uint32_t s_mask[];            // [E2 + N (+ E)] lane masks of the tile's tokens
   __shared__ int s_e[kTile][kMaxTopK];            // the tile's entries
-  __shared__ int s_key[kTile][kMaxTopK];          // stage-2 key of an entry that takes a row, else -1
+  __shared__ int s_key[kTile][kMaxTopK];          // stage-2 key of an entry that takes a row, -2: none, -1: invalid
   __shared__ float s_node[kTile][32];             // routing: node-score exchange
   const int tid = threadIdx.x;
   const int j = blockIdx.x;                       // tile
@@ -69,7 +72,8 @@ __global__ __launch_bounds__(kTileThreads) void tile_count_kernel(LayoutArgs a) 
   const int ntok = min(kTile, a.T - t0);          // tokens in this tile
   const int E2 = a.E2, N = a.N, K = a.K, E = a.E;
   const int64_t i0 = static_cast<int64_t>(s) * a.T + t0;
-  for (int x = tid; x < E2 + N; x += blockDim.x) s_mask[x] = 0;
+  const int by_expert = a.hist_x ? E : 0;         // keys behind the others: experts, for their order
+  for (int x = tid; x < E2 + N + by_expert; x += blockDim.x) s_mask[x] = 0;
   // e / L and e / P by shifts when they are powers of two
   auto div_l = [&](int e) { return a.l_shift >= 0 ? e >> a.l_shift : e / a.L; };
   auto div_p = [&](int e) { return a.p_shift >= 0 ? e >> a.p_shift : e / a.P; };
@@ -134,7 +138,8 @@ __global__ __launch_bounds__(kTileThreads) void tile_count_kernel(LayoutArgs a) 
       const bool first = ok && !same_key;
       if (first) atomicOr(&s_mask[key], 1u << slot);
       if (a.ht && ok && !same_node) atomicOr(&s_mask[E2 + nd], 1u << slot);
-      s_key[slot][k] = first ? key : -1;
+      if (by_expert && ok) atomicOr(&s_mask[E2 + N + e], 1u << slot);
+      s_key[slot][k] = first ? key : ok ? -2 : -1;
     }
     if (bad) atomicOr(a.err, bad);
     __syncthreads();
@@ -143,6 +148,8 @@ __global__ __launch_bounds__(kTileThreads) void tile_count_kernel(LayoutArgs a) 
       const int slot = x / K, k = x - slot * K;
       const int key = s_key[slot][k];
       a.rank_e[i0 * K + x] = key >= 0 ? __popc(s_mask[key] & ((1u << slot) - 1u)) : -1;
+      if (by_expert)
+        a.rank_x[i0 * K + x] = key != -1 ? __popc(s_mask[E2 + N + s_e[slot][k]] & ((1u << slot) - 1u)) : -1;
     }
   }
   if (a.ht) {
@@ -156,6 +163,8 @@ __global__ __launch_bounds__(kTileThreads) void tile_count_kernel(LayoutArgs a) 
   for (int x = tid; x < E2; x += blockDim.x) a.hist_e[static_cast<int64_t>(j) * E2 + x] = __popc(s_mask[x]);
   if (a.ht)
     for (int x = tid; x < N; x += blockDim.x) a.hist_n[static_cast<int64_t>(j) * N + x] = __popc(s_mask[E2 + x]);
+  for (int x = tid; x < by_expert; x += blockDim.x)
+    a.hist_x[static_cast<int64_t>(j) * E + x] = __popc(s_mask[E2 + N + x]);
 }
 
 // LL: the (expert, source) pairs are independent -- a source's slots for an
@@ -187,7 +196,8 @@ constexpr int kScanThreads = 256;   // four keys per workgroup
 // HT: one wave per key.  Keys [0, E2) are the stage-2 keys, whose sequence
 // is every tile in order; keys E2 + d (d = n*G + g, d < R) are the stage-1
 // ranks, whose sequence is the tiles of the sources s = g, g+G, g+2G, ...
-// in order, counter n of each.  A lane takes kScanPerLane consecutive
+// in order, counter n of each; keys from E2 + R on (with expert order) are
+// the experts, over every tile again.  A lane takes kScanPerLane consecutive
 // elements of the sequence per pass (independent loads), the lanes' sums are
 // scanned across the wave, and the exclusive prefixes are written back in
 // place; the key's total goes to c2 / c1.
@@ -195,14 +205,17 @@ __global__ __launch_bounds__(kScanThreads) void scan_keys_kernel(LayoutArgs a) {
   const int lane = threadIdx.x & 63;
   const int key = blockIdx.x * (kScanThreads / 64) + (threadIdx.x >> 6);
   const int E2 = a.E2, N = a.N, G = a.G, R = N * G, tps = a.tps;
-  if (key < E2 + R) {
-    const bool expert = key < E2;
+  const bool order = key >= E2 + R;
+  if (key < E2 + R + (a.hist_x ? a.E : 0)) {
+    const bool expert = key < E2 || order;
+    int32_t* const hist = order ? a.hist_x : a.hist_e;
+    const int width = order ? a.E : E2, col = order ? key - E2 - R : key;
     const int d = key - E2, n = expert ? 0 : d / G, g = expert ? 0 : d - n * G;
     const int nsrc = expert ? 0 : (g < a.S ? (a.S - g + G - 1) / G : 0);
     const int len = expert ? a.n_tiles : nsrc * tps;
     // address of element q of the key's sequence
     auto at = [&](int q) -> int32_t* {
-      if (expert) return a.hist_e + static_cast<int64_t>(q) * E2 + key;
+      if (expert) return hist + static_cast<int64_t>(q) * width + col;
       const int src = g + (q / tps) * G, tt = q - (q / tps) * tps;
       return a.hist_n + static_cast<int64_t>(src * tps + tt) * N + n;
     };
@@ -225,8 +238,64 @@ __global__ __launch_bounds__(kScanThreads) void scan_keys_kernel(LayoutArgs a) {
       }
       carry += __shfl(incl, 63, 64);
     }
-    if (lane == 0) (expert ? a.c2 + key : a.c1 + d)[0] = carry;
+    if (lane == 0) (order ? a.cx + col : expert ? a.c2 + key : a.c1 + d)[0] = carry;
   }
+}
+
+// Exclusive prefix sums of up to 4 * kPlaceThreads counts in LDS.
+constexpr int kPlaceThreads = 256;
+static_assert(kMaxExperts <= 4 * kPlaceThreads && kMaxRanks <= 4 * kPlaceThreads, "four counts a thread");
+
+__device__ __forceinline__ void scan_counts(const int32_t* count, int n, int32_t* s_off, int* s_wave) {
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  int v[4], sum = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    v[q] = 4 * tid + q < n ? count[4 * tid + q] : 0;
+    sum += v[q];
+  }
+  const int incl = wave_inclusive_scan(sum, lane);
+  if (lane == 63) s_wave[w] = incl;
+  __syncthreads();
+  int run = incl - sum;
+  for (int q = 0; q < w; ++q) run += s_wave[q];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (4 * tid + q < n) s_off[4 * tid + q] = run;
+    run += v[q];
+  }
+  __syncthreads();
+}
+
+// The entries' places in expert order and their ranks' rows: key offset + tile prefix + in-tile rank of each.
+// The rank's row is that of the token's first entry on the rank.  One entry a thread; every workgroup scans the
+// totals itself.
+__global__ __launch_bounds__(kPlaceThreads) void places_kernel(LayoutArgs a) {
+  __shared__ int32_t s_expert[kMaxExperts], s_rank[kMaxRanks];
+  __shared__ int s_wave[2][kPlaceThreads / 64];
+  scan_counts(a.cx, a.E, s_expert, s_wave[0]);
+  scan_counts(a.c2, a.E2, s_rank, s_wave[1]);
+  const int K = a.K;
+  const int64_t x = static_cast<int64_t>(blockIdx.x) * kPlaceThreads + threadIdx.x;
+  if (x >= a.n * K) return;
+  const int64_t i = x / K;
+  const int k = static_cast<int>(x - i * K);
+  const int s = static_cast<int>(i / a.T), t = static_cast<int>(i - static_cast<int64_t>(s) * a.T);
+  const int64_t j = static_cast<int64_t>(s) * a.tps + t / kTile;
+  const int rx = a.rank_x[x];
+  int place = -1, row = -1;
+  if (rx >= 0) {
+    const int e = a.topk_copy[x], d = e / a.L;
+    place = s_expert[e] + a.hist_x[j * a.E + e] + rx;
+    int first = 0;
+    for (int q = k; q >= 0; --q) {
+      const int r = a.rank_e[i * K + q], eq = a.topk_copy[i * K + q];
+      if (r >= 0 && eq / a.L == d) first = r;   // of a rank's entries one has a rank in the tile
+    }
+    row = s_rank[d] + a.hist_e[j * a.E2 + d] + first;
+  }
+  a.place[x] = place;
+  a.entry_row[x] = row;
 }
 
 // Receive stage of a dispatch: the per-(expert, source) counters [E, S] as
@@ -291,7 +360,7 @@ hipError_t launch_layout(const LayoutArgs& a_in, hipStream_t stream) {
   if (a_in.n == 0) return hipSuccess;
   LayoutArgs a = a_in;
   const dim3 grid(static_cast<unsigned>(a.n_tiles));
-  const size_t lds = static_cast<size_t>(a.E2 + a.N) * 4;
+  const size_t lds = static_cast<size_t>(a.E2 + a.N + (a.hist_x ? a.E : 0)) * 4;
   int lpn = 0;
   bool routed = false;
   if (a.scores && fast_path(a.scores, a.ld, a.E, a.N, a.K, a.J, &lpn)) {
@@ -324,9 +393,13 @@ hipError_t launch_layout(const LayoutArgs& a_in, hipStream_t stream) {
     tile_count_kernel<false, 4, 1><<<grid, dim3(kTileThreads), lds, stream>>>(a);
   }
   if (a.ht) {
-    const int keys = a.E2 + a.N * a.G;
+    const int keys = a.E2 + a.N * a.G + (a.hist_x ? a.E : 0);
     const int per = kScanThreads / 64;
     scan_keys_kernel<<<dim3(static_cast<unsigned>((keys + per - 1) / per)), dim3(kScanThreads), 0, stream>>>(a);
+    if (a.hist_x) {
+      const int64_t blocks = (a.n * a.K + kPlaceThreads - 1) / kPlaceThreads;   // n * K < 2^31
+      places_kernel<<<dim3(static_cast<unsigned>(blocks)), dim3(kPlaceThreads), 0, stream>>>(a);
+    }
   } else {
     const int64_t pairs = static_cast<int64_t>(a.E2) * a.S;
     layout_scan_ll_kernel<<<dim3(static_cast<unsigned>((pairs + 255) / 256)), dim3(256), 0, stream>>>(a);

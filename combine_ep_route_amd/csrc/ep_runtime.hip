@@ -303,7 +303,8 @@ ep_status_t check_topology(const ep_config_t& cfg, Topology* t) {
   if (cfg.mode != EP_MODE_LL && cfg.mode != EP_MODE_HT) return EP_ERR_INVALID_ARGUMENT;
   if (cfg.num_nodes <= 0 || cfg.ranks_per_node <= 0 || cfg.num_experts <= 0 || cfg.top_k <= 0 ||
       cfg.max_tokens_per_rank <= 0 || cfg.num_src_ranks <= 0 || cfg.max_nodes_per_token < 0 ||
-      (cfg.ht_stage2 != EP_HT_STAGE2_PER_EXPERT && cfg.ht_stage2 != EP_HT_STAGE2_PER_RANK))
+      (cfg.ht_stage2 != EP_HT_STAGE2_PER_EXPERT && cfg.ht_stage2 != EP_HT_STAGE2_PER_RANK &&
+       cfg.ht_stage2 != EP_HT_STAGE2_PER_RANK_SORTED))
     return EP_ERR_INVALID_ARGUMENT;
   const int64_t R = static_cast<int64_t>(cfg.num_nodes) * cfg.ranks_per_node;
   if (cfg.num_experts % R != 0) return EP_ERR_INVALID_ARGUMENT;
@@ -321,7 +322,8 @@ ep_status_t check_topology(const ep_config_t& cfg, Topology* t) {
   t->P = P;
   t->M = M;
   t->J = J;
-  t->s2_rank = cfg.mode == EP_MODE_HT && cfg.ht_stage2 == EP_HT_STAGE2_PER_RANK;
+  t->sorted = cfg.mode == EP_MODE_HT && cfg.ht_stage2 == EP_HT_STAGE2_PER_RANK_SORTED;
+  t->s2_rank = t->sorted || (cfg.mode == EP_MODE_HT && cfg.ht_stage2 == EP_HT_STAGE2_PER_RANK);
   t->E2 = t->s2_rank ? t->R : E;
   return EP_OK;
 }
@@ -362,6 +364,7 @@ EP_API ep_status_t ep_create_group(const ep_config_t* cfg_in, ep_stream_t stream
   g->J = J;
   g->fp8 = cfg.payload == EP_DTYPE_FP8_E4M3;
   g->s2_rank = s2_rank;
+  g->sorted = topo.sorted;
   g->E2 = E2;
   g->row_bytes = g->fp8 ? cfg.hidden + cfg.hidden / 128 * 4 : static_cast<int64_t>(cfg.hidden) * 2;
   g->msg_bytes = g->row_bytes + 16;
@@ -441,6 +444,7 @@ EP_API ep_status_t ep_create_group(const ep_config_t* cfg_in, ep_stream_t stream
     } else {
       bytes += align_up(nm * N * 4) + align_up(nm * K * 4) + align_up(R * 4) * 2 + align_up(E * 4) * 2;
     }
+    if (g->sorted) bytes += align_up(nm * K * 4) * 3 + align_up(E * 4) + align_up(tiles * E * 4);
     bytes += align_up(tiles * E * 4) + align_up(tiles * N * 4);
     uint8_t* b = static_cast<uint8_t*>(dev_alloc(g, bytes, &st));
     if (!b) break;
@@ -466,6 +470,13 @@ EP_API ep_status_t ep_create_group(const ep_config_t* cfg_in, ep_stream_t stream
       h->off1 = cv.take<int32_t>(R);
       h->c2 = cv.take<int32_t>(E);
       h->off2 = cv.take<int32_t>(E);
+    }
+    if (g->sorted) {
+      h->rank_x = cv.take<int32_t>(nm * K);
+      h->place = cv.take<int32_t>(nm * K);
+      h->entry_row = cv.take<int32_t>(nm * K);
+      h->cx = cv.take<int32_t>(E);
+      h->hist_x = cv.take<int32_t>(tiles * E);
     }
     h->hist_e = cv.take<int32_t>(tiles * E);
     h->hist_n = cv.take<int32_t>(tiles * N);
@@ -619,6 +630,11 @@ ep_status_t make_handle(Group* g, const int32_t* topk, const float* scores, int6
   a.ll_count = h->ll_count;
   a.c1 = h->c1;
   a.c2 = h->c2;
+  a.rank_x = h->rank_x;
+  a.hist_x = h->hist_x;
+  a.cx = h->cx;
+  a.place = h->place;
+  a.entry_row = h->entry_row;
   a.err = g->err;
   h->maps_ready = (n == 0);
   h->buf_half = -1;
@@ -630,6 +646,7 @@ ep_status_t make_handle(Group* g, const int32_t* topk, const float* scores, int6
     EP_HIP(launch_fill_i32(h->off1, g->R, 0, s));
     EP_HIP(launch_fill_i32(h->c2, a.E2, 0, s));
     EP_HIP(launch_fill_i32(h->off2, a.E2, 0, s));
+    if (h->cx) EP_HIP(launch_fill_i32(h->cx, a.E, 0, s));
   } else if (n == 0) {
     EP_HIP(launch_fill_i32(h->ll_count, static_cast<int64_t>(a.E) * S, 0, s));
   }
@@ -727,6 +744,8 @@ EP_API ep_status_t ep_handle_get_map(ep_handle_t handle, int32_t which, ep_tenso
     case EP_MAP_HT_RANK_OFFSET: if (ll) break; fill_view(view, h->off1, EP_DTYPE_I32, g->R, 0, EP_TAG_NONE); return EP_OK;
     case EP_MAP_HT_EXPERT_COUNT: if (ll) break; fill_view(view, h->c2, EP_DTYPE_I32, g->E2, 0, EP_TAG_TOKENS_PER_EXPERT); return EP_OK;
     case EP_MAP_HT_EXPERT_OFFSET: if (ll) break; fill_view(view, h->off2, EP_DTYPE_I32, g->E2, 0, EP_TAG_NONE); return EP_OK;
+    case EP_MAP_HT_SORTED_ROW: if (!g->sorted) break; fill_view(view, h->place, EP_DTYPE_I32, h->n, K, EP_TAG_NONE); return EP_OK;
+    case EP_MAP_HT_SORTED_COUNT: if (!g->sorted) break; fill_view(view, h->cx, EP_DTYPE_I32, E, 0, EP_TAG_TOKENS_PER_EXPERT); return EP_OK;
     default: break;
   }
   return EP_ERR_INVALID_ARGUMENT;
@@ -1012,9 +1031,11 @@ EP_API ep_status_t ep_combine_backward(ep_handle_t handle, const ep_tensor_t* gr
   Group* g = h->g;
   const int H = g->cfg.hidden, K = g->cfg.top_k;
   const bool ll = g->cfg.mode == EP_MODE_LL;
-  if (g->s2_rank) return EP_ERR_UNSUPPORTED;   // the experts apply the weights: nothing to differentiate here
+  // Rows of ranks are weighted already: nothing but the rows to differentiate here, by unit weights.
+  if (g->s2_rank && !g->sorted) return EP_ERR_UNSUPPORTED;
   if (!check2d(grad_out, EP_DTYPE_BF16, h->n, H, EP_TAG_TOKENS, true)) return EP_ERR_INVALID_ARGUMENT;
-  if (!check2d(topk_weights, EP_DTYPE_F32, h->n, K, EP_TAG_TOPK_WEIGHTS, false) || !contiguous2d(topk_weights))
+  if (g->sorted ? topk_weights || expert_out || grad_weights
+                : !check2d(topk_weights, EP_DTYPE_F32, h->n, K, EP_TAG_TOPK_WEIGHTS, false) || !contiguous2d(topk_weights))
     return EP_ERR_INVALID_ARGUMENT;
   ep_tensor_t dy2, y2;
   if (!expert_rows(g, grad_expert_out, &dy2)) return EP_ERR_INVALID_ARGUMENT;
@@ -1035,7 +1056,7 @@ EP_API ep_status_t ep_combine_backward(ep_handle_t handle, const ep_tensor_t* gr
   a.dy = static_cast<uint16_t*>(dy2.data);
   a.ld_dy = dy2.strides[0];
   a.rows = expert_out ? std::min(dy2.sizes[0], y2.sizes[0]) : dy2.sizes[0];
-  a.w = static_cast<const float*>(topk_weights->data);
+  a.w = topk_weights ? static_cast<const float*>(topk_weights->data) : nullptr;
   a.loc = ll ? h->slot_map : h->row2;
   a.dw = grad_weights ? static_cast<float*>(grad_weights->data) : nullptr;
   a.n = h->n;
@@ -1111,6 +1132,144 @@ EP_API ep_status_t ep_complete(ep_handle_t handle, ep_stream_t stream) {
 }
 
 // ===========================================================================
+// Rows of ranks in expert order, and back
+// ===========================================================================
+
+namespace {
+
+// The maps were written when the handle was made.
+ep_status_t sorted_ready(const Handle* h) { return h->g->sorted ? EP_OK : EP_ERR_UNSUPPORTED; }
+
+// BF16 [rows, H].
+bool bf16_rows(const Group* g, const ep_tensor_t* t) {
+  return check2d(t, EP_DTYPE_BF16, -1, g->cfg.hidden, EP_TAG_TOKENS, true);
+}
+
+bool entry_weights(const Handle* h, const ep_tensor_t* t) {
+  return check2d(t, EP_DTYPE_F32, h->n, h->g->cfg.top_k, EP_TAG_TOPK_WEIGHTS, false) && contiguous2d(t);
+}
+
+ep_status_t unsort(Handle* h, const ep_tensor_t* y, const ep_tensor_t* w, ep_tensor_t* out, ep_stream_t stream,
+                   const char* what) {
+  Group* g = h->g;
+  const hipStream_t s = as_stream(stream);
+  if (const ep_status_t st = ensure_device(g, s); st != EP_OK) return st;
+  h->stream = s;
+  UnsortArgs a{};
+  a.y = static_cast<const uint16_t*>(y->data);
+  a.ld_y = y->strides[0];
+  a.rows_y = y->sizes[0];
+  a.w = w ? static_cast<const float*>(w->data) : nullptr;
+  a.out = static_cast<uint16_t*>(out->data);
+  a.ld_out = out->strides[0];
+  a.rows_out = out->sizes[0];
+  a.row = h->entry_row;
+  a.place = h->place;
+  a.n = h->n;
+  a.K = g->cfg.top_k;
+  a.H = g->cfg.hidden;
+  a.max_blocks = dispatch_block_cap(g);
+  a.err = g->err;
+  const ep_status_t st = from_hip(launch_unsort(a, s));
+  if (st == EP_OK) trace(g, what, h->n);
+  return st;
+}
+
+}  // namespace
+
+EP_API ep_status_t ep_expert_sort(ep_handle_t handle, const ep_tensor_t* rows, ep_tensor_t* out, ep_stream_t stream) {
+  Handle* h = reinterpret_cast<Handle*>(handle);
+  if (!handle_ok(h) || !rows || !out) return EP_ERR_INVALID_ARGUMENT;
+  Group* g = h->g;
+  if (const ep_status_t st = sorted_ready(h); st != EP_OK) return st;
+  const bool packed = rows->dtype == EP_DTYPE_U8;
+  if (packed ? !check2d(rows, EP_DTYPE_U8, -1, -1, EP_TAG_TOKENS, true) || rows->sizes[1] < g->row_bytes ||
+                   !check2d(out, EP_DTYPE_U8, -1, -1, EP_TAG_TOKENS, true) || out->sizes[1] < g->row_bytes
+             : !bf16_rows(g, rows) || !bf16_rows(g, out))
+    return EP_ERR_INVALID_ARGUMENT;
+  const hipStream_t s = as_stream(stream);
+  if (const ep_status_t st = ensure_device(g, s); st != EP_OK) return st;
+  h->stream = s;
+  const int64_t es = packed ? 1 : 2;
+  SortArgs a{};
+  a.x = static_cast<const uint8_t*>(rows->data);
+  a.ld_x = rows->strides[0] * es;
+  a.rows_x = rows->sizes[0];
+  a.out = static_cast<uint8_t*>(out->data);
+  a.ld_out = out->strides[0] * es;
+  a.rows_out = out->sizes[0];
+  a.bytes = static_cast<int32_t>(packed ? g->row_bytes : 2 * static_cast<int64_t>(g->cfg.hidden));
+  if (packed && out->sizes[1] >= g->row_pitch) a.pad = static_cast<int32_t>(g->row_pitch - g->row_bytes);
+  a.row = h->entry_row;
+  a.place = h->place;
+  a.n = h->n;
+  a.K = g->cfg.top_k;
+  a.max_blocks = dispatch_block_cap(g);
+  a.err = g->err;
+  const ep_status_t st = from_hip(launch_sort(a, s));
+  if (st == EP_OK) trace(g, "expert_sort", h->n);
+  return st;
+}
+
+EP_API ep_status_t ep_expert_sort_backward(ep_handle_t handle, const ep_tensor_t* grad_out, ep_tensor_t* grad_rows,
+                                           ep_stream_t stream) {
+  Handle* h = reinterpret_cast<Handle*>(handle);
+  if (!handle_ok(h)) return EP_ERR_INVALID_ARGUMENT;
+  if (const ep_status_t st = sorted_ready(h); st != EP_OK) return st;
+  if (!bf16_rows(h->g, grad_out) || !bf16_rows(h->g, grad_rows)) return EP_ERR_INVALID_ARGUMENT;
+  return unsort(h, grad_out, nullptr, grad_rows, stream, "expert_sort_backward");
+}
+
+EP_API ep_status_t ep_expert_unsort(ep_handle_t handle, const ep_tensor_t* expert_out, const ep_tensor_t* topk_weights,
+                                    ep_tensor_t* out, ep_stream_t stream) {
+  Handle* h = reinterpret_cast<Handle*>(handle);
+  if (!handle_ok(h)) return EP_ERR_INVALID_ARGUMENT;
+  if (const ep_status_t st = sorted_ready(h); st != EP_OK) return st;
+  if (!bf16_rows(h->g, expert_out) || !entry_weights(h, topk_weights) || !bf16_rows(h->g, out))
+    return EP_ERR_INVALID_ARGUMENT;
+  return unsort(h, expert_out, topk_weights, out, stream, "expert_unsort");
+}
+
+EP_API ep_status_t ep_expert_unsort_backward(ep_handle_t handle, const ep_tensor_t* grad_out,
+                                             const ep_tensor_t* expert_out, const ep_tensor_t* topk_weights,
+                                             ep_tensor_t* grad_expert_out, ep_tensor_t* grad_weights,
+                                             ep_stream_t stream) {
+  Handle* h = reinterpret_cast<Handle*>(handle);
+  if (!handle_ok(h)) return EP_ERR_INVALID_ARGUMENT;
+  Group* g = h->g;
+  if (const ep_status_t st = sorted_ready(h); st != EP_OK) return st;
+  if (!bf16_rows(g, grad_out) || (expert_out && !bf16_rows(g, expert_out)) || !entry_weights(h, topk_weights) ||
+      !bf16_rows(g, grad_expert_out) || (grad_weights && (!expert_out || !entry_weights(h, grad_weights))))
+    return EP_ERR_INVALID_ARGUMENT;
+  const hipStream_t s = as_stream(stream);
+  if (const ep_status_t st = ensure_device(g, s); st != EP_OK) return st;
+  h->stream = s;
+  UnsortBwdArgs a{};
+  a.g = static_cast<const uint16_t*>(grad_out->data);
+  a.ld_g = grad_out->strides[0];
+  a.rows_g = grad_out->sizes[0];
+  if (grad_weights) {   // without them the rows themselves are not read
+    a.y = static_cast<const uint16_t*>(expert_out->data);
+    a.ld_y = expert_out->strides[0];
+    a.dw = static_cast<float*>(grad_weights->data);
+  }
+  a.dy = static_cast<uint16_t*>(grad_expert_out->data);
+  a.ld_dy = grad_expert_out->strides[0];
+  a.rows_y = expert_out ? std::min(expert_out->sizes[0], grad_expert_out->sizes[0]) : grad_expert_out->sizes[0];
+  a.w = static_cast<const float*>(topk_weights->data);
+  a.row = h->entry_row;
+  a.place = h->place;
+  a.n = h->n;
+  a.K = g->cfg.top_k;
+  a.H = g->cfg.hidden;
+  a.max_blocks = dispatch_block_cap(g);
+  a.err = g->err;
+  const ep_status_t st = from_hip(launch_unsort_backward(a, s));
+  if (st == EP_OK) trace(g, "expert_unsort_backward", h->n);
+  return st;
+}
+
+// ===========================================================================
 // The experts' products
 // ===========================================================================
 
@@ -1175,7 +1334,8 @@ bool holds_slots(const Group* g, const ep_tensor_t& t) {
 }
 
 ep_status_t expert_ready(const Handle* h) {
-  if (h->g->s2_rank) return EP_ERR_UNSUPPORTED;   // a row belongs to several experts there
+  // a row of a rank belongs to several experts; in expert order each is one's
+  if (h->g->s2_rank && !h->g->sorted) return EP_ERR_UNSUPPORTED;
   return h->pend == Handle::kPendNone ? EP_OK : EP_ERR_INVALID_ARGUMENT;
 }
 
@@ -1186,7 +1346,7 @@ ExpertRows rows_of_experts(const Handle* h, int64_t limit) {
   r.limit = limit;
   r.err = g->err;
   r.sources = 1;
-  r.count = h->c2;
+  r.count = g->sorted ? h->cx : h->c2;
   if (g->cfg.mode == EP_MODE_LL) {
     r.stride = g->cfg.num_src_ranks * g->cfg.max_tokens_per_rank;
     r.slots = g->cfg.max_tokens_per_rank;
@@ -1434,7 +1594,7 @@ EP_API ep_status_t ep_expert_quantize(ep_handle_t handle, const ep_tensor_t* x_i
     a.tps = h->tps;
     a.slots = g->cfg.max_tokens_per_rank;
   } else {
-    a.count = h->c2;
+    a.count = g->sorted ? h->cx : h->c2;
   }
   a.H = static_cast<int>(C);
   a.rows = std::min({x.sizes[0], qd.sizes[0], sd.sizes[0]});

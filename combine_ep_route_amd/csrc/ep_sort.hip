@@ -1,0 +1,281 @@
+// Between the ranks' stage-2 rows and rows in expert order: what a rank does with its received rows before and
+// behind its experts when a token comes to it once (per-rank stage 2), and the adjoints.
+//
+// Entry k of token i has a row of its rank, row(i,k), which entries on the same rank share, and a place in expert
+// order, place(i,k), of its own; both were worked out with the handle.
+//   sort:             S[place(i,k)] = X[row(i,k)]
+//   unsort:           P[r] = bf16_rne(fma chain in k order from +0 of w[i,k] Y[place(i,k)]) over the entries on r
+//   sort, backward:   the same with unit weights
+//   unsort, backward: dY[place(i,k)] = bf16_rne(w[i,k] dP[row(i,k)]), dw[i,k] = <dP[row(i,k)], Y[place(i,k)]>
+//
+// All move rows and compute next to nothing.  Work is split by token: a token's entries hold all that its rows
+// need, so a shared row is read once and a sum needs no atomics.  A lane owns 16 bytes of a row.  Rows and places
+// of a token are the same for all lanes (scalar loads), and so are the branches on them.
+#include "ep_internal.h"
+
+namespace ep {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kBatch = 8;   // entries whose loads are started before the first is used
+
+__device__ __forceinline__ u32x4 load16(const void* p) {
+  return __builtin_nontemporal_load(static_cast<const u32x4*>(p));
+}
+__device__ __forceinline__ void store16(u32x4 v, void* p) { __builtin_nontemporal_store(v, static_cast<u32x4*>(p)); }
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(lo)) |
+         static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(hi))) << 16;
+}
+__device__ __forceinline__ void unpack(u32x4 v, float (&f)[8]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    f[2 * q] = __uint_as_float(v[q] << 16);
+    f[2 * q + 1] = __uint_as_float(v[q] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ u32x4 pack(const float (&f)[8]) {
+  return {bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7])};
+}
+
+// Up to kBatch entries of a token from k0 on: row and place, -1 where there is none or the tensors do not hold it.
+struct Entries {
+  int32_t row[kBatch], place[kBatch];
+  bool beyond = false;
+  __device__ __forceinline__ Entries(const int32_t* rows, const int32_t* places, int64_t i, int K, int k0, int64_t rows_max,
+                                     int64_t places_max) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const bool in = k0 + b < K;
+      row[b] = in ? rows[i * K + k0 + b] : -1;
+      place[b] = in ? places[i * K + k0 + b] : -1;
+      beyond |= row[b] >= rows_max || place[b] >= places_max;
+      if (row[b] >= rows_max) row[b] = -1;
+      if (place[b] >= places_max) place[b] = -1;
+    }
+  }
+  // whether no entry before b in the batch has its row
+  __device__ __forceinline__ bool first(int b) const {
+    bool f = row[b] >= 0;
+#pragma unroll
+    for (int q = 0; q < b; ++q) f = f && row[q] != row[b];
+    return f;
+  }
+};
+
+__global__ __launch_bounds__(256) void sort_kernel(SortArgs a) {
+  const int at = (blockIdx.x * blockDim.x + threadIdx.x) * 16;
+  const int end = a.bytes + a.pad;
+  const bool whole = at + 16 <= a.bytes;
+  const int words = (end - at) >> 2;      // 4-byte words that this lane writes, four at most
+  for (int64_t i = blockIdx.y; i < a.n; i += gridDim.y) {
+    for (int k0 = 0; k0 < a.K; k0 += kBatch) {
+      const Entries t(a.row, a.place, i, a.K, k0, a.rows_x, a.rows_out);
+      if (t.beyond && at == 0) atomicOr(a.err, EP_DEVERR_ROW_RANGE);
+      u32x4 v[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (!t.first(b) || words <= 0) continue;
+        const uint8_t* p = a.x + t.row[b] * a.ld_x + at;
+        if (whole) {
+          v[b] = load16(p);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[b][q] = at + 4 * q < a.bytes ? reinterpret_cast<const uint32_t*>(p)[q] : 0;
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (!t.first(b) || words <= 0) continue;
+#pragma unroll
+        for (int q = b; q < kBatch; ++q) {
+          if (t.row[q] != t.row[b] || t.place[q] < 0) continue;
+          uint8_t* p = a.out + t.place[q] * a.ld_out + at;
+          if (words >= 4) {
+            store16(v[b], p);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+              if (j < words) reinterpret_cast<uint32_t*>(p)[j] = v[b][j];
+          }
+        }
+      }
+    }
+  }
+}
+
+// FEW: K <= kBatch, and all of a token's rows are loaded before the first sum.  Else the entries are taken row by
+// row, kBatch loads at a time.
+template <bool FEW>
+__global__ __launch_bounds__(256) void unsort_kernel(UnsortArgs a) {
+  const int c = blockIdx.x * blockDim.x + threadIdx.x;
+  const bool active = c < a.H / 8;
+  auto add = [&](float (&acc)[8], u32x4 v, float w) {
+    float f[8];
+    unpack(v, f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[q] = __builtin_fmaf(w, f[q], acc[q]);
+  };
+  for (int64_t i = blockIdx.y; i < a.n; i += gridDim.y) {
+    if constexpr (FEW) {
+      const Entries t(a.row, a.place, i, a.K, 0, a.rows_out, a.rows_y);
+      if (t.beyond && c == 0) atomicOr(a.err, EP_DEVERR_ROW_RANGE);
+      u32x4 v[kBatch];
+      float w[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        w[b] = b < a.K ? (a.w ? a.w[i * a.K + b] : 1.0f) : 0.0f;
+        if (t.place[b] >= 0 && active) v[b] = load16(a.y + t.place[b] * a.ld_y + 8 * c);
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (!t.first(b)) continue;
+        float acc[8] = {};
+#pragma unroll
+        for (int q = b; q < kBatch; ++q)
+          if (t.row[q] == t.row[b] && t.place[q] >= 0) add(acc, v[q], w[q]);
+        if (active) store16(pack(acc), a.out + t.row[b] * a.ld_out + 8 * c);
+      }
+    } else {
+      uint32_t left = 0;   // entries whose row is still to come
+      for (int k = 0; k < a.K; ++k) left |= a.row[i * a.K + k] >= 0 ? 1u << k : 0u;
+      while (left) {
+        const int32_t r = a.row[i * a.K + __builtin_ctz(left)];
+        const bool out_in = r < a.rows_out;
+        if (!out_in && c == 0) atomicOr(a.err, EP_DEVERR_ROW_RANGE);
+        float acc[8] = {};
+        uint32_t mine = 0;   // the entries on r
+        for (int k = __builtin_ctz(left); k < a.K; ++k) mine |= a.row[i * a.K + k] == r ? 1u << k : 0u;
+        left &= ~mine;
+        while (mine) {
+          u32x4 v[kBatch];
+          float w[kBatch];
+          bool on[kBatch];
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int k = mine ? __builtin_ctz(mine) : 0;
+            const int32_t p = mine ? a.place[i * a.K + k] : -1;
+            on[b] = p >= 0 && p < a.rows_y;
+            if (p >= a.rows_y && c == 0) atomicOr(a.err, EP_DEVERR_ROW_RANGE);
+            w[b] = a.w ? a.w[i * a.K + k] : 1.0f;
+            if (on[b] && active) v[b] = load16(a.y + p * a.ld_y + 8 * c);
+            mine &= mine - 1;
+          }
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b)
+            if (on[b]) add(acc, v[b], w[b]);
+        }
+        if (active && out_in) store16(pack(acc), a.out + r * a.ld_out + 8 * c);
+      }
+    }
+  }
+}
+
+// One workgroup a token, which sums the dot products over its threads' chunks in a fixed order: per-thread fp32
+// fma chains, a tree over the lanes, the waves in turn.
+__global__ __launch_bounds__(512) void unsort_backward_kernel(UnsortBwdArgs a) {
+  __shared__ float part[kBatch][8];
+  const int C = a.H / 8;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  for (int64_t i = blockIdx.x; i < a.n; i += gridDim.x) {
+    for (int k0 = 0; k0 < a.K; k0 += kBatch) {
+      const Entries t(a.row, a.place, i, a.K, k0, a.rows_g, a.rows_y);
+      if (t.beyond && threadIdx.x == 0) atomicOr(a.err, EP_DEVERR_ROW_RANGE);
+      float w[kBatch], dot[kBatch] = {};
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) w[b] = k0 + b < a.K ? a.w[i * a.K + k0 + b] : 0.0f;
+      for (int c = threadIdx.x; c < C; c += blockDim.x) {
+        u32x4 g[kBatch], y[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          if (t.first(b)) g[b] = load16(a.g + t.row[b] * a.ld_g + 8 * c);
+          if (a.y && t.row[b] >= 0 && t.place[b] >= 0) y[b] = load16(a.y + t.place[b] * a.ld_y + 8 * c);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          if (!t.first(b)) continue;
+          float f[8];
+          unpack(g[b], f);
+#pragma unroll
+          for (int q = b; q < kBatch; ++q) {
+            if (t.row[q] != t.row[b] || t.place[q] < 0) continue;
+            float o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = w[q] * f[j];
+            store16(pack(o), a.dy + t.place[q] * a.ld_dy + 8 * c);
+            if (a.y) {
+              float z[8];
+              unpack(y[q], z);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) dot[q] = __builtin_fmaf(f[j], z[j], dot[q]);
+            }
+          }
+        }
+      }
+      if (a.dw) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          float v = dot[b];
+#pragma unroll
+          for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+          if (lane == 0) part[b][wave] = v;
+        }
+        __syncthreads();
+        const int k = k0 + threadIdx.x;
+        if (threadIdx.x < kBatch && k < a.K) {
+          float sum = 0.0f;   // of an entry without a row or beyond the tensors: nothing was added
+          for (int q = 0; q < waves; ++q) sum += part[threadIdx.x][q];
+          a.dw[i * a.K + k] = sum;
+        }
+        __syncthreads();
+      }
+    }
+  }
+}
+
+// Threads of a workgroup for rows of C 16-byte chunks, `most` at most: the largest number of waves that the chunks
+// fill whole, or as many waves as they need.
+int threads_for(int C, int most) {
+  for (int t = most; t >= 128; t -= 64)
+    if (C % t == 0) return t;
+  return C >= most ? most : (C + 63) / 64 * 64;
+}
+
+// Column blocks and tokens; with a cap on the blocks, fewer tokens at a time.
+dim3 grid_for(int64_t n, int cols, int max_blocks) {
+  int64_t rows = n;
+  if (max_blocks > 0) rows = rows < max_blocks / cols ? rows : max_blocks / cols > 0 ? max_blocks / cols : 1;
+  return dim3(static_cast<unsigned>(cols), static_cast<unsigned>(rows < 65535 ? rows : 65535));
+}
+
+}  // namespace
+
+hipError_t launch_sort(const SortArgs& a, hipStream_t stream) {
+  if (a.n == 0) return hipSuccess;
+  const int C = (a.bytes + a.pad + 15) / 16, threads = threads_for(C, 256);
+  sort_kernel<<<grid_for(a.n, (C + threads - 1) / threads, a.max_blocks), threads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_unsort(const UnsortArgs& a, hipStream_t stream) {
+  if (a.n == 0) return hipSuccess;
+  const int C = a.H / 8, threads = threads_for(C, 256);
+  const dim3 grid = grid_for(a.n, (C + threads - 1) / threads, a.max_blocks);
+  if (a.K <= kBatch) unsort_kernel<true><<<grid, threads, 0, stream>>>(a);
+  else unsort_kernel<false><<<grid, threads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_unsort_backward(const UnsortBwdArgs& a, hipStream_t stream) {
+  if (a.n == 0) return hipSuccess;
+  const int threads = threads_for(a.H / 8, 512);
+  int64_t blocks = a.n;
+  if (a.max_blocks > 0 && blocks > a.max_blocks) blocks = a.max_blocks;
+  const dim3 grid(grid_blocks(blocks, threads));
+  unsort_backward_kernel<<<grid, threads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace ep

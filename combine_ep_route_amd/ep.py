@@ -125,7 +125,8 @@ def make_config(mode="ht", num_nodes=8, ranks_per_node=8, num_experts=256, top_k
     c.max_handles = max_handles
     c.num_cus = num_cus
     c.ll_buffers = ll_buffers
-    c.ht_stage2 = {"expert": A.EP_HT_STAGE2_PER_EXPERT, "rank": A.EP_HT_STAGE2_PER_RANK}[ht_stage2] \
+    c.ht_stage2 = {"expert": A.EP_HT_STAGE2_PER_EXPERT, "rank": A.EP_HT_STAGE2_PER_RANK,
+                   "rank_sorted": A.EP_HT_STAGE2_PER_RANK_SORTED}[ht_stage2] \
         if isinstance(ht_stage2, str) else ht_stage2
     c.ht_buffers = ht_buffers
     c.alloc_fn = alloc_fn if alloc_fn is not None else A.ALLOC_FN()
@@ -223,7 +224,7 @@ def ep_combine(handle: Handle, expert_out: torch.Tensor, topk_weights: Optional[
         handle._staged = (expert_out, topk_weights, out)   # alive until ep_complete
 
 
-def ep_combine_backward(handle: Handle, grad_out: torch.Tensor, topk_weights: torch.Tensor,
+def ep_combine_backward(handle: Handle, grad_out: torch.Tensor, topk_weights: Optional[torch.Tensor],
                         grad_expert_out: torch.Tensor, expert_out: Optional[torch.Tensor] = None,
                         grad_weights: Optional[torch.Tensor] = None, stream=None) -> None:
     g = desc(grad_out, A.EP_TAG_TOKENS)
@@ -245,6 +246,32 @@ def ep_dispatch_backward(handle: Handle, grad_expert_in: torch.Tensor, grad_toke
 def ep_complete(handle: Handle, stream=None) -> None:
     _check("ep_complete", A.lib().ep_complete(handle.ptr, _stream(stream)))
     handle._staged = None
+
+
+def ep_expert_sort(handle: Handle, rows: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    r, o = desc(rows, A.EP_TAG_TOKENS), desc(out, A.EP_TAG_TOKENS)
+    _check("ep_expert_sort", A.lib().ep_expert_sort(handle.ptr, _ref(r), _ref(o), _stream(stream)))
+
+
+def ep_expert_sort_backward(handle: Handle, grad_out: torch.Tensor, grad_rows: torch.Tensor, stream=None) -> None:
+    g, r = desc(grad_out, A.EP_TAG_TOKENS), desc(grad_rows, A.EP_TAG_TOKENS)
+    _check("ep_expert_sort_backward", A.lib().ep_expert_sort_backward(handle.ptr, _ref(g), _ref(r), _stream(stream)))
+
+
+def ep_expert_unsort(handle: Handle, expert_out: torch.Tensor, topk_weights: torch.Tensor, out: torch.Tensor,
+                     stream=None) -> None:
+    y, w, o = desc(expert_out, A.EP_TAG_TOKENS), desc(topk_weights, A.EP_TAG_TOPK_WEIGHTS), desc(out, A.EP_TAG_TOKENS)
+    _check("ep_expert_unsort", A.lib().ep_expert_unsort(handle.ptr, _ref(y), _ref(w), _ref(o), _stream(stream)))
+
+
+def ep_expert_unsort_backward(handle: Handle, grad_out: torch.Tensor, topk_weights: torch.Tensor,
+                              grad_expert_out: torch.Tensor, expert_out: Optional[torch.Tensor] = None,
+                              grad_weights: Optional[torch.Tensor] = None, stream=None) -> None:
+    g, y = desc(grad_out, A.EP_TAG_TOKENS), desc(expert_out, A.EP_TAG_TOKENS)
+    w, dw = desc(topk_weights, A.EP_TAG_TOPK_WEIGHTS), desc(grad_weights, A.EP_TAG_TOPK_WEIGHTS)
+    dy = desc(grad_expert_out, A.EP_TAG_TOKENS)
+    _check("ep_expert_unsort_backward", A.lib().ep_expert_unsort_backward(handle.ptr, _ref(g), _ref(y), _ref(w),
+                                                                          _ref(dy), _ref(dw), _stream(stream)))
 
 
 _ACTIVATIONS = {"silu": A.EP_ACT_SILU, "gelu_tanh": A.EP_ACT_GELU_TANH}

@@ -22,8 +22,8 @@
  *    ep_stream_t, i.e. a hipStream_t; NULL is the default stream) and returns
  *    without waiting, except the functions documented as blocking.
  *  - A group, and every handle made from it, is used from one stream at a
- *    time, except where a function says otherwise (the experts' products and
- *    ep_expert_quantize); the library takes no locks, so host threads that
+ *    time, except where a function says otherwise (the experts' products,
+ *    ep_expert_quantize, the moves into expert order and back); the library takes no locks, so host threads that
  *    share a group take turns.
  *  - Arguments are validated on the host before any HIP call; a rejected call
  *    enqueues nothing.  Routing entries are checked on the device and
@@ -64,8 +64,16 @@ typedef enum { EP_MODE_LL = 0, EP_MODE_HT = 1 } ep_mode_t;
  *   PER_RANK:   one row per (token, distinct destination rank), grouped by
  *               rank, with the token's entries local to that rank (DeepEP's
  *               received top-k form); the experts' weighted partial sums come
- *               back per rank and the combine sums them. */
-typedef enum { EP_HT_STAGE2_PER_EXPERT = 0, EP_HT_STAGE2_PER_RANK = 1 } ep_ht_stage2_t;
+ *               back per rank and the combine sums them.
+ *   PER_RANK_SORTED: PER_RANK, and a handle's creation also works out each
+ *               entry's place in expert order, which ep_expert_sort and
+ *               ep_expert_unsort go by; the experts' products take rows in
+ *               that order. */
+typedef enum {
+    EP_HT_STAGE2_PER_EXPERT = 0,
+    EP_HT_STAGE2_PER_RANK = 1,
+    EP_HT_STAGE2_PER_RANK_SORTED = 3   /* PER_RANK with the bit 2 */
+} ep_ht_stage2_t;
 
 /* Element types (NCCL-EP tensor abstraction: FP32/BF16/FP16/FP8). */
 typedef enum {
@@ -135,7 +143,8 @@ typedef struct {
     int32_t num_cus;             /* cap on CUs used by dispatch/combine; 0=all */
     int32_t ll_buffers;          /* LL receive buffers used in turn: 1 or 2;
                                     0 means 2 (double buffering, NCCL-EP LL) */
-    int32_t ht_stage2;           /* ep_ht_stage2_t (HT only)                   */
+    int32_t ht_stage2;           /* ep_ht_stage2_t (HT only; the experts' places
+                                    cost a handle 12 bytes an entry more)    */
     int32_t ht_buffers;          /* HT stage-row sets (stage-1 and stage-2 rows
                                     with metadata) used in turn: 1 or 2; 0
                                     means 1.  With 2 a dispatch may run while
@@ -272,16 +281,19 @@ typedef enum {
     EP_MAP_LL_SLOT = 0,   /* I32 [n, K]: global slot (e*S+s)*T_max + slot, or -1 */
     EP_MAP_LL_COUNT = 1,  /* I32 [E, S]                                          */
     EP_MAP_HT_NODE_ROW = 2, /* I32 [n, N]: global stage-1 row, or -1            */
-    EP_MAP_HT_ROW = 3,    /* I32 [n, K]: global stage-2 row, or -1.  PER_RANK: the
+    EP_MAP_HT_ROW = 3,    /* I32 [n, K]: global stage-2 row, or -1.  PER_RANK(_SORTED): the
                              row of the entry's rank at the token's first entry
                              on that rank, -1 at its other entries            */
     EP_MAP_HT_RANK_COUNT = 4,  /* I32 [R]: stage-1 rows per destination rank    */
     EP_MAP_HT_RANK_OFFSET = 5, /* I32 [R]: exclusive prefix sum of the above    */
     EP_MAP_HT_EXPERT_COUNT = 6,  /* I32 [E]: stage-2 rows per expert
-                                    (PER_RANK: [R] rows per rank)             */
-    EP_MAP_HT_EXPERT_OFFSET = 7  /* exclusive prefix sum of the above          */
+                                    (PER_RANK(_SORTED): [R] rows per rank)    */
+    EP_MAP_HT_EXPERT_OFFSET = 7, /* exclusive prefix sum of the above          */
+    EP_MAP_HT_SORTED_ROW = 8,  /* PER_RANK_SORTED: I32 [n, K]: the entry's row in
+                             expert order, or -1                               */
+    EP_MAP_HT_SORTED_COUNT = 9 /* PER_RANK_SORTED: I32 [E]: rows per expert     */
 } ep_map_t;
-/* The counts are written when the handle is made.  The slot / row maps and
+/* The counts and EP_MAP_HT_SORTED_ROW are written when the handle is made.  The slot / row maps and
  * the HT offsets are written by the handle's dispatch; asked for before a
  * dispatch has run, they are computed by a maps-only pass that this call
  * enqueues on the handle's stream (no rows are written).  The same pass goes
@@ -422,9 +434,9 @@ typedef enum {
     EP_BUF_HT_STAGE2_SRC = 7,    /* I32 [S*T_max*K]                           */
     EP_BUF_HT_STAGE2_TOKEN = 8,  /* I32 [S*T_max*K]                           */
     EP_BUF_HT_STAGE2_K = 9,      /* I32 [S*T_max*K]: k of the row's (first) entry */
-    EP_BUF_HT_STAGE2_TOPK = 10,  /* PER_RANK: I32 [S*T_max*K, K] the token's entries
+    EP_BUF_HT_STAGE2_TOPK = 10,  /* PER_RANK(_SORTED): I32 [S*T_max*K, K] the token's entries
                                     on the row's rank as local expert ids, else -1 */
-    EP_BUF_HT_STAGE2_WEIGHTS = 11 /* PER_RANK: F32 [S*T_max*K, K] their weights, else 0 */
+    EP_BUF_HT_STAGE2_WEIGHTS = 11 /* PER_RANK(_SORTED): F32 [S*T_max*K, K] their weights, else 0 */
 } ep_buffer_t;
 ep_status_t ep_get_buffer(ep_group_t group, int32_t which, ep_tensor_t *view);
 
@@ -523,7 +535,10 @@ ep_status_t ep_complete(ep_handle_t handle, ep_stream_t stream);
  *                     [E, S*T_max, H]).
  *   grad_weights    : optional F32 [n, K] contiguous.
  * EP_ERR_UNSUPPORTED with the PER_RANK stage 2 (the experts apply the
- * weights there, so the combine has none to differentiate). */
+ * weights there, so the combine has none to differentiate).  With
+ * PER_RANK_SORTED expert_out, topk_weights and grad_weights are NULL and the
+ * weights 1: every rank's row of a token gets the token's gradient, which
+ * ep_expert_unsort_backward takes. */
 ep_status_t ep_combine_backward(ep_handle_t handle, const ep_tensor_t *grad_out,
                                 const ep_tensor_t *expert_out,
                                 const ep_tensor_t *topk_weights,
@@ -538,6 +553,79 @@ ep_status_t ep_combine_backward(ep_handle_t handle, const ep_tensor_t *grad_out,
  *   grad_tokens    : BF16 [n, H], rows 16-byte aligned. */
 ep_status_t ep_dispatch_backward(ep_handle_t handle, const ep_tensor_t *grad_expert_in,
                                  ep_tensor_t *grad_tokens, ep_stream_t stream);
+
+/* ----------------------------------------------------------------------- */
+/* Rows of ranks in expert order, and back                                   */
+/* ----------------------------------------------------------------------- */
+
+/* With the per-rank stage 2 a token comes to a rank once, however many of the
+ * rank's experts it names.  In front of the experts the rank copies its rows
+ * into expert order, one for each entry, and behind them it weights and sums
+ * an entry's results into one row again, which ep_combine takes.  These calls
+ * do that for all ranks at once (a rank's experts are neighbours, so its rows
+ * in expert order are one run), and so do their adjoints.  They need a group
+ * with EP_HT_STAGE2_PER_RANK_SORTED.
+ *
+ * Entry (i, k), if valid, has
+ *   row(i,k):   the stage-2 row of its rank, shared by the token's entries on
+ *               that rank (EP_MAP_HT_ROW at the first of them);
+ *   place(i,k): its row in expert order (EP_MAP_HT_SORTED_ROW): experts in
+ *               order, (source, token) ascending inside an expert -- the
+ *               stage-2 row that PER_EXPERT would give it.
+ * The experts' products and ep_expert_quantize of such a group take rows at
+ * the places ("rows at the dispatch geometry" below are [rows, C] with one row
+ * for each place); ep_combine and ep_dispatch_backward take the ranks' rows.
+ *
+ * "Ranks' rows" and "sorted rows" are 2-D, innermost contiguous, data and rows
+ * 16-byte aligned, with at least as many rows as are in use (n*K always do).
+ * Rows that no entry has are neither read nor written.  An entry whose row or
+ * place the tensors do not hold is left out (a rank's row that is held is still
+ * the sum of the others) and sets EP_DEVERR_ROW_RANGE.  Outputs overlap
+ * nothing.  What the calls need of the handle is written when it is made: once
+ * that work has run, they may run on several streams at the same time, each
+ * with outputs of its own, and each can be captured.  Repeated calls give the
+ * same bits.
+ * Errors: EP_ERR_INVALID_ARGUMENT (handle, descriptors, shapes, alignment),
+ * EP_ERR_UNSUPPORTED (a group of another stage-2 kind). */
+
+/* out[place(i,k)] = rows[row(i,k)].
+ *   rows : U8 [rows, >= row bytes] as the dispatch packed them
+ *          (EP_BUF_HT_STAGE2), or BF16 [rows, H].
+ *   out  : the same type.  Of a U8 row as wide as the buffers' row pitch (the
+ *          row's bytes up to a multiple of 128) what lies between the row's end
+ *          and that multiple is written as zeros; other bytes behind a row are
+ *          not written. */
+ep_status_t ep_expert_sort(ep_handle_t handle, const ep_tensor_t *rows, ep_tensor_t *out,
+                           ep_stream_t stream);
+
+/* Its adjoint (the quantisation of packed rows counts as the identity):
+ *   grad_rows[r] = bf16_rne(fp32 sum in k order from +0 of grad_out[place(i,k)])
+ * over the entries with row(i,k) = r.  Both BF16 [rows, H]. */
+ep_status_t ep_expert_sort_backward(ep_handle_t handle, const ep_tensor_t *grad_out,
+                                    ep_tensor_t *grad_rows, ep_stream_t stream);
+
+/* out[r] = bf16_rne(fma chain in k order from +0 of
+ *                   topk_weights[i][k] * expert_out[place(i,k)])   in fp32
+ * over the entries with row(i,k) = r.
+ *   expert_out   : BF16 sorted rows [rows, H].
+ *   topk_weights : F32 [n, K] contiguous.
+ *   out          : BF16 ranks' rows [rows, H]: ep_combine's expert_out. */
+ep_status_t ep_expert_unsort(ep_handle_t handle, const ep_tensor_t *expert_out,
+                             const ep_tensor_t *topk_weights, ep_tensor_t *out, ep_stream_t stream);
+
+/* Its adjoint:
+ *   grad_expert_out[place(i,k)] = bf16_rne(topk_weights[i][k] * grad_out[row(i,k)])
+ *   grad_weights[i][k] = sum over h of grad_out[row(i,k)][h] * expert_out[place(i,k)][h]
+ *                        in fp32, in a fixed order; 0 for an invalid entry and
+ *                        for one that the tensors do not hold.
+ *   grad_out        : BF16 ranks' rows: what ep_combine_backward gives.
+ *   expert_out      : BF16 sorted rows, or NULL (then grad_weights must be NULL).
+ *   grad_expert_out : BF16 sorted rows.
+ *   grad_weights    : optional F32 [n, K] contiguous. */
+ep_status_t ep_expert_unsort_backward(ep_handle_t handle, const ep_tensor_t *grad_out,
+                                      const ep_tensor_t *expert_out, const ep_tensor_t *topk_weights,
+                                      ep_tensor_t *grad_expert_out, ep_tensor_t *grad_weights,
+                                      ep_stream_t stream);
 
 /* ----------------------------------------------------------------------- */
 /* The experts' products                                                     */
@@ -570,7 +658,7 @@ ep_status_t ep_dispatch_backward(ep_handle_t handle, const ep_tensor_t *grad_exp
  * Errors of all of them: EP_ERR_INVALID_ARGUMENT (handle, descriptors, shapes,
  * alignment, an unknown activation, or a staged operation pending on the
  * handle); EP_ERR_UNSUPPORTED with the PER_RANK stage 2 (its rows belong to
- * several experts), for sizes above 2^20, for strides that put 256 rows of a
+ * several experts; PER_RANK_SORTED takes the sorted ones), for sizes above 2^20, for strides that put 256 rows of a
  * tensor (LL with several sources: the slots of one expert) or of a weight
  * matrix 2^31 bytes or more apart, and for more tiles than one grid holds
  * (about four million).  What a call needs of the handle is written when the
