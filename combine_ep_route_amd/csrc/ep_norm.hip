@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "ep_internal.h"
+#include "ep_wave_dev.h"
 
 namespace ep {
 namespace norm {
@@ -13,20 +14,6 @@ constexpr int kMaxThreads = 1024;
 enum Gate { kNone, kChannel, kToken };
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
-
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float add_dpp(float v) {
-  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
-}
-// The sum over a wave, in lane 63: pairs, quads, halves and whole rows of 16 lanes, then the rows.
-__device__ __forceinline__ float add_wave(float v) {
-  v = add_dpp<0xb1, 0xf>(v);    // lanes 1 0 3 2 of each quad
-  v = add_dpp<0x4e, 0xf>(v);    // lanes 2 3 0 1
-  v = add_dpp<0x141, 0xf>(v);   // half rows mirrored
-  v = add_dpp<0x140, 0xf>(v);   // rows mirrored
-  v = add_dpp<0x142, 0xa>(v);   // each row's last lane to the next row
-  return add_dpp<0x143, 0xc>(v);   // lane 31 to the upper rows
-}
 
 // Sums over the workgroup's waves, in a fixed order.  Consecutive calls take turns between two buffers: a wave
 // that writes one again has passed the barrier of the call between, before which all waves have read it.
@@ -45,7 +32,7 @@ struct BlockSum {
     turn ^= 1;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      v[i] = add_wave(v[i]);
+      v[i] = wave::add_wave(v[i]);
       if (lane_id() == 63) p[i * 16 + (threadIdx.x >> 6)] = v[i];
     }
     __syncthreads();

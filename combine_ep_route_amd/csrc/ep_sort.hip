@@ -8,10 +8,16 @@
 //   sort, backward:   the same with unit weights
 //   unsort, backward: dY[place(i,k)] = bf16_rne(w[i,k] dP[row(i,k)]), dw[i,k] = <dP[row(i,k)], Y[place(i,k)]>
 //
-// All move rows and compute next to nothing.  Work is split by token: a token's entries hold all that its rows
-// need, so a shared row is read once and a sum needs no atomics.  A lane owns 16 bytes of a row.  Rows and places
+// All move rows and compute next to nothing, so the memory bounds them (a copy of 2 GiB: 4.87 TB/s of reads and
+// writes).  Work is split by token: a token's entries hold all that its rows need, so a sum needs no atomics.  A lane
+// owns 16 bytes of a row and starts the loads of all of a token's entries before it uses the first.  Rows and places
 // of a token are the same for all lanes (scalar loads), and so are the branches on them.
+// 4096 tokens of 8 of 256 experts on 64 ranks, hidden 7168, 30714 rows of ranks (bytes that have to move):
+//   sort, FP8 rows     96.5 us, 4.86 TB/s      unsort                      174 us, 5.22 TB/s
+//   sort, backward    700 us, 5.20 TB/s (16384 tokens)     unsort, backward   279 us, 4.95 TB/s
+// 128 tokens: unsort 7.7 us, 3.7 TB/s; the smallest sort (128 tokens, 512-byte rows) 3.0 us, a launch.
 #include "ep_internal.h"
+#include "ep_wave_dev.h"
 
 namespace ep {
 namespace {
@@ -56,15 +62,18 @@ struct Entries {
       if (place[b] >= places_max) place[b] = -1;
     }
   }
-  // whether no entry before b in the batch has its row
-  __device__ __forceinline__ bool first(int b) const {
-    bool f = row[b] >= 0;
+  __device__ __forceinline__ bool on(int b) const { return row[b] >= 0 && place[b] >= 0; }
+  // Bits q > b of the entries that share b's row.
+  __device__ __forceinline__ uint32_t behind(int b) const {
+    uint32_t m = 0;
 #pragma unroll
-    for (int q = 0; q < b; ++q) f = f && row[q] != row[b];
-    return f;
+    for (int q = b + 1; q < kBatch; ++q) m |= row[q] == row[b] ? 1u << q : 0u;
+    return m;
   }
 };
 
+// Every entry loads its row itself: entries of a token that share one meet in the cache (loading it once for all of
+// them took the branches' 51 spilled scalars: the smallest sort 3.45 us, so 3.0).
 __global__ __launch_bounds__(256) void sort_kernel(SortArgs a) {
   const int at = (blockIdx.x * blockDim.x + threadIdx.x) * 16;
   const int end = a.bytes + a.pad;
@@ -77,7 +86,7 @@ __global__ __launch_bounds__(256) void sort_kernel(SortArgs a) {
       u32x4 v[kBatch];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        if (!t.first(b) || words <= 0) continue;
+        if (!t.on(b) || words <= 0) continue;
         const uint8_t* p = a.x + t.row[b] * a.ld_x + at;
         if (whole) {
           v[b] = load16(p);
@@ -88,18 +97,14 @@ __global__ __launch_bounds__(256) void sort_kernel(SortArgs a) {
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        if (!t.first(b) || words <= 0) continue;
+        if (!t.on(b) || words <= 0) continue;
+        uint8_t* p = a.out + t.place[b] * a.ld_out + at;
+        if (words >= 4) {
+          store16(v[b], p);
+        } else {
 #pragma unroll
-        for (int q = b; q < kBatch; ++q) {
-          if (t.row[q] != t.row[b] || t.place[q] < 0) continue;
-          uint8_t* p = a.out + t.place[q] * a.ld_out + at;
-          if (words >= 4) {
-            store16(v[b], p);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 3; ++j)
-              if (j < words) reinterpret_cast<uint32_t*>(p)[j] = v[b][j];
-          }
+          for (int j = 0; j < 3; ++j)
+            if (j < words) reinterpret_cast<uint32_t*>(p)[j] = v[b][j];
         }
       }
     }
@@ -129,13 +134,19 @@ __global__ __launch_bounds__(256) void unsort_kernel(UnsortArgs a) {
         w[b] = b < a.K ? (a.w ? a.w[i * a.K + b] : 1.0f) : 0.0f;
         if (t.place[b] >= 0 && active) v[b] = load16(a.y + t.place[b] * a.ld_y + 8 * c);
       }
+      uint32_t done = 0;   // entries whose row has been written
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        if (!t.first(b)) continue;
+        if (t.row[b] < 0 || (done >> b & 1)) continue;
+        const uint32_t more = t.behind(b);
+        done |= more;
         float acc[8] = {};
+        if (t.place[b] >= 0) add(acc, v[b], w[b]);
+        if (more) {
 #pragma unroll
-        for (int q = b; q < kBatch; ++q)
-          if (t.row[q] == t.row[b] && t.place[q] >= 0) add(acc, v[q], w[q]);
+          for (int q = b + 1; q < kBatch; ++q)
+            if ((more >> q & 1) && t.place[q] >= 0) add(acc, v[q], w[q]);
+        }
         if (active) store16(pack(acc), a.out + t.row[b] * a.ld_out + 8 * c);
       }
     } else {
@@ -174,11 +185,14 @@ __global__ __launch_bounds__(256) void unsort_kernel(UnsortArgs a) {
 }
 
 // One workgroup a token, which sums the dot products over its threads' chunks in a fixed order: per-thread fp32
-// fma chains, a tree over the lanes, the waves in turn.
+// fma chains, a tree over the lanes, the waves in turn.  An entry loads its gradient row itself; a row read once for
+// all entries on it, the entries' branches nested in its own, left the loads waiting for each other: 376 us for the
+// 4096 tokens above, 280 so.  Half as many entries at a time take 69 registers instead of 109, and the same time.
+// With the lanes' sums by shuffles 1000 tokens of 6 entries on 4 ranks, hidden 2048, take 15.8 us, so 14.8.
 __global__ __launch_bounds__(512) void unsort_backward_kernel(UnsortBwdArgs a) {
   __shared__ float part[kBatch][8];
   const int C = a.H / 8;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, at = threadIdx.x >> 6, waves = blockDim.x >> 6;
   for (int64_t i = blockIdx.x; i < a.n; i += gridDim.x) {
     for (int k0 = 0; k0 < a.K; k0 += kBatch) {
       const Entries t(a.row, a.place, i, a.K, k0, a.rows_g, a.rows_y);
@@ -190,37 +204,28 @@ __global__ __launch_bounds__(512) void unsort_backward_kernel(UnsortBwdArgs a) {
         u32x4 g[kBatch], y[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-          if (t.first(b)) g[b] = load16(a.g + t.row[b] * a.ld_g + 8 * c);
-          if (a.y && t.row[b] >= 0 && t.place[b] >= 0) y[b] = load16(a.y + t.place[b] * a.ld_y + 8 * c);
+          g[b] = t.on(b) ? *reinterpret_cast<const u32x4*>(a.g + t.row[b] * a.ld_g + 8 * c) : u32x4{0, 0, 0, 0};
+          y[b] = a.y && t.on(b) ? load16(a.y + t.place[b] * a.ld_y + 8 * c) : u32x4{0, 0, 0, 0};
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-          if (!t.first(b)) continue;
-          float f[8];
+          if (!t.on(b)) continue;
+          float f[8], o[8], z[8];
           unpack(g[b], f);
+          unpack(y[b], z);
 #pragma unroll
-          for (int q = b; q < kBatch; ++q) {
-            if (t.row[q] != t.row[b] || t.place[q] < 0) continue;
-            float o[8];
+          for (int j = 0; j < 8; ++j) o[j] = w[b] * f[j];
+          store16(pack(o), a.dy + t.place[b] * a.ld_dy + 8 * c);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = w[q] * f[j];
-            store16(pack(o), a.dy + t.place[q] * a.ld_dy + 8 * c);
-            if (a.y) {
-              float z[8];
-              unpack(y[q], z);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) dot[q] = __builtin_fmaf(f[j], z[j], dot[q]);
-            }
-          }
+          for (int j = 0; j < 8; ++j) dot[b] = __builtin_fmaf(f[j], z[j], dot[b]);
         }
       }
       if (a.dw) {
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-          float v = dot[b];
-#pragma unroll
-          for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-          if (lane == 0) part[b][wave] = v;
+          if (k0 + b >= a.K) continue;
+          const float v = wave::add_wave(dot[b]);
+          if (lane == 63) part[b][at] = v;
         }
         __syncthreads();
         const int k = k0 + threadIdx.x;
