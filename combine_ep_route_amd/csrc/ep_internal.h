@@ -427,7 +427,8 @@ struct AlongArgs {
 };
 hipError_t launch_linear(const AlongArgs& a, bool fp8, hipStream_t stream, bool check = false);
 hipError_t launch_gated(const AlongArgs& a, bool fp8, int act, hipStream_t stream, bool check = false);
-// out = the gradients of the gate's and of the up product
+// out = the gradients of the gate's and of the up product.  With x_scales x holds codes and k_bytes counts the
+// weights' bytes.
 hipError_t launch_gated_grad(const AlongArgs& a, int act, hipStream_t stream, bool check = false);
 
 struct RowGradArgs {
@@ -450,6 +451,8 @@ struct WeightGradArgs {
   int64_t ld_dy[2];
   const uint8_t* x;
   int64_t ld_x;
+  const uint8_t* x_scales;            // x holds codes, one float per 128 of a row; or null: bf16
+  int64_t ld_xs;
   uint8_t* dw[2];
   int64_t ld_dw[2], dw_expert[2];
 };

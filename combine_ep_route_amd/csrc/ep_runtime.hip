@@ -1436,13 +1436,17 @@ void add_part(RowGradArgs* r, const ep_tensor_t& dy, const ep_tensor_t* w) {
   r->w_expert[i] = w->strides[0] * 2;
 }
 
-WeightGradArgs weight_grad_args(const Handle* h, const ep_tensor_t& x, int64_t i, int64_t n, int64_t limit) {
+// With scales x holds codes.
+WeightGradArgs weight_grad_args(const Handle* h, const ep_tensor_t& x, const uint8_t* scales, int64_t ld_scales, int64_t i,
+                                int64_t n, int64_t limit) {
   WeightGradArgs r{};
   r.rows = rows_of_experts(h, limit);
   r.I = static_cast<int32_t>(i);
   r.H = static_cast<int32_t>(n);
   r.x = static_cast<const uint8_t*>(x.data);
-  r.ld_x = x.strides[0] * 2;
+  r.ld_x = x.strides[0] * (scales ? 1 : 2);
+  r.x_scales = scales;
+  r.ld_xs = ld_scales;
   return r;
 }
 
@@ -1497,10 +1501,35 @@ EP_API ep_status_t ep_expert_gated(ep_handle_t handle, const ep_tensor_t* rows, 
   return st;
 }
 
-EP_API ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_t* rows, const ep_tensor_t* w_gate,
-                                            const ep_tensor_t* w_up, const ep_tensor_t* grad_out, int32_t activation,
-                                            ep_tensor_t* grad_gate, ep_tensor_t* grad_up, ep_tensor_t* grad_rows,
-                                            ep_tensor_t* grad_w_gate, ep_tensor_t* grad_w_up, ep_stream_t stream) {
+namespace {
+
+// Rows kept in 8 bits: FP8 [rows, C] at the dispatch geometry with F32 scales [rows, C/128], or without scales
+// the dispatch's packed rows of H codes.  *s: their scales, *s_ld: bytes from one row's to the next one's.
+bool coded_rows(const Group* g, const ep_tensor_t* t, const ep_tensor_t* scales, int64_t C, ep_tensor_t* out,
+                const uint8_t** s, int64_t* s_ld) {
+  if (!t || C % 128 != 0) return false;
+  if (!scales) {
+    bool codes;
+    if (C != g->cfg.hidden || !received_rows(g, t, out, &codes) || !codes) return false;
+    *s = static_cast<const uint8_t*>(out->data) + C;
+    *s_ld = out->strides[0];
+    return true;
+  }
+  ep_tensor_t v;
+  if (!geometry_rows(g, t, EP_DTYPE_FP8_E4M3, C, EP_TAG_TOKENS, true, out) ||
+      !geometry_rows(g, scales, EP_DTYPE_F32, C / 128, EP_TAG_SCALES, false, &v) || v.sizes[0] < out->sizes[0] ||
+      (reinterpret_cast<uintptr_t>(v.data) & 3))
+    return false;
+  *s = static_cast<const uint8_t*>(v.data);
+  *s_ld = v.strides[0] * 4;
+  return true;
+}
+
+// The gated product's backward pass; `coded`: from rows kept in 8 bits.
+ep_status_t gated_backward(ep_handle_t handle, const ep_tensor_t* rows, const ep_tensor_t* scales, bool coded,
+                           const ep_tensor_t* w_gate, const ep_tensor_t* w_up, const ep_tensor_t* grad_out,
+                           int32_t activation, ep_tensor_t* grad_gate, ep_tensor_t* grad_up, ep_tensor_t* grad_rows,
+                           ep_tensor_t* grad_w_gate, ep_tensor_t* grad_w_up, ep_stream_t stream) {
   Handle* h = reinterpret_cast<Handle*>(handle);
   if (!handle_ok(h) || !w_gate || w_gate->ndim != 3) return EP_ERR_INVALID_ARGUMENT;
   Group* g = h->g;
@@ -1508,8 +1537,12 @@ EP_API ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_
   const int64_t H = g->cfg.hidden, I = w_gate->sizes[1];
   if (activation != EP_ACT_SILU && activation != EP_ACT_GELU_TANH) return EP_ERR_INVALID_ARGUMENT;
   ep_tensor_t x, d, dg, du, dx{};
-  bool fp8;
-  if (!received_rows(g, rows, &x, &fp8) || fp8 || !product_size(I)) return EP_ERR_INVALID_ARGUMENT;
+  const uint8_t* xs = nullptr;
+  int64_t ld_xs = 0;
+  bool fp8 = false;
+  if (coded ? !coded_rows(g, rows, scales, H, &x, &xs, &ld_xs) : !received_rows(g, rows, &x, &fp8) || fp8)
+    return EP_ERR_INVALID_ARGUMENT;
+  if (!product_size(I)) return EP_ERR_INVALID_ARGUMENT;
   if (!check_weights(g, w_gate, EP_DTYPE_BF16, I, H) || !check_weights(g, w_up, EP_DTYPE_BF16, I, H) ||
       !geometry_rows(g, grad_out, EP_DTYPE_BF16, I, EP_TAG_TOKENS, true, &d) ||
       !geometry_rows(g, grad_gate, EP_DTYPE_BF16, I, EP_TAG_TOKENS, true, &dg) ||
@@ -1524,12 +1557,15 @@ EP_API ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_
       (grad_rows && !holds_slots(g, dx)))
     return EP_ERR_INVALID_ARGUMENT;
   if (I > kMaxProductSize || !short_rows(g, x) || !short_rows(g, dg) || !short_rows(g, du) ||
-      !short_weights(w_gate) || !short_weights(w_up))
+      !short_weights(w_gate) || !short_weights(w_up) || (coded && !short_rows(g, ld_xs)))
     return EP_ERR_UNSUPPORTED;
 
   int64_t limit = std::min({x.sizes[0], d.sizes[0], dg.sizes[0], du.sizes[0]});
   if (grad_rows) limit = std::min(limit, dx.sizes[0]);
   AlongArgs a = along_args(h, x, H, I, limit);
+  a.k_bytes = H * 2;   // of the weights
+  a.x_scales = xs;
+  a.ld_xs = ld_xs;
   set_weights(&a, 0, w_gate, nullptr);
   set_weights(&a, 1, w_up, nullptr);
   set_out(&a, 0, dg);
@@ -1539,7 +1575,7 @@ EP_API ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_
   RowGradArgs r = row_grad_args(h, I, H, dx, limit);
   add_part(&r, dg, w_gate);
   add_part(&r, du, w_up);
-  WeightGradArgs w = weight_grad_args(h, x, I, H, limit);
+  WeightGradArgs w = weight_grad_args(h, x, xs, ld_xs, I, H, limit);
   const bool f32 = grad_w_gate && grad_w_gate->dtype == EP_DTYPE_F32;
   if (grad_w_gate) {
     add_part(&w, dg, grad_w_gate);
@@ -1553,8 +1589,27 @@ EP_API ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_
   EP_HIP(expert::launch_gated_grad(a, activation, s));
   if (grad_rows) EP_HIP(expert::launch_row_grad(r, s));
   if (grad_w_gate) EP_HIP(expert::launch_weight_grad(w, f32, s));
-  trace(g, "expert_gated_backward", h->n);
+  trace(g, coded ? "expert_gated_backward_fp8" : "expert_gated_backward", h->n);
   return EP_OK;
+}
+
+}  // namespace
+
+EP_API ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_t* rows, const ep_tensor_t* w_gate,
+                                            const ep_tensor_t* w_up, const ep_tensor_t* grad_out, int32_t activation,
+                                            ep_tensor_t* grad_gate, ep_tensor_t* grad_up, ep_tensor_t* grad_rows,
+                                            ep_tensor_t* grad_w_gate, ep_tensor_t* grad_w_up, ep_stream_t stream) {
+  return gated_backward(handle, rows, nullptr, false, w_gate, w_up, grad_out, activation, grad_gate, grad_up, grad_rows,
+                        grad_w_gate, grad_w_up, stream);
+}
+
+EP_API ep_status_t ep_expert_gated_backward_fp8(ep_handle_t handle, const ep_tensor_t* rows, const ep_tensor_t* rows_scales,
+                                                const ep_tensor_t* w_gate, const ep_tensor_t* w_up,
+                                                const ep_tensor_t* grad_out, int32_t activation,
+                                                ep_tensor_t* grad_gate, ep_tensor_t* grad_up, ep_tensor_t* grad_rows,
+                                                ep_tensor_t* grad_w_gate, ep_tensor_t* grad_w_up, ep_stream_t stream) {
+  return gated_backward(handle, rows, rows_scales, true, w_gate, w_up, grad_out, activation, grad_gate, grad_up, grad_rows,
+                        grad_w_gate, grad_w_up, stream);
 }
 
 EP_API ep_status_t ep_expert_quantize(ep_handle_t handle, const ep_tensor_t* x_in, ep_tensor_t* q, ep_tensor_t* scales,
@@ -1644,31 +1699,38 @@ EP_API ep_status_t ep_expert_linear(ep_handle_t handle, const ep_tensor_t* x_in,
   return st;
 }
 
-EP_API ep_status_t ep_expert_linear_backward(ep_handle_t handle, const ep_tensor_t* x_in, const ep_tensor_t* w,
-                                             const ep_tensor_t* grad_out, ep_tensor_t* grad_x, ep_tensor_t* grad_w,
-                                             ep_stream_t stream) {
+namespace {
+
+// The linear product's backward pass; `coded`: from rows kept in 8 bits.
+ep_status_t linear_backward(ep_handle_t handle, const ep_tensor_t* x_in, const ep_tensor_t* scales, bool coded,
+                            const ep_tensor_t* w, const ep_tensor_t* grad_out, ep_tensor_t* grad_x,
+                            ep_tensor_t* grad_w, ep_stream_t stream) {
   Handle* h = reinterpret_cast<Handle*>(handle);
   if (!handle_ok(h) || !w || w->ndim != 3) return EP_ERR_INVALID_ARGUMENT;
   Group* g = h->g;
   if (const ep_status_t st = expert_ready(h); st != EP_OK) return st;
   const int64_t N = w->sizes[1], C = w->sizes[2];
   ep_tensor_t x, d, dx{};
+  const uint8_t* xs = nullptr;
+  int64_t ld_xs = 0;
   if (!product_size(N) || !product_size(C)) return EP_ERR_INVALID_ARGUMENT;
-  if (!geometry_rows(g, x_in, EP_DTYPE_BF16, C, EP_TAG_TOKENS, true, &x) ||
+  if ((coded ? !scales || !coded_rows(g, x_in, scales, C, &x, &xs, &ld_xs)
+             : !geometry_rows(g, x_in, EP_DTYPE_BF16, C, EP_TAG_TOKENS, true, &x)) ||
       !check_weights(g, w, EP_DTYPE_BF16, N, C) ||
       !geometry_rows(g, grad_out, EP_DTYPE_BF16, N, EP_TAG_TOKENS, true, &d) ||
       (grad_x && !geometry_rows(g, grad_x, EP_DTYPE_BF16, C, EP_TAG_TOKENS, true, &dx)) ||
       (grad_w && !check_weight_grad(g, grad_w, N, C)))
     return EP_ERR_INVALID_ARGUMENT;
   if (!holds_slots(g, x) || !holds_slots(g, d) || (grad_x && !holds_slots(g, dx))) return EP_ERR_INVALID_ARGUMENT;
-  if (N > kMaxProductSize || C > kMaxProductSize || !short_rows(g, x) || !short_rows(g, d) || !short_weights(w))
+  if (N > kMaxProductSize || C > kMaxProductSize || !short_rows(g, x) || !short_rows(g, d) || !short_weights(w) ||
+      (coded && !short_rows(g, ld_xs)))
     return EP_ERR_UNSUPPORTED;
 
   int64_t limit = std::min(x.sizes[0], d.sizes[0]);
   if (grad_x) limit = std::min(limit, dx.sizes[0]);
   RowGradArgs r = row_grad_args(h, N, C, dx, limit);
   add_part(&r, d, w);
-  WeightGradArgs wg = weight_grad_args(h, x, N, C, limit);
+  WeightGradArgs wg = weight_grad_args(h, x, xs, ld_xs, N, C, limit);
   const bool f32 = grad_w && grad_w->dtype == EP_DTYPE_F32;
   if (grad_w) add_part(&wg, d, grad_w);
   const hipStream_t s = as_stream(stream);
@@ -1677,8 +1739,22 @@ EP_API ep_status_t ep_expert_linear_backward(ep_handle_t handle, const ep_tensor
   if (const ep_status_t st = start_products(h, s); st != EP_OK) return st;
   if (grad_x) EP_HIP(expert::launch_row_grad(r, s));
   if (grad_w) EP_HIP(expert::launch_weight_grad(wg, f32, s));
-  trace(g, "expert_linear_backward", h->n);
+  trace(g, coded ? "expert_linear_backward_fp8" : "expert_linear_backward", h->n);
   return EP_OK;
+}
+
+}  // namespace
+
+EP_API ep_status_t ep_expert_linear_backward(ep_handle_t handle, const ep_tensor_t* x, const ep_tensor_t* w,
+                                             const ep_tensor_t* grad_out, ep_tensor_t* grad_x, ep_tensor_t* grad_w,
+                                             ep_stream_t stream) {
+  return linear_backward(handle, x, nullptr, false, w, grad_out, grad_x, grad_w, stream);
+}
+
+EP_API ep_status_t ep_expert_linear_backward_fp8(ep_handle_t handle, const ep_tensor_t* x, const ep_tensor_t* x_scales,
+                                                 const ep_tensor_t* w, const ep_tensor_t* grad_out, ep_tensor_t* grad_x,
+                                                 ep_tensor_t* grad_w, ep_stream_t stream) {
+  return linear_backward(handle, x, x_scales, true, w, grad_out, grad_x, grad_w, stream);
 }
 
 // ===========================================================================

@@ -707,7 +707,27 @@ ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_t *rows
                                      ep_tensor_t *grad_rows, ep_tensor_t *grad_w_gate,
                                      ep_tensor_t *grad_w_up, ep_stream_t stream);
 
-/* FP8 quantisation of the experts' rows, for an FP8 product behind ep_expert_gated:
+/* The same from rows kept in 8 bits -- the rows that an FP8 dispatch left
+ * (or ep_expert_sort put in order), or codes and scales that ep_expert_quantize
+ * made -- without a BF16 copy of them: X = bf16_rne(code * scale), the values
+ * that ep_dequantize_rows gives, so the results have the bits that
+ * ep_expert_gated_backward gives on those.  The quantisation counts as the
+ * identity.
+ *   rows        : U8 packed FP8 rows of a group with an FP8 payload (rows_scales
+ *                 NULL), or FP8_E4M3 [rows, H] at the dispatch geometry with
+ *   rows_scales : F32 [rows, H/128] (or LL [E, S*T_max, H/128]), contiguous in
+ *                 the last dimension; H a multiple of 128.
+ * The rest as above; the weights are BF16. */
+ep_status_t ep_expert_gated_backward_fp8(ep_handle_t handle, const ep_tensor_t *rows,
+                                         const ep_tensor_t *rows_scales, const ep_tensor_t *w_gate,
+                                         const ep_tensor_t *w_up, const ep_tensor_t *grad_out,
+                                         int32_t activation, ep_tensor_t *grad_gate,
+                                         ep_tensor_t *grad_up, ep_tensor_t *grad_rows,
+                                         ep_tensor_t *grad_w_gate, ep_tensor_t *grad_w_up,
+                                         ep_stream_t stream);
+
+/* FP8 quantisation of the experts' rows, for an FP8 product behind ep_expert_gated
+ * and for a backward pass from 8 bits:
  * every row that holds a message, with ep_quantize's arithmetic (scale = amax/448
  * per 128 elements, codes the nearest-even, saturating E4M3 of x/scale).
  *   x      : BF16 [rows, C] at the dispatch geometry, C a multiple of 128.
@@ -735,6 +755,16 @@ ep_status_t ep_expert_linear(ep_handle_t handle, const ep_tensor_t *x, const ep_
 ep_status_t ep_expert_linear_backward(ep_handle_t handle, const ep_tensor_t *x, const ep_tensor_t *w,
                                       const ep_tensor_t *grad_out, ep_tensor_t *grad_x,
                                       ep_tensor_t *grad_w, ep_stream_t stream);
+
+/* The same from rows kept in 8 bits (as ep_expert_gated_backward_fp8):
+ *   x        : FP8_E4M3 [rows, C] at the dispatch geometry, C a multiple of 128.
+ *   x_scales : F32 [rows, C/128] (or LL [E, S*T_max, C/128]), contiguous in the
+ *              last dimension.
+ *   w        : BF16 [E, N, C]. */
+ep_status_t ep_expert_linear_backward_fp8(ep_handle_t handle, const ep_tensor_t *x,
+                                          const ep_tensor_t *x_scales, const ep_tensor_t *w,
+                                          const ep_tensor_t *grad_out, ep_tensor_t *grad_x,
+                                          ep_tensor_t *grad_w, ep_stream_t stream);
 
 /* ----------------------------------------------------------------------- */
 /* Norms around the block                                                    */
