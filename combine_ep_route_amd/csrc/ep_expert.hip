@@ -25,9 +25,6 @@ struct AlongSrc {
   int offa[C::JA], offb[C::JB], offs;
   int left;                          // bytes of the contraction behind this lane's piece
   bool inside;
-  // Rows kept as codes: bases and offsets of the next load, codes of the contraction behind it
-  const uint8_t *xq, *xs;
-  int offq[C::NL], offqs[C::NL], codes_done, codes_left;
 
   static constexpr int wave_span_a() { return GATED ? C::TA / 2 : C::TA; }
   static __device__ __forceinline__ int frag_a_at(int fa, int i) {
@@ -42,20 +39,6 @@ struct AlongSrc {
     const int row0 = first_row(a.rows, s, m0);
     w0 = a.w[0] + s.e * a.w_expert[0] + n0 * a.ld_w[0] - C::PIECE;
     w1 = GATED ? a.w[1] + s.e * a.w_expert[1] + n0 * a.ld_w[1] - C::PIECE : nullptr;
-    if constexpr (C::CB) {
-      constexpr int step = C::PIECE / 2;   // codes of a row in a step, 64: two steps share a scale
-      xq = a.x + row0 * a.ld_x - step;
-      xs = a.x_scales + row0 * a.ld_xs;
-      codes_done = -step;
-      codes_left = static_cast<int>(a.k_bytes / 2) + step;
-#pragma unroll
-      for (int j = 0; j < C::NL; ++j) {
-        const int p = m0 + C::code_row(j);
-        const int r = p < s.count ? row_of(a.rows, s, p) - row0 : 0;
-        offq[j] = p < s.count ? r * static_cast<int>(a.ld_x) + C::code_value() : kOutside;
-        offqs[j] = p < s.count ? r * static_cast<int>(a.ld_xs) : kOutside;
-      }
-    }
     x = a.x + row0 * a.ld_x - C::PIECE;
     left = static_cast<int>(a.k_bytes) - piece + C::PIECE;
 #pragma unroll
@@ -65,12 +48,10 @@ struct AlongSrc {
       const int n = second ? r - kCols : r;
       offa[j] = n0 + n < a.N ? n * static_cast<int>(a.ld_w[second]) + piece : kOutside;
     }
-    if constexpr (!C::CB) {
 #pragma unroll
-      for (int j = 0; j < C::JB; ++j) {
-        const int p = m0 + (j * C::NW + w) * C::ROWS + C::along_row();
-        offb[j] = p < s.count ? (row_of(a.rows, s, p) - row0) * static_cast<int>(a.ld_x) + piece : kOutside;
-      }
+    for (int j = 0; j < C::JB; ++j) {
+      const int p = m0 + (j * C::NW + w) * C::ROWS + C::along_row();
+      offb[j] = p < s.count ? (row_of(a.rows, s, p) - row0) * static_cast<int>(a.ld_x) + piece : kOutside;
     }
     if constexpr (C::F8) {
       const int t = threadIdx.x;
@@ -94,17 +75,6 @@ struct AlongSrc {
     inside = left > 0;
     if (C::F8) sc += 4;
   }
-  __device__ __forceinline__ void step_codes() {
-    xq += C::PIECE / 2;
-    codes_done += C::PIECE / 2;
-    codes_left -= C::PIECE / 2;
-  }
-  // All bits set (kOutside) behind the contraction, without a condition.
-  __device__ __forceinline__ int codes_end() const { return (codes_left - 1) >> 31; }
-  __device__ __forceinline__ Rsrc code_rsrc() const { return rsrc(xq, kExtent); }
-  __device__ __forceinline__ int code(int j) const { return offq[j] | codes_end(); }
-  __device__ __forceinline__ Rsrc code_scale_rsrc() const { return rsrc(xs + codes_done / 128 * 4, kExtent); }
-  __device__ __forceinline__ int code_scale(int j) const { return offqs[j] | codes_end(); }
   __device__ __forceinline__ Rsrc a_rsrc(int j) const { return rsrc(GATED && j >= C::JA / 2 ? w1 : w0, kExtent); }
   __device__ __forceinline__ Rsrc b_rsrc() const { return rsrc(x, kExtent); }
   __device__ __forceinline__ Rsrc scale_rsrc() const { return rsrc(sc, kExtent); }
@@ -149,14 +119,17 @@ __global__ __launch_bounds__(C::NT) void along_kernel(AlongArgs a) {
     return p < s.count ? static_cast<int64_t>(row_of(a.rows, s, p)) : -1;
   };
   if constexpr (KIND == kGatedGrad) {
+    uint2 d[CF][C::FB];
     auto grad_row = [&](int r) {
       const int64_t at = row(r);
       return at < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.grad + at * a.ld_grad + first);
     };
-    C::template for_rows<CF>(bytes, grad_row, [&](int j, const uint2 (&d)[CF]) {
+    C::template load_rows<CF>(d, bytes, grad_row);
 #pragma unroll
-      for (int i = 0; i < CF; ++i) {
-        const uint2 b = d[i];
+    for (int i = 0; i < CF; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FB; ++j) {
+        const uint2 b = d[i][j];
         const f32x4 dh = {from_bf16(b.x & 0xffff), from_bf16(b.x >> 16), from_bf16(b.y & 0xffff), from_bf16(b.y >> 16)};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -166,7 +139,6 @@ __global__ __launch_bounds__(C::NT) void along_kernel(AlongArgs a) {
           acc[i + CF][j][k] = f * dh[k];
         }
       }
-    });
   } else if constexpr (KIND == kGated) {
 #pragma unroll
     for (int i = 0; i < CF; ++i)
@@ -281,9 +253,6 @@ struct WeightGradSrc {
   int64_t ld_dy;
   int offa[C::JA], offb[C::JB];
   int h0, i0, left;
-  // Rows kept as codes: bases and offsets of the next load, rows from it on
-  const uint8_t *xq, *xs;
-  int offq, offqs, codes_left;
 
   static constexpr int wave_span_a() { return C::TA; }
   static __device__ __forceinline__ int frag_a_at(int fa, int i) { return fa + i * 16; }
@@ -294,17 +263,9 @@ struct WeightGradSrc {
     x = g.x + (s.first - back) * g.ld_x;
     dy = g.dy[which] + (s.first - back) * ld_dy;
     left = s.count + C::KROWS;
-    if constexpr (C::CA) {
-      xq = g.x + (s.first - back) * g.ld_x;
-      xs = g.x_scales + (s.first - back) * g.ld_xs;
-      codes_left = s.count + C::KROWS;
-      if constexpr (!LIST) set_codes(C::code_row(0));
-    }
     if constexpr (!LIST) {
-      if constexpr (!C::CA) {
 #pragma unroll
-        for (int j = 0; j < C::JA; ++j) offa[j] = offset_a(j, C::template across_row<C::BA>(j * C::NW + v));
-      }
+      for (int j = 0; j < C::JA; ++j) offa[j] = offset_a(j, C::template across_row<C::BA>(j * C::NW + v));
 #pragma unroll
       for (int j = 0; j < C::JB; ++j) offb[j] = offset_b(j, C::template across_row<C::BB>(j * C::NW + v));
     }
@@ -313,29 +274,6 @@ struct WeightGradSrc {
     const int h = h0 + C::template across_col<C::BA>(j * C::NW + wave_id());
     return h < g.H ? row * static_cast<int>(g.ld_x) + h * 2 : kOutside;
   }
-  __device__ __forceinline__ void set_codes(int row) {
-    const int h = h0 + C::code_value();
-    offq = h < g.H ? row * static_cast<int>(g.ld_x) + h : kOutside;
-    offqs = h < g.H ? row * static_cast<int>(g.ld_xs) + h / 128 * 4 : kOutside;
-  }
-  __device__ __forceinline__ void step_codes() {
-    codes_left -= C::KROWS;
-    if constexpr (!LIST) {
-      xq += g.ld_x * C::KROWS;
-      xs += g.ld_xs * C::KROWS;
-    } else {
-      const int r = C::code_row(0);
-      if (r < codes_left) set_codes(row_of(g.rows, s, s.count - codes_left + r) - s.first);
-      else offq = offqs = kOutside;
-    }
-  }
-  // rows past the last one lie behind the extent
-  __device__ __forceinline__ Rsrc code_rsrc() const { return rsrc(xq, LIST ? kExtent : extent_of(codes_left * g.ld_x)); }
-  __device__ __forceinline__ int code(int) const { return offq; }
-  __device__ __forceinline__ Rsrc code_scale_rsrc() const {
-    return rsrc(xs, LIST ? kExtent : extent_of(codes_left * g.ld_xs));
-  }
-  __device__ __forceinline__ int code_scale(int) const { return offqs; }
   __device__ __forceinline__ int offset_b(int j, int row) const {
     const int i = i0 + C::template across_col<C::BB>(j * C::NW + wave_id());
     return i < g.I ? row * static_cast<int>(ld_dy) + i * 2 : kOutside;
@@ -347,7 +285,7 @@ struct WeightGradSrc {
       dy += ld_dy * C::KROWS;
     } else {
 #pragma unroll
-      for (int j = 0; j < (C::CA ? 0 : C::JA); ++j) {
+      for (int j = 0; j < C::JA; ++j) {
         const int r = C::template across_row<C::BA>(j * C::NW + wave_id());
         offa[j] = r < left ? offset_a(j, row_of(g.rows, s, s.count - left + r) - s.first) : kOutside;
       }
@@ -471,15 +409,6 @@ Size tile_size(const ExpertRows& r, int64_t rows, int64_t col_tiles) {
   return each <= 96 || r.E * ((each + 255) / 256) * col_tiles < 256 ? kMiddle : kBig;
 }
 
-template <int ACT>
-hipError_t launch_gated_grad_codes(const AlongArgs& a, hipStream_t stream, bool check) {
-  switch (tile_size(a.rows, a.rows_max, (a.N + 127) / 128)) {
-    case kSmall: return launch_along_as<Core<128, 32, 4, 1, false, false, false, 4, 128, kCodedB, 4>, kGatedGrad, ACT>(a, stream, check);
-    case kMiddle: return launch_along_as<Core<128, 128, 2, 2, false, false, false, 2, 128, kCodedB, 1>, kGatedGrad, ACT>(a, stream, check);
-    default: return launch_along_as<Core<256, 256, 2, 4, false, false, false, 4, 64, kCodedB, 2>, kGatedGrad, ACT>(a, stream, check);
-  }
-}
-
 template <bool F8, int KIND, int ACT>
 hipError_t launch_along_kind(const AlongArgs& a, hipStream_t stream, bool check) {
   const int cols = KIND == kLinear ? 256 : 128;
@@ -514,8 +443,6 @@ hipError_t launch_gated(const AlongArgs& a, bool fp8, int act, hipStream_t strea
 }
 
 hipError_t launch_gated_grad(const AlongArgs& a, int act, hipStream_t stream, bool check) {
-  if (a.x_scales) return act == kSilu ? launch_gated_grad_codes<kSilu>(a, stream, check)
-                                      : launch_gated_grad_codes<kGeluTanh>(a, stream, check);
   return act == kSilu ? launch_along_kind<false, kGatedGrad, kSilu>(a, stream, check)
                       : launch_along_kind<false, kGatedGrad, kGeluTanh>(a, stream, check);
 }
@@ -566,11 +493,7 @@ hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check)
 //    512 (32 of 1024 x 1024)           42 / 37   40 / 30      2048 (128 of 1024 x 1024)  163 / 121  145 / 100
 // Near the border the big ones win where they fill the CUs a whole number of times (256, 512).
 hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check) {
-  const bool small = static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + 255) / 256) * ((g.I + 255) / 256) < 512;
-  if (g.x_scales)
-    return small ? launch_weight_grad_as<Core<128, 128, 2, 2, true, true, false, 4, 64, kCodedA, 2>>(g, f32, stream, check)
-                 : launch_weight_grad_as<Core<256, 256, 2, 4, true, true, false, 4, 64, kCodedA, 1>>(g, f32, stream, check);
-  if (small)
+  if (static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + 255) / 256) * ((g.I + 255) / 256) < 512)
     return launch_weight_grad_as<Core<128, 128, 2, 2, true, true, false, 4, 64>>(g, f32, stream, check);
   return launch_weight_grad_as<Core<256, 256, 2, 4, true, true, false, 4, 64>>(g, f32, stream, check);
 }

@@ -16,8 +16,6 @@
 //   "along" operands are contiguous in the contracted index: PIECE bytes of each output row or column
 //   (64 bytes: 32 bf16 values; 128: 64 bf16 or 128 FP8 values);
 //   "across" operands are contiguous in the output index: PIECE/2 contracted rows of bf16 values.
-// An operand may be kept as E4M3 codes with a scale per 128 values of a row and multiplied as bf16 (the gradients'
-// products from rows kept in 8 bits): its codes pass the registers, which write bf16 values to LDS.
 // Products are formed transposed (weights as the first operand, rows as the second), so that the
 // four results a lane holds are four consecutive columns of one output row: 8-byte stores.
 #pragma once
@@ -45,9 +43,6 @@ constexpr uint32_t kExtent = 0x7fffffffu;   // an extent for offsets that were c
 
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 
-template <int N>
-struct Width {};
-
 __device__ __forceinline__ Rsrc rsrc(const uint8_t* base, uint32_t extent) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, static_cast<int>(extent), 0x27000);
 }
@@ -61,18 +56,6 @@ __device__ __forceinline__ void load_lds16(Rsrc r, int offset, uint8_t* l) {
 }
 __device__ __forceinline__ void load_lds4(Rsrc r, int offset, uint8_t* l) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)l, 4, offset, 0, 0, 0);
-}
-
-// To registers.
-__device__ __forceinline__ i32x4 load_codes(Rsrc r, int offset, Width<16>) {
-  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
-}
-__device__ __forceinline__ i32x4 load_codes(Rsrc r, int offset, Width<8>) {
-  const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, offset, 0, 0);
-  return i32x4{static_cast<int>(v[0]), static_cast<int>(v[1]), 0, 0};
-}
-__device__ __forceinline__ float load_scale(Rsrc r, int offset) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, offset, 0, 0));
 }
 
 // Waits until at most N of this wave's vector loads are in flight and all its LDS reads and writes
@@ -225,11 +208,6 @@ __device__ __forceinline__ int row_of(const ExpertRows& r, const Span& s, int p)
 __device__ __forceinline__ uint32_t bf16_bits(float v) {
   return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(v)));
 }
-__device__ __forceinline__ int bf16_pair(float lo, float hi) {
-  typedef __attribute__((ext_vector_type(2))) float f32x2;
-  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
-  return __builtin_bit_cast(int, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
-}
 __device__ __forceinline__ uint2 bf16x4(f32x4 v) {
   return {bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16};
 }
@@ -248,14 +226,9 @@ struct One {
   __device__ __forceinline__ Src source(int) const { return src; }
 };
 
-// What comes as codes and is multiplied as bf16: nothing, the second operand (along), or the first (across).
-enum Coded { kNoCodes, kCodedB, kCodedA };
-
 // BA x BB results from WA x WB waves; ANC / BNC: the operand lies across (else along); F8: E4M3 operands
-// with scales (both along); ST: stages of the LDS ring; PIECE: see above.  AHEAD: steps that codes are loaded
-// ahead of their place in the ring.
-template <int BA_, int BB_, int WA_, int WB_, bool ANC_, bool BNC_, bool F8_, int ST_, int PIECE_,
-          Coded CODED_ = kNoCodes, int AHEAD_ = 1>
+// with scales (both along); ST: stages of the LDS ring; PIECE: see above.
+template <int BA_, int BB_, int WA_, int WB_, bool ANC_, bool BNC_, bool F8_, int ST_, int PIECE_>
 struct Core {
   static constexpr int BA = BA_, BB = BB_, WA = WA_, WB = WB_, ST = ST_, PIECE = PIECE_;
   static constexpr bool ANC = ANC_, BNC = BNC_, F8 = F8_;
@@ -269,26 +242,12 @@ struct Core {
   // wave of its own.
   static constexpr int WS = (BB + 63) / 64 * 64;
   static constexpr int SCALES = F8 ? NT * 4 : 0;
-  static constexpr Coded CODED = CODED_;
-  static constexpr bool CA = CODED == kCodedA, CB = CODED == kCodedB;
-  static constexpr int AHEAD = AHEAD_;
-  static constexpr int AT_B = CA ? 0 : BA * PIECE;   // the second operand's tile in a stage
-  static constexpr int STAGE = ((CA ? 0 : BA) + (CB ? 0 : BB)) * PIECE + SCALES;
-  // Codes of a step that a thread loads: CL at a time (one row's, 16 or fewer), NL times.
-  static constexpr int CPT = CODED == kNoCodes ? 16 : (CA ? BA : BB) * PIECE / 2 / NT;
-  static constexpr int CL = CPT < 16 ? CPT : 16, NL = CPT / CL;
-  static constexpr int CODE_LOADS = CODED == kNoCodes ? 0 : 2 * NL;   // with their scales
-  static constexpr int PARTS = NL * CL / 8;                           // 16-byte pieces of LDS that it writes
-  static constexpr int TPR = (CA ? BA : PIECE / 2) / CL;              // threads that share a row
-  static_assert(CODED == kNoCodes || ((CL == 8 || CL == 16) && CL * NL == CPT && ST % AHEAD == 0 && PIECE >= 64),
-                "whole loads of codes, sets of registers that the ring goes round with");
-  static_assert(!CB || (!BNC && !F8 && NT / TPR % 8 == 0), "codes of rows along: the same spread in every load");
-  static_assert(!CA || (ANC && !F8 && NL == 1 && CL == 16), "codes of rows across: a 32-byte chunk a thread");
+  static constexpr int STAGE = (BA + BB) * PIECE + SCALES;
   static_assert(BA / ROWS % NW == 0 && BB / ROWS % NW == 0, "loads must divide over the waves");
   static_assert(TA % 16 == 0 && TB % 16 == 0, "whole fragments");
   static_assert(PIECE == 64 || PIECE == 128, "32 or 64 contracted bf16 values");
   static_assert(!F8 || (!ANC && !BNC && PIECE == 128 && WS + 128 <= NT), "FP8 operands lie along");
-  static_assert(ST >= 2 && ST <= 4 && (JA + JB + 1 + CODE_LOADS) * (ST - 1) < 64, "the wait counts at most 63 loads");
+  static_assert(ST >= 2 && ST <= 4 && (JA + JB + 1) * (ST - 1) < 64, "the wait counts at most 63 loads");
 
   typedef f32x4 Acc[FA][FB];
 
@@ -308,26 +267,6 @@ struct Core {
     __shared__ __attribute__((aligned(1024))) uint8_t s[ST > 3 ? STAGE : 16];
     return s;
   }
-
-  // Decoded tiles: arrays of their own, since the compiler would wait for all loads into an array that it writes.
-  static constexpr int DECODED = CODED == kNoCodes ? 16 : (CA ? BA : BB) * PIECE;
-  template <int S>
-  static __device__ __forceinline__ uint8_t* decoded() {
-    __shared__ __attribute__((aligned(1024))) uint8_t s[S < ST ? DECODED : 16];
-    return s;
-  }
-  // A stage of the ring: the loaded tiles, and the decoded one.
-  struct Stage {
-    uint8_t *loaded, *coded;
-    __device__ __forceinline__ const uint8_t* a() const { return CA ? coded : loaded; }
-    __device__ __forceinline__ const uint8_t* b() const { return CB ? coded : loaded + AT_B; }
-  };
-  // A thread's codes of one step.
-  struct Codes {
-    i32x4 q[NL];
-    float s[NL];
-    int at;   // code_at()
-  };
 
   // Where a 16-byte piece of an "along" row lies: rows of 64 or 128 bytes put equal pieces of neighbouring
   // rows on the same banks; the exclusive or spreads the eight rows a read takes at once over all of them.
@@ -352,10 +291,7 @@ struct Core {
     const int need = (16 * WB * nj + ROWS * NW - 1) / (ROWS * NW);
     return BNC || need > JB ? JB : need;
   }
-  static constexpr int loads(int nj) { return (CA ? 0 : JA) + (CB ? 0 : loads_b(nj)) + (F8 ? 1 : 0); }
-  // Loads behind those of a stage that may be in flight when the stage has to be complete: those of the ST-2
-  // stages after it, and the codes loaded with each.
-  static constexpr int behind(int nj) { return loads(nj) * (ST - 2) + CODE_LOADS * (ST - 1); }
+  static constexpr int loads(int nj) { return JA + loads_b(nj) + (F8 ? 1 : 0); }
 
   // Load `at` of a step (scales first).  The loads of a step are spread over the products: a burst of them
   // fills the address unit's queue, and a wave that waits there issues no product either.
@@ -366,60 +302,15 @@ struct Core {
       if constexpr (F8) load_lds4(src.scale_rsrc(), src.scale(), buf + (BA + BB) * PIECE + w * 256);
       return;
     }
-    constexpr int from_a = CA ? 0 : JA, from_b = CB ? 0 : loads_b(NJ);
     const int j = at - (F8 ? 1 : 0);
-    if (j < from_a) load_lds16(src.a_rsrc(j), src.a(j), buf + (j * NW + w) * 1024);
-    else if (j < from_a + from_b)
-      load_lds16(src.b_rsrc(), src.b(j - from_a), buf + AT_B + ((j - from_a) * NW + w) * 1024);
+    if (j < JA) load_lds16(src.a_rsrc(j), src.a(j), buf + (j * NW + w) * 1024);
+    else if (j < JA + loads_b(NJ)) load_lds16(src.b_rsrc(), src.b(j - JA), buf + BA * PIECE + ((j - JA) * NW + w) * 1024);
   }
   template <int NJ, class Src>
-  static __device__ __forceinline__ void issue(Src& src, const Stage& st, Codes& c) {
+  static __device__ __forceinline__ void issue(Src& src, uint8_t* buf) {
     src.step();
 #pragma unroll
-    for (int i = 0; i < loads(NJ); ++i) issue_one<NJ>(src, i, st.loaded);
-    if constexpr (CODED != kNoCodes) {
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int p = 0; p < PARTS; ++p) decode_part(p, c, st.coded);
-      fetch(src, c);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-
-  // Codes: fetched AHEAD steps before the step whose stage they are decoded into.
-  template <class Src>
-  static __device__ __forceinline__ void fetch(Src& src, Codes& c) {
-    src.step_codes();
-#pragma unroll
-    for (int j = 0; j < NL; ++j) {
-      c.q[j] = load_codes(src.code_rsrc(), src.code(j), Width<CL>{});
-      c.s[j] = load_scale(src.code_scale_rsrc(), src.code_scale(j));
-    }
-  }
-  // Row, and first value in it, of this thread's load j.
-  static __device__ __forceinline__ int code_row(int j) { return (threadIdx.x + j * NT) / TPR; }
-  static __device__ __forceinline__ int code_value() { return threadIdx.x % TPR * CL; }
-  // Eight codes to bf16: nearest of code * scale, the values that ep_dequantize_rows gives.  The matrix unit takes
-  // bf16 operands here, as the weights and gradients are; the rounding is one half step of bf16 in an operand, as
-  // large as the results' own.
-  static __device__ __forceinline__ void decode_part(int p, const Codes& c, uint8_t* tile) {
-    const int j = p / (CL / 8), half = p % (CL / 8);
-    i32x4 v;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int codes = c.q[j][2 * half + w];
-      const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(codes, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(codes, true);
-      v[2 * w] = bf16_pair(lo[0] * c.s[j], lo[1] * c.s[j]);
-      v[2 * w + 1] = bf16_pair(hi[0] * c.s[j], hi[1] * c.s[j]);
-    }
-    const int at = one_address(c.at);
-    *reinterpret_cast<i32x4*>(tile + (at ^ (half * 16)) + j * (NT / TPR) * (CA ? BA * 2 : PIECE)) = v;
-  }
-  // Where this thread's first 16 bytes lie in a decoded tile; its second ones in a row lie at the address with bit 4
-  // the other way, the next row's NT / TPR rows on.
-  static __device__ __forceinline__ int code_at() {
-    const int row = code_row(0), t = threadIdx.x % TPR;
-    return CA ? row * (BA * 2) + ((t ^ (mix(row) & (BA / 16 - 1))) << 5) : row * PIECE + (((t * (CL / 8)) ^ spread(row)) << 4);
+    for (int i = 0; i < loads(NJ); ++i) issue_one<NJ>(src, i, buf);
   }
   // The part of a step's loads that goes with fragment i of the first operand.
   template <int NJ, class Src>
@@ -428,13 +319,6 @@ struct Core {
 #pragma unroll
     for (int k = 0; k < per; ++k)
       if (i * per + k < loads(NJ)) issue_one<NJ>(src, i * per + k, buf);
-  }
-
-  // An address that the compiler works on where it is used.  Codes and their offsets take the registers in which it
-  // would keep one address for each fragment, part and stage.
-  static __device__ __forceinline__ int one_address(int at) {
-    if constexpr (CODED != kNoCodes) asm volatile("" : "+v"(at));
-    return at;
   }
 
   // 16 rows or columns from `from` of the step's part s, 8 contracted values a lane: lane group
@@ -446,7 +330,7 @@ struct Core {
   template <int B>
   static __device__ __forceinline__ i32x4 across_frag(const uint8_t* t, int from, int s) {
     const int l = lane_id(), k = (l >> 4) * 8 + ((l & 15) >> 2);   // mix(k + 32) == mix(k)
-    const int at = one_address(k * (B * 2) + ((mix(k) & (B / 16 - 1)) << 5) + (l & 3) * 8) ^ (from << 1);
+    const int at = (k * (B * 2) + ((mix(k) & (B / 16 - 1)) << 5) + (l & 3) * 8) ^ (from << 1);
     const uint8_t* p = t + at + s * 32 * (B * 2);
     typedef __attribute__((address_space(3))) s16x4 lds4;
     union { s16x4 h[2]; i32x4 v; } u;
@@ -524,14 +408,14 @@ struct Core {
 
   // A step of bf16 that reads all its fragments and then multiplies.
   template <int NJ, class Src>
-  static __device__ __forceinline__ void compute(const Src&, const Stage& st, Acc& acc, int fa) {
+  static __device__ __forceinline__ void compute(const Src&, const uint8_t* buf, Acc& acc, int fa) {
 #pragma unroll
     for (int s = 0; s < PIECE / 64; ++s) {
       i32x4 a[FA], b[NJ];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) b[j] = frag_b(st.b(), from_b(j), s);
+      for (int j = 0; j < NJ; ++j) b[j] = frag_b(buf + BA * PIECE, from_b(j), s);
 #pragma unroll
-      for (int i = 0; i < FA; ++i) a[i] = frag_a(st.a(), Src::frag_a_at(fa, i), s);
+      for (int i = 0; i < FA; ++i) a[i] = frag_a(buf, Src::frag_a_at(fa, i), s);
 #pragma unroll
       for (int i = 0; i < FA; ++i)
 #pragma unroll
@@ -546,14 +430,13 @@ struct Core {
   // start the loads of step t+ST-1 into the stage that step t-1 read (every wave has read it: its LDS reads
   // ended before the barrier), multiply.
   template <int NJ, class Src>
-  static __device__ __forceinline__ void ring_step(Src& src, const Stage& cur, const Stage& before, Codes& c, Acc& acc,
-                                                   int fa) {
-    wait_and_meet<behind(NJ)>();
+  static __device__ __forceinline__ void ring_step(Src& src, uint8_t* cur, uint8_t* before, Acc& acc, int fa) {
+    wait_and_meet<loads(NJ) * (ST - 2)>();
     if constexpr (F8) {
       src.step();
-      compute_fp8<NJ>(src, cur.loaded, before.loaded, acc, fa);
+      compute_fp8<NJ>(src, cur, before, acc, fa);
     } else {
-      issue<NJ>(src, before, c);
+      issue<NJ>(src, before);
       compute<NJ>(src, cur, acc, fa);
     }
   }
@@ -562,40 +445,33 @@ struct Core {
   // fragment run, the one after the next is read; with the last two run the reads of the next step's first
   // two and its second operand.  When a stage's last fragment is in registers all waves meet: the next stage
   // is complete, and this one takes the loads of step t+ST, kEarly of them at once and the others with the
-  // next step's first fragments.  Codes are decoded into the stage with the next step's first fragments too, and
-  // their registers loaded again.
+  // next step's first fragments.
   static constexpr int kEarly = 4;
   template <int NJ, class Src>
-  static __device__ __forceinline__ void piped_step(Src& src, const Stage& before, const Stage& cur, const Stage& next,
-                                                    Codes& codes, Acc& acc, int fa, i32x4 (&b)[NJ], i32x4 (&a)[2]) {
+  static __device__ __forceinline__ void piped_step(Src& src, uint8_t* before, uint8_t* cur, uint8_t* next, Acc& acc,
+                                                    int fa, i32x4 (&b)[NJ], i32x4 (&a)[2]) {
     constexpr int H = PIECE / 64, N = H * FA;
-    static_assert(CODED == kNoCodes || (loads(NJ) <= kEarly && PARTS <= N - 2),
-                  "the other loads come before those of the codes, which come before the waves meet");
     i32x4 c[NJ];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int i = n % FA, s = n / FA, m = n + 2;
-      if (kEarly + 2 * n < loads(NJ)) issue_one<NJ>(src, kEarly + 2 * n, before.loaded);
-      if (kEarly + 2 * n + 1 < loads(NJ)) issue_one<NJ>(src, kEarly + 2 * n + 1, before.loaded);
-      if constexpr (CODED != kNoCodes) {
-        if (n < PARTS) decode_part(n, codes, before.coded);
-        if (n == PARTS - 1) fetch(src, codes);
-      }
+      if (kEarly + 2 * n < loads(NJ)) issue_one<NJ>(src, kEarly + 2 * n, before);
+      if (kEarly + 2 * n + 1 < loads(NJ)) issue_one<NJ>(src, kEarly + 2 * n + 1, before);
       if (n == N - 2) {
-        wait_and_meet<behind(NJ)>();
+        wait_and_meet<loads(NJ) * (ST - 2)>();
         src.step();
       }
       if (n >= N - 2) {
         const int from = (n - (N - 2)) * 2;
-        if (from < loads(NJ) && from < kEarly) issue_one<NJ>(src, from, cur.loaded);
-        if (from + 1 < loads(NJ) && from + 1 < kEarly) issue_one<NJ>(src, from + 1, cur.loaded);
+        if (from < loads(NJ) && from < kEarly) issue_one<NJ>(src, from, cur);
+        if (from + 1 < loads(NJ) && from + 1 < kEarly) issue_one<NJ>(src, from + 1, cur);
       }
       if (i == FA - 2) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) c[j] = frag_b((s + 1 < H ? cur : next).b(), from_b(j), s + 1 < H ? s + 1 : 0);
+        for (int j = 0; j < NJ; ++j) c[j] = frag_b((s + 1 < H ? cur : next) + BA * PIECE, from_b(j), s + 1 < H ? s + 1 : 0);
       }
-      const i32x4 ahead = m < N ? frag_a(cur.a(), Src::frag_a_at(fa, m % FA), m / FA)
-                                : frag_a(next.a(), Src::frag_a_at(fa, m - N), 0);
+      const i32x4 ahead = m < N ? frag_a(cur, Src::frag_a_at(fa, m % FA), m / FA)
+                                : frag_a(next, Src::frag_a_at(fa, m - N), 0);
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[n & 1]),
@@ -612,54 +488,44 @@ struct Core {
   // The main loops hold no condition: with one, the compiler waits for all LDS reads where blocks join.  So
   // loads are started past the last step too, which sources answer with zeros, and waited for at the end.
   template <int NJ, class Src>
-  static __device__ __forceinline__ void run_part(Src& src, int steps, Acc& acc, const Stage& s0, const Stage& s1,
-                                                  const Stage& s2, const Stage& s3) {
+  static __device__ __forceinline__ void run_part(Src& src, int steps, Acc& acc, uint8_t* s0, uint8_t* s1, uint8_t* s2,
+                                                  uint8_t* s3) {
     const int fa = (wave_id() % WA) * Src::wave_span_a();
     constexpr bool PIPED = !F8 && FA >= 4;
-    const Stage& last = ST == 2 ? s1 : ST == 3 ? s2 : s3;
+    uint8_t* const last = ST == 2 ? s1 : ST == 3 ? s2 : s3;
     int t = 0;
-    Codes c[AHEAD];   // those of stage s in set s % AHEAD
-    if constexpr (CODED != kNoCodes) {
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        c[i].at = code_at();
-        fetch(src, c[i]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    issue<NJ>(src, s0, c[0]);
-    if constexpr (ST > 2) issue<NJ>(src, s1, c[1 % AHEAD]);
-    if constexpr (ST > 3) issue<NJ>(src, s2, c[2 % AHEAD]);
-    Codes &c0 = c[(ST - 1) % AHEAD], &c1 = c[ST % AHEAD], &c2 = c[(ST + 1) % AHEAD], &c3 = c[(ST + 2) % AHEAD];
+    issue<NJ>(src, s0);
+    if constexpr (ST > 2) issue<NJ>(src, s1);
+    if constexpr (ST > 3) issue<NJ>(src, s2);
     if constexpr (PIPED) {
       i32x4 b[NJ], a[2];
       src.step();
 #pragma unroll
-      for (int i = 0; i < kEarly && i < loads(NJ); ++i) issue_one<NJ>(src, i, last.loaded);
-      wait_and_meet<behind(NJ) + (kEarly < loads(NJ) ? kEarly : loads(NJ))>();
+      for (int i = 0; i < kEarly && i < loads(NJ); ++i) issue_one<NJ>(src, i, last);
+      wait_and_meet<loads(NJ) * (ST - 2) + (kEarly < loads(NJ) ? kEarly : loads(NJ))>();
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) b[j] = frag_b(s0.b(), from_b(j), 0);
-      a[0] = frag_a(s0.a(), Src::frag_a_at(fa, 0), 0);
-      a[1] = frag_a(s0.a(), Src::frag_a_at(fa, 1), 0);
+      for (int j = 0; j < NJ; ++j) b[j] = frag_b(s0 + BA * PIECE, from_b(j), 0);
+      a[0] = frag_a(s0, Src::frag_a_at(fa, 0), 0);
+      a[1] = frag_a(s0, Src::frag_a_at(fa, 1), 0);
       for (; t + ST <= steps; t += ST) {
-        piped_step<NJ>(src, last, s0, s1, c0, acc, fa, b, a);
-        piped_step<NJ>(src, s0, s1, ST == 2 ? s0 : s2, c1, acc, fa, b, a);
-        if constexpr (ST > 2) piped_step<NJ>(src, s1, s2, ST == 3 ? s0 : s3, c2, acc, fa, b, a);
-        if constexpr (ST > 3) piped_step<NJ>(src, s2, s3, s0, c3, acc, fa, b, a);
+        piped_step<NJ>(src, last, s0, s1, acc, fa, b, a);
+        piped_step<NJ>(src, s0, s1, ST == 2 ? s0 : s2, acc, fa, b, a);
+        if constexpr (ST > 2) piped_step<NJ>(src, s1, s2, ST == 3 ? s0 : s3, acc, fa, b, a);
+        if constexpr (ST > 3) piped_step<NJ>(src, s2, s3, s0, acc, fa, b, a);
       }
-      if (t < steps) piped_step<NJ>(src, last, s0, s1, c0, acc, fa, b, a);
-      if (ST > 2 && t + 1 < steps) piped_step<NJ>(src, s0, s1, s2, c1, acc, fa, b, a);
-      if (ST > 3 && t + 2 < steps) piped_step<NJ>(src, s1, s2, s3, c2, acc, fa, b, a);
+      if (t < steps) piped_step<NJ>(src, last, s0, s1, acc, fa, b, a);
+      if (ST > 2 && t + 1 < steps) piped_step<NJ>(src, s0, s1, s2, acc, fa, b, a);
+      if (ST > 3 && t + 2 < steps) piped_step<NJ>(src, s1, s2, s3, acc, fa, b, a);
     } else {
       for (; t + ST <= steps; t += ST) {
-        ring_step<NJ>(src, s0, last, c0, acc, fa);
-        ring_step<NJ>(src, s1, s0, c1, acc, fa);
-        if constexpr (ST > 2) ring_step<NJ>(src, s2, s1, c2, acc, fa);
-        if constexpr (ST > 3) ring_step<NJ>(src, s3, s2, c3, acc, fa);
+        ring_step<NJ>(src, s0, last, acc, fa);
+        ring_step<NJ>(src, s1, s0, acc, fa);
+        if constexpr (ST > 2) ring_step<NJ>(src, s2, s1, acc, fa);
+        if constexpr (ST > 3) ring_step<NJ>(src, s3, s2, acc, fa);
       }
-      if (t < steps) ring_step<NJ>(src, s0, last, c0, acc, fa);
-      if (ST > 2 && t + 1 < steps) ring_step<NJ>(src, s1, s0, c1, acc, fa);
-      if (ST > 3 && t + 2 < steps) ring_step<NJ>(src, s2, s1, c2, acc, fa);
+      if (t < steps) ring_step<NJ>(src, s0, last, acc, fa);
+      if (ST > 2 && t + 1 < steps) ring_step<NJ>(src, s1, s0, acc, fa);
+      if (ST > 3 && t + 2 < steps) ring_step<NJ>(src, s2, s1, acc, fa);
     }
     // no load into LDS may outlive the workgroup, and the next part starts with all stages free
     wait_and_meet<0>();
@@ -669,8 +535,10 @@ struct Core {
   // rows of the second operand that count.
   template <class Plan>
   static __device__ __forceinline__ void run(const Plan& plan, int steps, int rows, Acc& acc) {
-    const Stage s0{stage0(), decoded<0>()}, s1{stage1(), decoded<1>()}, s2{stage2(), decoded<2>()},
-        s3{stage3(), decoded<3>()};
+    uint8_t* const s0 = stage0();
+    uint8_t* const s1 = stage1();
+    uint8_t* const s2 = stage2();
+    uint8_t* const s3 = stage3();
     if (steps <= 0) return;
     auto all = [&](auto nj) {
       for (int p = 0; p < plan.parts(); ++p) {
@@ -693,15 +561,11 @@ struct Core {
   // they go through LDS (the stages are free behind run()): whole rows of the wave's CF*16 columns, 16 bytes a
   // lane.  64 experts of 2048 x 7168, 512 rows each, gated backward: 7.05 ms with stores as they lie, 6.52 so.
   // Each wave has kRegion bytes of its own; a row's 16-byte pieces are spread over the banks by the row.
-  static constexpr int kShared = 2 * (STAGE - SCALES) / NW >= 8192 ? 2 : 4;   // stages that hold the regions
-  static constexpr int kRegion = kShared * (STAGE - SCALES) / NW / 1024 * 1024;
-  static_assert(kRegion >= 8192 && kShared <= ST && NW % kShared == 0, "16 rows of 128 fp32 values");
+  static constexpr int kRegion = 2 * (STAGE - SCALES) / NW / 1024 * 1024;
+  static_assert(kRegion >= 8192, "16 rows of 128 fp32 values");
   static __device__ __forceinline__ uint8_t* region() {
-    constexpr int per = NW / kShared;
     const int w = wave_id();
-    uint8_t* const low = w < per ? stage0() : stage1();
-    uint8_t* const s = kShared == 2 || w < 2 * per ? low : w < 3 * per ? stage2() : stage3();
-    return s + w % per * kRegion;
+    return (w < NW / 2 ? stage0() : stage1()) + w % (NW / 2) * kRegion;
   }
   template <int CF, int ES>
   struct Tile {
@@ -759,39 +623,25 @@ struct Core {
       turn();
     }
   }
-  // The other way, 16 rows at a time: f(j, v) gets the bf16 values v[i], as bits, of the lane's four columns in fragment
-  // i, rows j.  The next rows' loads run behind f.
-  template <int CF, class Row, class F>
-  static __device__ __forceinline__ void for_rows(int bytes, Row row, F f) {
+  // The other way: bf16 rows to the lanes' places, v[i][j] four columns as bits.
+  template <int CF, class Row>
+  static __device__ __forceinline__ void load_rows(uint2 (&v)[CF][FB], int bytes, Row row) {
     using T = Tile<CF, 2>;
-    constexpr int LOADS = (16 * T::PIECES + 63) / 64;
     const int l = lane_id();
-    uint4 next[LOADS];
-    auto load = [&](int j) {
 #pragma unroll
-      for (int k = 0; k < LOADS; ++k) {
-        const int n = k * 64 + l, byte = n % T::PIECES * 16;
-        const uint8_t* from = n < 16 * T::PIECES ? row(j * 16 + n / T::PIECES) : nullptr;
-        next[k] = from && byte < bytes ? *reinterpret_cast<const uint4*>(from + byte) : uint4{0, 0, 0, 0};
-      }
-    };
-    load(0);
-#pragma unroll
-    for (int j = 0; j < FB; ++j) {
-#pragma unroll
-      for (int k = 0; k < LOADS; ++k) {
-        const int n = k * 64 + l;
-        if (n < 16 * T::PIECES)
-          *reinterpret_cast<uint4*>(region() + T::at(n / T::PIECES, n % T::PIECES * 16)) = next[k];
-      }
-      if (j + 1 < FB) load(j + 1);
+    for (int round = 0; round < TB / T::ROUND; ++round) {
+      T::pieces(round, [&](int r, int byte, uint8_t* to) {
+        const uint8_t* from = row(r);
+        *reinterpret_cast<uint4*>(to) = from && byte < bytes ? *reinterpret_cast<const uint4*>(from + byte) : uint4{0, 0, 0, 0};
+      });
       turn();
-      uint2 v[CF];
 #pragma unroll
-      for (int i = 0; i < CF; ++i)
-        v[i] = *reinterpret_cast<const uint2*>(region() + T::at(l & 15, (i * 16 + (l >> 4) * 4) * 2));
+      for (int j = 0; j < T::ROUND / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < CF; ++i)
+          v[i][round * (T::ROUND / 16) + j] =
+              *reinterpret_cast<const uint2*>(region() + T::at(j * 16 + (l & 15), (i * 16 + (l >> 4) * 4) * 2));
       turn();
-      f(j, v);
     }
   }
 };

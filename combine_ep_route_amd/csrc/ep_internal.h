@@ -290,8 +290,12 @@ struct QuantArgs {
   int32_t E, K, S, T, tps, slots;
   int64_t rows;
   int32_t* err;
+  uint16_t* decoded;      // launch_decode: BF16 [n, H] out, from q and scales
+  int64_t ld_d;           // elements
 };
 hipError_t launch_quantize(const QuantArgs& a, hipStream_t stream);
+// Codes of the experts' rows that hold a message (count, or topk, rank_e and hist_e given) to bf16.
+hipError_t launch_decode(const QuantArgs& a, hipStream_t stream);
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t stream);
 
@@ -427,8 +431,7 @@ struct AlongArgs {
 };
 hipError_t launch_linear(const AlongArgs& a, bool fp8, hipStream_t stream, bool check = false);
 hipError_t launch_gated(const AlongArgs& a, bool fp8, int act, hipStream_t stream, bool check = false);
-// out = the gradients of the gate's and of the up product.  With x_scales x holds codes and k_bytes counts the
-// weights' bytes.
+// out = the gradients of the gate's and of the up product
 hipError_t launch_gated_grad(const AlongArgs& a, int act, hipStream_t stream, bool check = false);
 
 struct RowGradArgs {
@@ -451,8 +454,6 @@ struct WeightGradArgs {
   int64_t ld_dy[2];
   const uint8_t* x;
   int64_t ld_x;
-  const uint8_t* x_scales;            // x holds codes, one float per 128 of a row; or null: bf16
-  int64_t ld_xs;
   uint8_t* dw[2];
   int64_t ld_dw[2], dw_expert[2];
 };

@@ -1361,6 +1361,27 @@ ExpertRows rows_of_experts(const Handle* h, int64_t limit) {
   return r;
 }
 
+// The experts' rows that hold a message, for the quantiser: from what the handle's creation has written; the maps may
+// not have been.
+void rows_in_use(const Handle* h, QuantArgs* a) {
+  const Group* g = h->g;
+  a->n = h->n * g->cfg.top_k;
+  a->E = g->cfg.num_experts;
+  a->err = g->err;
+  if (g->cfg.mode == EP_MODE_LL) {
+    a->topk = h->topk;
+    a->rank_e = h->rank_e;
+    a->hist_e = h->hist_e;
+    a->K = g->cfg.top_k;
+    a->S = g->cfg.num_src_ranks;
+    a->T = h->T;
+    a->tps = h->tps;
+    a->slots = g->cfg.max_tokens_per_rank;
+  } else {
+    a->count = g->sorted ? h->cx : h->c2;
+  }
+}
+
 // Enqueues what the products need first: the rows' list in LL with many
 // sources.  It is formed at every call, from the handle's counts alone, so a
 // captured call does not depend on what ran outside its graph.
@@ -1436,17 +1457,13 @@ void add_part(RowGradArgs* r, const ep_tensor_t& dy, const ep_tensor_t* w) {
   r->w_expert[i] = w->strides[0] * 2;
 }
 
-// With scales x holds codes.
-WeightGradArgs weight_grad_args(const Handle* h, const ep_tensor_t& x, const uint8_t* scales, int64_t ld_scales, int64_t i,
-                                int64_t n, int64_t limit) {
+WeightGradArgs weight_grad_args(const Handle* h, const ep_tensor_t& x, int64_t i, int64_t n, int64_t limit) {
   WeightGradArgs r{};
   r.rows = rows_of_experts(h, limit);
   r.I = static_cast<int32_t>(i);
   r.H = static_cast<int32_t>(n);
   r.x = static_cast<const uint8_t*>(x.data);
-  r.ld_x = x.strides[0] * (scales ? 1 : 2);
-  r.x_scales = scales;
-  r.ld_xs = ld_scales;
+  r.ld_x = x.strides[0] * 2;
   return r;
 }
 
@@ -1525,7 +1542,30 @@ bool coded_rows(const Group* g, const ep_tensor_t* t, const ep_tensor_t* scales,
   return true;
 }
 
-// The gated product's backward pass; `coded`: from rows kept in 8 bits.
+// The decoding of rows kept in 8 bits into `to`.
+QuantArgs decode_args(const Handle* h, const ep_tensor_t& x, const uint8_t* scales, int64_t ld_scales, int64_t C,
+                      const ep_tensor_t& to, int64_t rows) {
+  QuantArgs q{};
+  rows_in_use(h, &q);
+  q.q = static_cast<uint8_t*>(x.data);
+  q.ld_q = x.strides[0];
+  q.scales = reinterpret_cast<float*>(const_cast<uint8_t*>(scales));
+  q.ld_s = ld_scales / 4;
+  q.H = static_cast<int>(C);
+  q.rows = rows;
+  q.decoded = static_cast<uint16_t*>(to.data);
+  q.ld_d = to.strides[0];
+  return q;
+}
+
+// The gated product's backward pass; `coded`: from rows kept in 8 bits.  Those are decoded once, into the rows' gradient,
+// which takes its own values last: a BF16 copy that needs no memory.  Decoding them in the products instead, on the way
+// to LDS, costs the tiles of every column the same work again.  64 experts of 7168 x 2048, us, so / in the products:
+//   rows an expert     gated           linear           16 experts of 1024 x 768: gated     linear
+//          8        2156 / 2238      796 / 839                      50 / 49               25 / 23
+//         48        2402 / 2535      884 / 932                      60 / 62               29 / 27
+//        128        2956 / 3281     1041 / 1117                     77 / 83               35 / 34
+//        256        4255 / 4742     1562 / 1698                     96 / 100              39 / 38
 ep_status_t gated_backward(ep_handle_t handle, const ep_tensor_t* rows, const ep_tensor_t* scales, bool coded,
                            const ep_tensor_t* w_gate, const ep_tensor_t* w_up, const ep_tensor_t* grad_out,
                            int32_t activation, ep_tensor_t* grad_gate, ep_tensor_t* grad_up, ep_tensor_t* grad_rows,
@@ -1540,7 +1580,7 @@ ep_status_t gated_backward(ep_handle_t handle, const ep_tensor_t* rows, const ep
   const uint8_t* xs = nullptr;
   int64_t ld_xs = 0;
   bool fp8 = false;
-  if (coded ? !coded_rows(g, rows, scales, H, &x, &xs, &ld_xs) : !received_rows(g, rows, &x, &fp8) || fp8)
+  if (coded ? !grad_rows || !coded_rows(g, rows, scales, H, &x, &xs, &ld_xs) : !received_rows(g, rows, &x, &fp8) || fp8)
     return EP_ERR_INVALID_ARGUMENT;
   if (!product_size(I)) return EP_ERR_INVALID_ARGUMENT;
   if (!check_weights(g, w_gate, EP_DTYPE_BF16, I, H) || !check_weights(g, w_up, EP_DTYPE_BF16, I, H) ||
@@ -1556,16 +1596,14 @@ ep_status_t gated_backward(ep_handle_t handle, const ep_tensor_t* rows, const ep
   if (!holds_slots(g, x) || !holds_slots(g, d) || !holds_slots(g, dg) || !holds_slots(g, du) ||
       (grad_rows && !holds_slots(g, dx)))
     return EP_ERR_INVALID_ARGUMENT;
-  if (I > kMaxProductSize || !short_rows(g, x) || !short_rows(g, dg) || !short_rows(g, du) ||
-      !short_weights(w_gate) || !short_weights(w_up) || (coded && !short_rows(g, ld_xs)))
+  if (I > kMaxProductSize || !short_rows(g, coded ? dx : x) || !short_rows(g, dg) || !short_rows(g, du) ||
+      !short_weights(w_gate) || !short_weights(w_up))
     return EP_ERR_UNSUPPORTED;
 
   int64_t limit = std::min({x.sizes[0], d.sizes[0], dg.sizes[0], du.sizes[0]});
   if (grad_rows) limit = std::min(limit, dx.sizes[0]);
-  AlongArgs a = along_args(h, x, H, I, limit);
-  a.k_bytes = H * 2;   // of the weights
-  a.x_scales = xs;
-  a.ld_xs = ld_xs;
+  const ep_tensor_t& values = coded ? dx : x;
+  AlongArgs a = along_args(h, values, H, I, limit);
   set_weights(&a, 0, w_gate, nullptr);
   set_weights(&a, 1, w_up, nullptr);
   set_out(&a, 0, dg);
@@ -1575,7 +1613,7 @@ ep_status_t gated_backward(ep_handle_t handle, const ep_tensor_t* rows, const ep
   RowGradArgs r = row_grad_args(h, I, H, dx, limit);
   add_part(&r, dg, w_gate);
   add_part(&r, du, w_up);
-  WeightGradArgs w = weight_grad_args(h, x, xs, ld_xs, I, H, limit);
+  WeightGradArgs w = weight_grad_args(h, values, I, H, limit);
   const bool f32 = grad_w_gate && grad_w_gate->dtype == EP_DTYPE_F32;
   if (grad_w_gate) {
     add_part(&w, dg, grad_w_gate);
@@ -1586,9 +1624,10 @@ ep_status_t gated_backward(ep_handle_t handle, const ep_tensor_t* rows, const ep
   if (const ep_status_t st = fits(expert::launch_row_grad(r, s, true)); st != EP_OK) return st;
   if (const ep_status_t st = fits(expert::launch_weight_grad(w, f32, s, true)); st != EP_OK) return st;
   if (const ep_status_t st = start_products(h, s); st != EP_OK) return st;
+  if (coded) EP_HIP(launch_decode(decode_args(h, x, xs, ld_xs, H, dx, limit), s));
   EP_HIP(expert::launch_gated_grad(a, activation, s));
-  if (grad_rows) EP_HIP(expert::launch_row_grad(r, s));
   if (grad_w_gate) EP_HIP(expert::launch_weight_grad(w, f32, s));
+  if (grad_rows) EP_HIP(expert::launch_row_grad(r, s));   // last: over the decoded rows
   trace(g, coded ? "expert_gated_backward_fp8" : "expert_gated_backward", h->n);
   return EP_OK;
 }
@@ -1636,24 +1675,9 @@ EP_API ep_status_t ep_expert_quantize(ep_handle_t handle, const ep_tensor_t* x_i
   a.ld_q = qd.strides[0];
   a.scales = static_cast<float*>(sd.data);
   a.ld_s = sd.strides[0];
-  // The rows in use follow from what the handle's creation has written; the maps may not have been.
-  a.n = h->n * g->cfg.top_k;
-  a.E = g->cfg.num_experts;
-  if (g->cfg.mode == EP_MODE_LL) {
-    a.topk = h->topk;
-    a.rank_e = h->rank_e;
-    a.hist_e = h->hist_e;
-    a.K = g->cfg.top_k;
-    a.S = g->cfg.num_src_ranks;
-    a.T = h->T;
-    a.tps = h->tps;
-    a.slots = g->cfg.max_tokens_per_rank;
-  } else {
-    a.count = g->sorted ? h->cx : h->c2;
-  }
+  rows_in_use(h, &a);
   a.H = static_cast<int>(C);
   a.rows = std::min({x.sizes[0], qd.sizes[0], sd.sizes[0]});
-  a.err = g->err;
   const ep_status_t st = from_hip(launch_quantize(a, s));
   if (st == EP_OK) trace(g, "expert_quantize", h->n);
   return st;
@@ -1714,7 +1738,7 @@ ep_status_t linear_backward(ep_handle_t handle, const ep_tensor_t* x_in, const e
   const uint8_t* xs = nullptr;
   int64_t ld_xs = 0;
   if (!product_size(N) || !product_size(C)) return EP_ERR_INVALID_ARGUMENT;
-  if ((coded ? !scales || !coded_rows(g, x_in, scales, C, &x, &xs, &ld_xs)
+  if ((coded ? !scales || !grad_x || !coded_rows(g, x_in, scales, C, &x, &xs, &ld_xs)
              : !geometry_rows(g, x_in, EP_DTYPE_BF16, C, EP_TAG_TOKENS, true, &x)) ||
       !check_weights(g, w, EP_DTYPE_BF16, N, C) ||
       !geometry_rows(g, grad_out, EP_DTYPE_BF16, N, EP_TAG_TOKENS, true, &d) ||
@@ -1722,23 +1746,23 @@ ep_status_t linear_backward(ep_handle_t handle, const ep_tensor_t* x_in, const e
       (grad_w && !check_weight_grad(g, grad_w, N, C)))
     return EP_ERR_INVALID_ARGUMENT;
   if (!holds_slots(g, x) || !holds_slots(g, d) || (grad_x && !holds_slots(g, dx))) return EP_ERR_INVALID_ARGUMENT;
-  if (N > kMaxProductSize || C > kMaxProductSize || !short_rows(g, x) || !short_rows(g, d) || !short_weights(w) ||
-      (coded && !short_rows(g, ld_xs)))
+  if (N > kMaxProductSize || C > kMaxProductSize || !short_rows(g, coded ? dx : x) || !short_rows(g, d) || !short_weights(w))
     return EP_ERR_UNSUPPORTED;
 
   int64_t limit = std::min(x.sizes[0], d.sizes[0]);
   if (grad_x) limit = std::min(limit, dx.sizes[0]);
   RowGradArgs r = row_grad_args(h, N, C, dx, limit);
   add_part(&r, d, w);
-  WeightGradArgs wg = weight_grad_args(h, x, xs, ld_xs, N, C, limit);
+  WeightGradArgs wg = weight_grad_args(h, coded ? dx : x, N, C, limit);
   const bool f32 = grad_w && grad_w->dtype == EP_DTYPE_F32;
   if (grad_w) add_part(&wg, d, grad_w);
   const hipStream_t s = as_stream(stream);
   if (const ep_status_t st = fits(expert::launch_row_grad(r, s, true)); st != EP_OK) return st;
   if (const ep_status_t st = fits(expert::launch_weight_grad(wg, f32, s, true)); st != EP_OK) return st;
   if (const ep_status_t st = start_products(h, s); st != EP_OK) return st;
-  if (grad_x) EP_HIP(expert::launch_row_grad(r, s));
+  if (coded && grad_w) EP_HIP(launch_decode(decode_args(h, x, xs, ld_xs, C, dx, limit), s));
   if (grad_w) EP_HIP(expert::launch_weight_grad(wg, f32, s));
+  if (grad_x) EP_HIP(expert::launch_row_grad(r, s));   // last: over the decoded rows
   trace(g, coded ? "expert_linear_backward_fp8" : "expert_linear_backward", h->n);
   return EP_OK;
 }

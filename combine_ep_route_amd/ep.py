@@ -313,8 +313,8 @@ def ep_expert_gated_backward(handle: Handle, rows: torch.Tensor, w_gate: torch.T
 
 def ep_expert_gated_backward_fp8(handle: Handle, rows: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
                                  grad_out: torch.Tensor, grad_gate: torch.Tensor, grad_up: torch.Tensor,
-                                 activation="silu", rows_scales: Optional[torch.Tensor] = None,
-                                 grad_rows: Optional[torch.Tensor] = None,
+                                 grad_rows: torch.Tensor, activation="silu",
+                                 rows_scales: Optional[torch.Tensor] = None,
                                  grad_w_gate: Optional[torch.Tensor] = None,
                                  grad_w_up: Optional[torch.Tensor] = None, stream=None) -> None:
     r, rs, g, u = desc(rows, A.EP_TAG_TOKENS), desc(rows_scales, A.EP_TAG_SCALES), desc(w_gate), desc(w_up)
@@ -352,7 +352,7 @@ def ep_expert_linear_backward(handle: Handle, x: torch.Tensor, w: torch.Tensor, 
 
 
 def ep_expert_linear_backward_fp8(handle: Handle, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
-                                  grad_out: torch.Tensor, grad_x: Optional[torch.Tensor] = None,
+                                  grad_out: torch.Tensor, grad_x: torch.Tensor,
                                   grad_w: Optional[torch.Tensor] = None, stream=None) -> None:
     xd, xs = desc(x, A.EP_TAG_TOKENS), desc(x_scales, A.EP_TAG_SCALES)
     wd, d = desc(w), desc(grad_out, A.EP_TAG_TOKENS)

@@ -709,14 +709,15 @@ ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_t *rows
 
 /* The same from rows kept in 8 bits -- the rows that an FP8 dispatch left
  * (or ep_expert_sort put in order), or codes and scales that ep_expert_quantize
- * made -- without a BF16 copy of them: X = bf16_rne(code * scale), the values
- * that ep_dequantize_rows gives, so the results have the bits that
- * ep_expert_gated_backward gives on those.  The quantisation counts as the
- * identity.
+ * made -- without memory for a BF16 copy of them: X = bf16_rne(code * scale),
+ * the values that ep_dequantize_rows gives, lies in grad_rows until that takes
+ * its own values, and the results have the bits that ep_expert_gated_backward
+ * gives on it.  The quantisation counts as the identity.
  *   rows        : U8 packed FP8 rows of a group with an FP8 payload (rows_scales
  *                 NULL), or FP8_E4M3 [rows, H] at the dispatch geometry with
  *   rows_scales : F32 [rows, H/128] (or LL [E, S*T_max, H/128]), contiguous in
  *                 the last dimension; H a multiple of 128.
+ *   grad_rows   : BF16 [rows, H], required.
  * The rest as above; the weights are BF16. */
 ep_status_t ep_expert_gated_backward_fp8(ep_handle_t handle, const ep_tensor_t *rows,
                                          const ep_tensor_t *rows_scales, const ep_tensor_t *w_gate,
@@ -760,7 +761,8 @@ ep_status_t ep_expert_linear_backward(ep_handle_t handle, const ep_tensor_t *x, 
  *   x        : FP8_E4M3 [rows, C] at the dispatch geometry, C a multiple of 128.
  *   x_scales : F32 [rows, C/128] (or LL [E, S*T_max, C/128]), contiguous in the
  *              last dimension.
- *   w        : BF16 [E, N, C]. */
+ *   w        : BF16 [E, N, C].
+ *   grad_x   : BF16 [rows, C], required. */
 ep_status_t ep_expert_linear_backward_fp8(ep_handle_t handle, const ep_tensor_t *x,
                                           const ep_tensor_t *x_scales, const ep_tensor_t *w,
                                           const ep_tensor_t *grad_out, ep_tensor_t *grad_x,

@@ -1,7 +1,7 @@
 """Backward passes of the experts' products from rows kept in 8 bits (ep_expert_gated_backward_fp8 and
 ep_expert_linear_backward_fp8).
 
-Their operands are bf16_rne(code * scale): the results have the bits of the BF16 calls on those values, whatever the
+Their operands are bf16_rne(code * scale), which lie in the rows' gradient meanwhile: the results have the bits of the BF16 calls on those values, whatever the
 sizes, and against the 64-bit formula at code * scale an operand's rounding, 2^-8 of it, comes on top of the bounds in
 expert_util.
 """
@@ -186,7 +186,7 @@ def test_scales_and_codes_of_every_kind():
             # the other rows must be finite: 0 * inf is NaN
             si = s.clone()
             si[torch.arange(n) != i] = 0
-            ep.ep_expert_linear_backward_fp8(r.handle, q, si, w, dy, grad_w=dw)
+            ep.ep_expert_linear_backward_fp8(r.handle, q, si, w, dy, torch.empty((n, C), dtype=BF16, device="cuda"), dw)
             want = (q[i].float() * s[i].repeat_interleave(128)).to(BF16).float()
             # the matrix unit may flush bf16 subnormals of its operands
             tiny = want.abs() < 2.0 ** -126
@@ -224,9 +224,11 @@ def test_not_finite_rows():
         # the linear product's gradient is given: only the columns of the code, or of the scale's block
         w, dy = weights(E, 64, H, 6), row_tensor(r, 64, 7)
         base = torch.empty((E, 64, H), device="cuda")
-        ep.ep_expert_linear_backward_fp8(r.handle, q, s, w, dy, grad_w=base)
-        dw = torch.empty_like(base)
-        ep.ep_expert_linear_backward_fp8(r.handle, q2.view(FP8), s2, w, dy, grad_w=dw)
+        dx = out_tensor(r, H)
+        ep.ep_expert_linear_backward_fp8(r.handle, q, s, w, dy, dx, base)
+        dw, dx2 = torch.empty_like(base), out_tensor(r, H)
+        ep.ep_expert_linear_backward_fp8(r.handle, q2.view(FP8), s2, w, dy, dx2, dw)
+        same(dx, dx2, "rows do not depend on them")
         assert bool(dw[2, :, columns].isnan().all())
         dw[2, :, columns] = base[2, :, columns]
         assert torch.equal(dw, base)
@@ -240,11 +242,18 @@ def test_short_tensors_and_no_tokens():
         q, s, values, rounded = coded(r, I, 2)
         w, dy = weights(E, H, I, 3), row_tensor(r, H, 5)
         dw, dw2 = torch.empty((E, H, I), device="cuda"), torch.empty((E, H, I), device="cuda")
-        ep.ep_expert_linear_backward_fp8(r.handle, q[:keep], s[:keep], w, dy, grad_w=dw)
-        assert ep.ep_get_device_error(r.group) == A.EP_DEVERR_ROW_RANGE
-        ep.ep_expert_linear_backward(r.handle, rounded[:keep], w, dy, grad_w=dw2)
-        same(dw, dw2, "short")
-        ep.ep_get_device_error(r.group)
+        for cut in ("codes", "gradient"):
+            dx = torch.full((r.rows, I), -7.25, dtype=BF16, device="cuda")
+            if cut == "codes":
+                ep.ep_expert_linear_backward_fp8(r.handle, q[:keep], s[:keep], w, dy, dx, dw)
+            else:
+                ep.ep_expert_linear_backward_fp8(r.handle, q, s, w, dy, dx[:keep], dw)
+            assert ep.ep_get_device_error(r.group) == A.EP_DEVERR_ROW_RANGE
+            dx2 = torch.full((r.rows, I), -7.25, dtype=BF16, device="cuda")
+            ep.ep_expert_linear_backward(r.handle, rounded[:keep], w, dy, grad_x=dx2, grad_w=dw2)
+            same(dw, dw2, cut)
+            same(dx, dx2, cut)
+            ep.ep_get_device_error(r.group)
         ep.ep_expert_linear_backward_fp8(r.handle, q[:0], s[:0], w, dy[:0], grad_x=torch.empty((0, I), dtype=BF16, device="cuda"),
                                          grad_w=dw)
         assert not bool(dw.any())
@@ -260,26 +269,30 @@ def test_short_tensors_and_no_tokens():
 
 
 def test_far_rows():
-    """Codes, scales and gradients more than 2^31 bytes behind the first; strides that a tile cannot span are refused."""
+    """Codes and scales more than 2^31 bytes behind the first, with any stride; strides of the decoded rows that a tile
+    cannot span are refused."""
     say("far rows")
     E, N, C = 8, 128, 256
     with Routing("ht", 1, 300, E, 1, N, seed=2) as r:
         q, s, _, rounded = coded(r, C, 3)
-        fq, fs = 8 * 1024 * 1024 - 16, 2 * 1024 * 1024 - 3
+        fq, fs = (1 << 24) + 16, (1 << 22) + 3
         big = torch.empty((300 * fq,), dtype=torch.uint8, device="cuda").as_strided((300, C), (fq, 1))
         big.copy_(q.view(torch.uint8))
         far = torch.empty((300 * fs,), device="cuda").as_strided((300, C // 128), (fs, 1))
         far.copy_(s)
         w, dy = weights(E, N, C, 4), row_tensor(r, N, 5)
         dw, dw2 = torch.empty((E, N, C), device="cuda"), torch.empty((E, N, C), device="cuda")
-        ep.ep_expert_linear_backward_fp8(r.handle, big.view(FP8), far, w, dy, grad_w=dw)
-        ep.ep_expert_linear_backward(r.handle, rounded, w, dy, grad_w=dw2)
+        fx = 4 * 1024 * 1024 - 8
+        dx = torch.empty((300 * fx,), dtype=BF16, device="cuda").as_strided((300, C), (fx, 1))
+        dx2 = out_tensor(r, C)
+        ep.ep_expert_linear_backward_fp8(r.handle, big.view(FP8), far, w, dy, dx, dw)
+        ep.ep_expert_linear_backward(r.handle, rounded, w, dy, grad_x=dx2, grad_w=dw2)
         same(dw, dw2, "far")
-        for codes, scales in ((torch.empty((300 << 24,), dtype=torch.uint8, device="cuda").as_strided((300, C), (1 << 24, 1)).view(FP8), s),
-                              (q, torch.empty((300 << 22,), device="cuda").as_strided((300, C // 128), (1 << 22, 1)))):
-            with pytest.raises(ep.EpError) as ei:
-                ep.ep_expert_linear_backward_fp8(r.handle, codes, scales, w, dy, grad_w=dw)
-            assert ei.value.status == A.EP_ERR_UNSUPPORTED
+        same(dx.contiguous(), dx2, "far")
+        too_far = torch.empty((300 << 23,), dtype=BF16, device="cuda").as_strided((300, C), (1 << 23, 1))
+        with pytest.raises(ep.EpError) as ei:
+            ep.ep_expert_linear_backward_fp8(r.handle, q, s, w, dy, too_far, dw)
+        assert ei.value.status == A.EP_ERR_UNSUPPORTED
 
 
 def refused(status, fn, *args, **kw):
@@ -300,8 +313,12 @@ def test_refusals():
             dg, du = out_tensor(r, I), out_tensor(r, I)
             dw = torch.full((E, I, H), 9.0, device="cuda")
 
-            def gated(rows=x, scales=s, w=wg, act="silu", **kw):
-                ep.ep_expert_gated_backward_fp8(r.handle, rows, w, w, dh, dg, du, activation=act, rows_scales=scales, **kw)
+            gx = out_tensor(r, H)
+
+            def gated(rows=x, scales=s, w=wg, act="silu", grad_rows=gx, **kw):
+                ep.ep_expert_gated_backward_fp8(r.handle, rows, w, w, dh, dg, du, grad_rows, activation=act,
+                                                rows_scales=scales, **kw)
+            refused(bad, gated, grad_rows=None)
             refused(bad, gated, scales=None)                                # codes without scales
             refused(bad, gated, rows=u8)                                    # packed rows with scales
             refused(bad, gated, rows=rounded)                               # BF16 rows: the other call takes them
@@ -322,6 +339,7 @@ def test_refusals():
             w, dy, dx = weights(E, H, I, 3), row_tensor(r, H, 6), out_tensor(r, I)
             lin = ep.ep_expert_linear_backward_fp8
             refused(bad, lin, r.handle, q, None, w, dy, grad_x=dx)
+            refused(bad, lin, r.handle, q, qs, w, dy, grad_x=None)
             refused(bad, lin, r.handle, rounded[:, :I], qs, w, dy, grad_x=dx)
             refused(bad, lin, r.handle, q, qs[:-1], w, dy, grad_x=dx)
             refused(bad, lin, r.handle, q.view(torch.uint8), qs, w, dy, grad_x=dx)
@@ -329,7 +347,7 @@ def test_refusals():
             refused(bad, lin, r.handle, q, qs, w.float(), dy, grad_x=dx)
             refused(bad, lin, r.handle, q, qs, w, dy[:, :128], grad_x=dx)
             torch.cuda.synchronize()
-            assert all(bool((t == -7.25).all()) for t in (dg, du, dx)) and bool((dw == 9).all())
+            assert all(bool((t == -7.25).all()) for t in (dg, du, dx, gx)) and bool((dw == 9).all())
             assert ep.ep_get_device_error(r.group) == 0
     g = ep.ep_create_group(mode="ht", num_nodes=2, ranks_per_node=2, num_experts=E, top_k=2, max_nodes_per_token=0,
                            hidden=H, max_tokens_per_rank=4, num_src_ranks=1, payload="bf16", ht_stage2="rank")
