@@ -247,8 +247,8 @@ __global__ __launch_bounds__(C::NT, 2) void row_grad_kernel(RowGradArgs g) {
 // follow each other.  Rows past the expert's last one are zeros in both operands.
 template <class C, bool LIST>
 struct WeightGradSrc {
-  const WeightGradArgs& g;
-  const Span& s;
+  const WeightGradArgs* args;
+  Span s;
   const uint8_t *x, *dy;      // bases of the step; else the expert's first slot
   int64_t ld_dy;
   int offa[C::JA], offb[C::JB];
@@ -258,7 +258,8 @@ struct WeightGradSrc {
   static __device__ __forceinline__ int frag_a_at(int fa, int i) { return fa + i * 16; }
 
   __device__ __forceinline__ WeightGradSrc(const WeightGradArgs& g_, const Span& s_, int which, int h0_, int i0_)
-      : g(g_), s(s_), ld_dy(g_.ld_dy[which]), h0(h0_), i0(i0_) {
+      : args(&g_), s(s_), ld_dy(g_.ld_dy[which]), h0(h0_), i0(i0_) {
+    const WeightGradArgs& g = g_;
     const int v = wave_id(), back = LIST ? 0 : C::KROWS;
     x = g.x + (s.first - back) * g.ld_x;
     dy = g.dy[which] + (s.first - back) * ld_dy;
@@ -271,14 +272,17 @@ struct WeightGradSrc {
     }
   }
   __device__ __forceinline__ int offset_a(int j, int row) const {
+    const WeightGradArgs& g = *args;
     const int h = h0 + C::template across_col<C::BA>(j * C::NW + wave_id());
     return h < g.H ? row * static_cast<int>(g.ld_x) + h * 2 : kOutside;
   }
   __device__ __forceinline__ int offset_b(int j, int row) const {
+    const WeightGradArgs& g = *args;
     const int i = i0 + C::template across_col<C::BB>(j * C::NW + wave_id());
     return i < g.I ? row * static_cast<int>(ld_dy) + i * 2 : kOutside;
   }
   __device__ __forceinline__ void step() {
+    const WeightGradArgs& g = *args;
     left -= C::KROWS;
     if constexpr (!LIST) {
       x += g.ld_x * C::KROWS;
@@ -296,7 +300,7 @@ struct WeightGradSrc {
       }
     }
   }
-  __device__ __forceinline__ Rsrc a_rsrc(int) const { return rsrc(x, LIST ? kExtent : extent_of(left * g.ld_x)); }
+  __device__ __forceinline__ Rsrc a_rsrc(int) const { return rsrc(x, LIST ? kExtent : extent_of(left * args->ld_x)); }
   __device__ __forceinline__ Rsrc b_rsrc() const { return rsrc(dy, LIST ? kExtent : extent_of(left * ld_dy)); }
   __device__ __forceinline__ int a(int j) const { return offa[j]; }
   __device__ __forceinline__ int b(int j) const { return offb[j]; }
@@ -331,6 +335,75 @@ __global__ __launch_bounds__(C::NT, 2) void weight_grad_kernel(WeightGradArgs g)
     const int i = i0 + C::wave_row(r);
     return i < g.I ? g.dw[which] + e * g.dw_expert[which] + i * g.ld_dw[which] + first * ES : nullptr;
   });
+}
+
+// The same, bf16 gradients, with one workgroup a CU that takes tile after tile: while a tile's results are stored the
+// next one's first loads run, and nothing is looked up again.  64 experts of 7168 x 2048, 512 rows each, both gated
+// gradients: 2.53 ms by a workgroup a tile, 2.28 so; one bf16 gradient, skewed rows: 1.25 and 1.19.  F32 gradients do
+// not gain (256 rows each: 1.76 ms with the gradient of the rows, 1.81 so): twice the stores stand between the loads.
+// Letting the stores run on behind the next tile's first two steps took registers from the main loop (6.2 ms in all
+// became 6.7).
+template <class C, bool LIST>
+__global__ __launch_bounds__(C::NT, 2) void weight_grads_kernel(WeightGradArgs g) {
+  __shared__ int before[kMaxExperts + 1];   // rows of the experts before each
+  const int ht = (g.H + C::BA - 1) / C::BA, it = (g.I + C::BB - 1) / C::BB;
+  const int per = ht * it * g.parts, total = per * g.rows.E;
+  // An XCD's workgroups share its eighth of the tiles in turn.
+  const int part = (total + 7) >> 3, turn = gridDim.x >> 3;
+  int tile = (blockIdx.x & 7) * part + (blockIdx.x >> 3);
+  const int end = (blockIdx.x & 7) * part + part < total ? (blockIdx.x & 7) * part + part : total;
+  if (tile >= end) return;
+  if (wave_id() == 0) {
+    int at = 0;
+    for (int e0 = 0; e0 < g.rows.E; e0 += 64) {
+      const int n = e0 + lane_id() < g.rows.E ? rows_of(g.rows, e0 + lane_id()) : 0, to = scan64(n);
+      if (e0 + lane_id() < g.rows.E) before[e0 + lane_id()] = at + to - n;
+      at += __builtin_amdgcn_readlane(to, 63);
+    }
+    if (lane_id() == 0) before[g.rows.E] = at;
+  }
+  __syncthreads();
+
+  int e, which, i0, h0;
+  auto take = [&]() {
+    e = tile / per;
+    const int local = tile - e * per;
+    which = local / (ht * it);
+    const int at = local - which * ht * it;
+    i0 = at / ht * C::BB;
+    h0 = at % ht * C::BA;
+    Span s;
+    s.e = e;
+    s.before = __builtin_amdgcn_readfirstlane(before[e]);
+    s.all = s.count = __builtin_amdgcn_readfirstlane(before[e + 1]) - s.before;
+    s.first = g.rows.stride > 0 ? e * g.rows.stride : s.before;
+    keep_limit(g.rows, &s);
+    if (s.count < s.all && local == 0 && threadIdx.x == 0) atomicOr(g.rows.err, EP_DEVERR_ROW_RANGE);
+    return s;
+  };
+  Span s = take();
+  WeightGradSrc<C, LIST> src(g, s, which, h0, i0);
+  C::start(src);
+  for (;;) {
+    typename C::Acc acc = {};
+    C::finish(src, (s.count + C::KROWS - 1) / C::KROWS, g.I - i0, acc);
+
+    const int first = h0 + (wave_id() % C::WA) * C::TA, from = i0, bytes = (g.H - first) * 2;
+    uint8_t* const to = g.dw[which] + e * g.dw_expert[which] + first * 2;
+    const int64_t ld = g.ld_dw[which];
+    const bool more = tile + turn < end;
+    if (more) {
+      tile += turn;
+      s = take();
+      src = WeightGradSrc<C, LIST>(g, s, which, h0, i0);
+      C::start(src);
+    }
+    C::template store_rows<C::FA, 2, typename C::LastStage>(acc, 0, bytes, [&](int r) -> uint8_t* {
+      const int i = from + C::wave_row(r);
+      return i < g.I ? to + i * ld : nullptr;
+    });
+    if (!more) break;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -374,6 +447,7 @@ int64_t row_tiles(const ExpertRows& r, int64_t rows, int64_t per_expert) {
 }
 
 constexpr int64_t kMaxBlocks = INT32_MAX / 512;
+constexpr int kCus = 256;
 
 template <class C, int KIND, int ACT>
 hipError_t launch_along_as(const AlongArgs& a, hipStream_t stream, bool check) {
@@ -402,18 +476,26 @@ hipError_t launch_along_as(const AlongArgs& a, hipStream_t stream, bool check) {
 // the experts as a router leaves them make many tiles of the average's multiple: at 128 rows on average (256
 // experts of 7168 x 2048, bf16) the big tile takes 2.35 ms, the middle one 2.67.
 // Few big tiles leave CUs idle: 88 of them (8 experts, 256 rows each) take 48 us, middle ones 37.
-enum Size { kSmall, kMiddle, kBig };
-Size tile_size(const ExpertRows& r, int64_t rows, int64_t col_tiles) {
+// No more middle tiles than CUs (by the average rows): each has a CU's LDS to itself, and a ring of four stages keeps
+// three of them in flight instead of one.  bf16, 8 experts of 1024 x 768, us, two stages / four: gated 15.1 / 11.1 of 32
+// rows each, 17.2 / 14.4 of 128; linear 10.3 / 9.7 and 14.9 / 13.0.  With more tiles two workgroups share a CU, which
+// four stages leave no room for: 24 experts of 1152 x 712, 48 rows each, gated 19.9 / 25.8.
+enum Size { kSmall, kMiddle, kMiddleDeep, kBig };
+Size tile_size(const ExpertRows& r, int64_t rows, int64_t col_tiles, int64_t middle_col_tiles) {
   const int64_t each = rows / r.E;
   if (each <= 24) return kSmall;
-  return each <= 96 || r.E * ((each + 255) / 256) * col_tiles < 256 ? kMiddle : kBig;
+  if (each > 96 && r.E * ((each + 255) / 256) * col_tiles >= 256) return kBig;
+  return r.E * ((each + 127) / 128) * middle_col_tiles <= kCus ? kMiddleDeep : kMiddle;
 }
 
 template <bool F8, int KIND, int ACT>
 hipError_t launch_along_kind(const AlongArgs& a, hipStream_t stream, bool check) {
   const int cols = KIND == kLinear ? 256 : 128;
-  switch (tile_size(a.rows, a.rows_max, (a.N + cols - 1) / cols)) {
+  switch (tile_size(a.rows, a.rows_max, (a.N + cols - 1) / cols, (a.N + cols / 2 - 1) / (cols / 2))) {
     case kSmall: return launch_along_as<Core<128, 32, 4, 1, false, false, F8, F8 ? 3 : 4, 128>, KIND, ACT>(a, stream, check);
+    case kMiddleDeep:
+      if constexpr (!F8) return launch_along_as<Core<128, 128, 2, 2, false, false, F8, 4, 128>, KIND, ACT>(a, stream, check);
+      [[fallthrough]];
     case kMiddle: return launch_along_as<Core<128, 128, 2, 2, false, false, F8, 2, 128>, KIND, ACT>(a, stream, check);
     default: return launch_along_as<Core<256, 256, 2, 4, false, false, F8, 2, 128>, KIND, ACT>(a, stream, check);
   }
@@ -458,28 +540,36 @@ hipError_t launch_row_grad_as(const RowGradArgs& g, hipStream_t stream, bool che
   return hipGetLastError();
 }
 
+// One workgroup a CU: an eighth of them on each XCD.
 template <class C>
-hipError_t launch_weight_grad_as(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check) {
+hipError_t launch_weight_grads_as(const WeightGradArgs& g, hipStream_t stream, bool check) {
+  const int64_t tiles = static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + C::BA - 1) / C::BA) *
+                        ((g.I + C::BB - 1) / C::BB);
+  if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
+  if (check) return hipSuccess;
+  if (scattered(g.rows)) weight_grads_kernel<C, true><<<kCus, C::NT, 0, stream>>>(g);
+  else weight_grads_kernel<C, false><<<kCus, C::NT, 0, stream>>>(g);
+  return hipGetLastError();
+}
+
+template <class C, bool F32>
+hipError_t launch_weight_grad_as(const WeightGradArgs& g, hipStream_t stream, bool check) {
   const int64_t tiles = static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + C::BA - 1) / C::BA) *
                         ((g.I + C::BB - 1) / C::BB);
   if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
   if (check) return hipSuccess;
   const int blocks = static_cast<int>((tiles + 7) / 8 * 8);
-  if (scattered(g.rows)) {
-    if (f32) weight_grad_kernel<C, true, true><<<blocks, C::NT, 0, stream>>>(g);
-    else weight_grad_kernel<C, false, true><<<blocks, C::NT, 0, stream>>>(g);
-  } else {
-    if (f32) weight_grad_kernel<C, true, false><<<blocks, C::NT, 0, stream>>>(g);
-    else weight_grad_kernel<C, false, false><<<blocks, C::NT, 0, stream>>>(g);
-  }
+  if (scattered(g.rows)) weight_grad_kernel<C, F32, true><<<blocks, C::NT, 0, stream>>>(g);
+  else weight_grad_kernel<C, F32, false><<<blocks, C::NT, 0, stream>>>(g);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check) {
-  switch (tile_size(g.rows, g.rows_max, (g.N + 255) / 256)) {
+  switch (tile_size(g.rows, g.rows_max, (g.N + 255) / 256, (g.N + 127) / 128)) {
     case kSmall: return launch_row_grad_as<Core<128, 32, 4, 1, true, false, false, 4, 128>>(g, stream, check);
+    case kMiddleDeep:
     case kMiddle: return launch_row_grad_as<Core<128, 128, 2, 2, true, false, false, 4, 64>>(g, stream, check);
     default: return launch_row_grad_as<Core<256, 256, 2, 4, true, false, false, 4, 64>>(g, stream, check);
   }
@@ -493,9 +583,12 @@ hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check)
 //    512 (32 of 1024 x 1024)           42 / 37   40 / 30      2048 (128 of 1024 x 1024)  163 / 121  145 / 100
 // Near the border the big ones win where they fill the CUs a whole number of times (256, 512).
 hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check) {
-  if (static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + 255) / 256) * ((g.I + 255) / 256) < 512)
-    return launch_weight_grad_as<Core<128, 128, 2, 2, true, true, false, 4, 64>>(g, f32, stream, check);
-  return launch_weight_grad_as<Core<256, 256, 2, 4, true, true, false, 4, 64>>(g, f32, stream, check);
+  if (static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + 255) / 256) * ((g.I + 255) / 256) < 512) {
+    using Small = Core<128, 128, 2, 2, true, true, false, 4, 64>;
+    return f32 ? launch_weight_grad_as<Small, true>(g, stream, check) : launch_weight_grad_as<Small, false>(g, stream, check);
+  }
+  using Big = Core<256, 256, 2, 4, true, true, false, 4, 64>;
+  return f32 ? launch_weight_grad_as<Big, true>(g, stream, check) : launch_weight_grads_as<Big>(g, stream, check);
 }
 
 }  // namespace expert

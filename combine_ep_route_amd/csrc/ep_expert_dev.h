@@ -110,6 +110,22 @@ __device__ __forceinline__ int xcd_tile(int block, int total) {
   return (block >> 3) < part && at < total ? at : -1;
 }
 
+// Leaves rows beyond the limit out.
+__device__ __forceinline__ void keep_limit(const ExpertRows& r, Span* s) {
+  if (!scattered(r) && s->first + static_cast<int64_t>(s->count) > r.limit)
+    s->count = r.limit > s->first ? static_cast<int>(r.limit - s->first) : 0;
+}
+
+// Rows of expert e.
+__device__ __forceinline__ int rows_of(const ExpertRows& r, int e) {
+  const int32_t* p = r.count + e * r.sources;
+  if (r.sources == 1) return p[0];
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < kFewSources; ++k) n += k < r.sources ? p[k < r.sources ? k : 0] : 0;
+  return n;
+}
+
 // Every wave scans the counts on its own (E <= 1024: up to 16 consecutive experts a lane).  With BM > 0 the
 // workgroup's tile: experts in order, in each the column tiles, in each the row tiles of BM rows.  With
 // BM == 0 the span of expert `which`.
@@ -175,8 +191,7 @@ __device__ __forceinline__ Span find_span(const ExpertRows& r, int which, int co
     s.n = local / t;
     s.m = local - s.n * t;
   }
-  if (!scattered(r) && s.first + static_cast<int64_t>(s.count) > r.limit)
-    s.count = r.limit > s.first ? static_cast<int>(r.limit - s.first) : 0;
+  keep_limit(r, &s);
   return s;
 }
 
@@ -487,18 +502,23 @@ struct Core {
 
   // The main loops hold no condition: with one, the compiler waits for all LDS reads where blocks join.  So
   // loads are started past the last step too, which sources answer with zeros, and waited for at the end.
-  template <int NJ, class Src>
+  // STARTED: the first ST-1 stages are being loaded already, and the last one has been in use.
+  template <int NJ, bool STARTED, class Src>
   static __device__ __forceinline__ void run_part(Src& src, int steps, Acc& acc, uint8_t* s0, uint8_t* s1, uint8_t* s2,
                                                   uint8_t* s3) {
     const int fa = (wave_id() % WA) * Src::wave_span_a();
     constexpr bool PIPED = !F8 && FA >= 4;
+    static_assert(PIPED || !STARTED, "the pipelined loop");
     uint8_t* const last = ST == 2 ? s1 : ST == 3 ? s2 : s3;
     int t = 0;
-    issue<NJ>(src, s0);
-    if constexpr (ST > 2) issue<NJ>(src, s1);
-    if constexpr (ST > 3) issue<NJ>(src, s2);
+    if constexpr (!STARTED) {
+      issue<NJ>(src, s0);
+      if constexpr (ST > 2) issue<NJ>(src, s1);
+      if constexpr (ST > 3) issue<NJ>(src, s2);
+    }
     if constexpr (PIPED) {
       i32x4 b[NJ], a[2];
+      if constexpr (STARTED) wait_and_meet<63>();
       src.step();
 #pragma unroll
       for (int i = 0; i < kEarly && i < loads(NJ); ++i) issue_one<NJ>(src, i, last);
@@ -543,15 +563,42 @@ struct Core {
     auto all = [&](auto nj) {
       for (int p = 0; p < plan.parts(); ++p) {
         auto src = plan.source(p);
-        run_part<decltype(nj)::value>(src, steps, acc, s0, s1, s2, s3);
+        run_part<decltype(nj)::value, false>(src, steps, acc, s0, s1, s2, s3);
       }
     };
-    constexpr int Q = FB >= 4 ? FB / 4 : 1;   // the loop exists for one to four quarters of the fragments
+    by_quarters(rows, all);
+  }
+  // The main loop exists for one to four quarters of the second operand's fragments.
+  template <class F>
+  static __device__ __forceinline__ void by_quarters(int rows, F f) {
+    constexpr int Q = FB >= 4 ? FB / 4 : 1;
     const int quarters = (rows + 16 * WB * Q - 1) / (16 * WB * Q);
-    if (Q < FB && quarters <= 1) all(Int<Q>{});
-    else if (2 * Q < FB && quarters == 2) all(Int<(2 * Q < FB ? 2 * Q : FB)>{});
-    else if (3 * Q < FB && quarters == 3) all(Int<(3 * Q < FB ? 3 * Q : FB)>{});
-    else all(Int<FB>{});
+    if (Q < FB && quarters <= 1) f(Int<Q>{});
+    else if (2 * Q < FB && quarters == 2) f(Int<(2 * Q < FB ? 2 * Q : FB)>{});
+    else if (3 * Q < FB && quarters == 3) f(Int<(3 * Q < FB ? 3 * Q : FB)>{});
+    else f(Int<FB>{});
+  }
+
+  // The same in two halves, for a workgroup that takes tile after tile: the next tile's first loads run while the
+  // results of this one are stored (through the last stage, LastStage).
+  template <class Src>
+  static __device__ __forceinline__ void start(Src& src) {
+    static_assert(ST == 4 && BNC, "three stages, of which every tile loads all");
+    issue<FB>(src, stage0());
+    issue<FB>(src, stage1());
+    issue<FB>(src, stage2());
+  }
+  template <class Src>
+  static __device__ __forceinline__ void finish(Src& src, int steps, int rows, Acc& acc) {
+    uint8_t* const s0 = stage0();
+    uint8_t* const s1 = stage1();
+    uint8_t* const s2 = stage2();
+    uint8_t* const s3 = stage3();
+    if (steps <= 0) {
+      wait_and_meet<0>();
+      return;
+    }
+    by_quarters(rows, [&](auto nj) { run_part<decltype(nj)::value, true>(src, steps, acc, s0, s1, s2, s3); });
   }
 
   // -------------------------------------------------------------------------
@@ -567,10 +614,19 @@ struct Core {
     const int w = wave_id();
     return (w < NW / 2 ? stage0() : stage1()) + w % (NW / 2) * kRegion;
   }
-  template <int CF, int ES>
+  // Where the regions lie: in the first stages, or in the last one.
+  struct FirstStages {
+    static constexpr int SIZE = kRegion;
+    static __device__ __forceinline__ uint8_t* place() { return region(); }
+  };
+  struct LastStage {
+    static constexpr int SIZE = (STAGE - SCALES) / NW / 1024 * 1024;
+    static __device__ __forceinline__ uint8_t* place() { return stage3() + wave_id() * SIZE; }
+  };
+  template <int CF, int ES, class At = FirstStages>
   struct Tile {
     static constexpr int ROW = CF * 16 * ES, PIECES = ROW / 16, MASK = (PIECES < 16 ? PIECES : 16) - 1;
-    static constexpr int fit(int rows) { return rows * ROW <= kRegion ? rows : fit(rows / 2); }
+    static constexpr int fit(int rows) { return rows * ROW <= At::SIZE ? rows : fit(rows / 2); }
     static constexpr int ROUND = fit(TB);   // rows that fit the region
     static __device__ __forceinline__ int at(int row, int byte) {
       return row * ROW + ((((byte >> 4) ^ row) & MASK) << 4 | (byte & ~(16 * MASK + 15)) | (byte & 15));
@@ -581,7 +637,7 @@ struct Core {
 #pragma unroll
       for (int k = 0; k < ROUND * PIECES / 64; ++k) {
         const int n = k * 64 + lane_id(), row = n / PIECES, byte = n % PIECES * 16;
-        f(round * ROUND + row, byte, region() + at(row, byte));
+        f(round * ROUND + row, byte, At::place() + at(row, byte));
       }
     }
   };
@@ -599,9 +655,10 @@ struct Core {
   // streaming ones: the results are not read again here, the operands are, and the L2 keeps those (backward of a
   // linear product of 64 experts of 2048 x 1408 and 24 rows each: 217 us with plain stores, 176 with these; of
   // 384 rows: 417 and 408; gated and linear of 96 rows behind each other: 258 and 247).
-  template <int CF, int ES, class Row>
+  template <int CF, int ES, class At = FirstStages, class Row>
   static __device__ __forceinline__ void store_rows(const Acc& acc, int i0, int bytes, Row row) {
-    using T = Tile<CF, ES>;
+    using T = Tile<CF, ES, At>;
+    static_assert(T::ROUND % 16 == 0, "whole fragments");
     const int l = lane_id();
 #pragma unroll
     for (int round = 0; round < TB / T::ROUND; ++round) {
@@ -610,7 +667,7 @@ struct Core {
 #pragma unroll
         for (int i = 0; i < CF; ++i) {
           const f32x4 v = acc[i0 + i][round * (T::ROUND / 16) + j];
-          uint8_t* p = region() + T::at(j * 16 + (l & 15), (i * 16 + (l >> 4) * 4) * ES);
+          uint8_t* p = At::place() + T::at(j * 16 + (l & 15), (i * 16 + (l >> 4) * 4) * ES);
           if constexpr (ES == 2) *reinterpret_cast<uint2*>(p) = bf16x4(v);
           else *reinterpret_cast<f32x4*>(p) = v;
         }
