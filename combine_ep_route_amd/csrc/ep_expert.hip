@@ -86,9 +86,9 @@ struct AlongSrc {
 // Rounded to bf16: the results, and of kGatedGrad the gradients of both products, which are operands of the
 // matrix unit next (all gradients together are then 0.0023 off in norm, 0.0017 with fp32 ones in between, of
 // which the results' own rounding makes the most); all else stays fp32.
-// The 256 x 256 tile of kGatedGrad does not fit its registers: load_rows holds the gradients of all the wave's rows
-// beside 128 accumulators, and 32 registers a lane go to scratch behind the main loop (438 MB written where the
-// results are 268).  The FP8 gated one spills one.
+// The 256 x 256 tile of kGatedGrad puts 16 registers a lane aside behind its main loop, beside 128 accumulators; with
+// the gradients of all the wave's rows at a time it was 32, and 64 experts of 7168 x 2048, 512 rows each, took 1 % more
+// in all (6.24 ms, 6.17 so).  The FP8 gated one spills one.
 // Measured, 256 experts of 7168 x 2048:
 //   32768 rows, none to several hundred an expert: gated bf16 2.28 ms, 840 TFLOP/s, 11.1 GB read beyond the L2 (8.1
 //   needed: an expert's row tiles drift apart); gated FP8 1.34 ms, 1440 TFLOP/s; linear bf16 1.21 ms, 800 TFLOP/s.
@@ -119,17 +119,14 @@ __global__ __launch_bounds__(C::NT) void along_kernel(AlongArgs a) {
     return p < s.count ? static_cast<int64_t>(row_of(a.rows, s, p)) : -1;
   };
   if constexpr (KIND == kGatedGrad) {
-    uint2 d[CF][C::FB];
     auto grad_row = [&](int r) {
       const int64_t at = row(r);
       return at < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.grad + at * a.ld_grad + first);
     };
-    C::template load_rows<CF>(d, bytes, grad_row);
+    C::template for_rows<CF>(bytes, grad_row, [&](int j, const uint2 (&d)[CF]) {
 #pragma unroll
-    for (int i = 0; i < CF; ++i)
-#pragma unroll
-      for (int j = 0; j < C::FB; ++j) {
-        const uint2 b = d[i][j];
+      for (int i = 0; i < CF; ++i) {
+        const uint2 b = d[i];
         const f32x4 dh = {from_bf16(b.x & 0xffff), from_bf16(b.x >> 16), from_bf16(b.y & 0xffff), from_bf16(b.y >> 16)};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -139,6 +136,7 @@ __global__ __launch_bounds__(C::NT) void along_kernel(AlongArgs a) {
           acc[i + CF][j][k] = f * dh[k];
         }
       }
+    });
   } else if constexpr (KIND == kGated) {
 #pragma unroll
     for (int i = 0; i < CF; ++i)

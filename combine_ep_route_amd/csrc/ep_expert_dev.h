@@ -680,25 +680,39 @@ struct Core {
       turn();
     }
   }
-  // The other way: bf16 rows to the lanes' places, v[i][j] four columns as bits.
-  template <int CF, class Row>
-  static __device__ __forceinline__ void load_rows(uint2 (&v)[CF][FB], int bytes, Row row) {
+  // The other way, 16 rows at a time: f(j, v) gets the bf16 values v[i], as bits, of the lane's four columns in fragment
+  // i, rows j.  The next rows' loads run behind f.
+  template <int CF, class Row, class F>
+  static __device__ __forceinline__ void for_rows(int bytes, Row row, F f) {
     using T = Tile<CF, 2>;
+    constexpr int LOADS = (16 * T::PIECES + 63) / 64;
     const int l = lane_id();
+    uint4 next[LOADS];
+    auto load = [&](int j) {
 #pragma unroll
-    for (int round = 0; round < TB / T::ROUND; ++round) {
-      T::pieces(round, [&](int r, int byte, uint8_t* to) {
-        const uint8_t* from = row(r);
-        *reinterpret_cast<uint4*>(to) = from && byte < bytes ? *reinterpret_cast<const uint4*>(from + byte) : uint4{0, 0, 0, 0};
-      });
+      for (int k = 0; k < LOADS; ++k) {
+        const int n = k * 64 + l, byte = n % T::PIECES * 16;
+        const uint8_t* from = n < 16 * T::PIECES ? row(j * 16 + n / T::PIECES) : nullptr;
+        next[k] = from && byte < bytes ? *reinterpret_cast<const uint4*>(from + byte) : uint4{0, 0, 0, 0};
+      }
+    };
+    load(0);
+#pragma unroll
+    for (int j = 0; j < FB; ++j) {
+#pragma unroll
+      for (int k = 0; k < LOADS; ++k) {
+        const int n = k * 64 + l;
+        if (n < 16 * T::PIECES)
+          *reinterpret_cast<uint4*>(region() + T::at(n / T::PIECES, n % T::PIECES * 16)) = next[k];
+      }
+      if (j + 1 < FB) load(j + 1);
       turn();
+      uint2 v[CF];
 #pragma unroll
-      for (int j = 0; j < T::ROUND / 16; ++j)
-#pragma unroll
-        for (int i = 0; i < CF; ++i)
-          v[i][round * (T::ROUND / 16) + j] =
-              *reinterpret_cast<const uint2*>(region() + T::at(j * 16 + (l & 15), (i * 16 + (l >> 4) * 4) * 2));
+      for (int i = 0; i < CF; ++i)
+        v[i] = *reinterpret_cast<const uint2*>(region() + T::at(l & 15, (i * 16 + (l >> 4) * 4) * 2));
       turn();
+      f(j, v);
     }
   }
 };
