@@ -341,16 +341,26 @@ __global__ __launch_bounds__(C::NT, 2) void weight_grad_kernel(WeightGradArgs g)
 // not gain (256 rows each: 1.76 ms with the gradient of the rows, 1.81 so): twice the stores stand between the loads.
 // Letting the stores run on behind the next tile's first two steps took registers from the main loop (6.2 ms in all
 // became 6.7).
+// An expert's tiles take as long as it has rows: a tile without any as long as kTileRows rows (512 rows: 20 us, of
+// which 256 are 6).  The XCDs share the tiles by that measure; by their number alone, skewed rows made the fullest XCD
+// late (64 experts of 7168 x 2048, 512 rows each on average, one gradient and that of the rows: 2.32 ms, 2.13 so).
+// Below eight turns of all workgroups equal numbers do (24 experts of 1152 x 712, gated: 102.4 us, by rows 103.9).
+constexpr int kTileRows = 320, kTurns = 8;
+
+// The first tile behind the share `t` of all that the experts take; before[e]: rows of the experts before e.
+__device__ __forceinline__ int tile_behind(const int* before, int experts, int per, int64_t t) {
+  auto cost = [&](int e) { return before[e] + static_cast<int64_t>(kTileRows) * e; };   // of the experts before e
+  int e = -1;   // the last one that begins at t or before it
+  for (int e0 = 0; e0 < experts; e0 += 64) e += __popcll(__ballot(e0 + lane_id() < experts && cost(e0 + lane_id()) <= t));
+  if (cost(experts) <= t) return experts * per;
+  return e * per + static_cast<int>((t - cost(e)) * per / (cost(e + 1) - cost(e)));
+}
+
 template <class C, bool LIST>
 __global__ __launch_bounds__(C::NT, 2) void weight_grads_kernel(WeightGradArgs g) {
   __shared__ int before[kMaxExperts + 1];   // rows of the experts before each
   const int ht = (g.H + C::BA - 1) / C::BA, it = (g.I + C::BB - 1) / C::BB;
-  const int per = ht * it * g.parts, total = per * g.rows.E;
-  // An XCD's workgroups share its eighth of the tiles in turn.
-  const int part = (total + 7) >> 3, turn = gridDim.x >> 3;
-  int tile = (blockIdx.x & 7) * part + (blockIdx.x >> 3);
-  const int end = (blockIdx.x & 7) * part + part < total ? (blockIdx.x & 7) * part + part : total;
-  if (tile >= end) return;
+  const int per = ht * it * g.parts;
   if (wave_id() == 0) {
     int at = 0;
     for (int e0 = 0; e0 < g.rows.E; e0 += 64) {
@@ -361,6 +371,19 @@ __global__ __launch_bounds__(C::NT, 2) void weight_grads_kernel(WeightGradArgs g
     if (lane_id() == 0) before[g.rows.E] = at;
   }
   __syncthreads();
+  // An XCD's workgroups take its tiles in turn.
+  const int64_t all = before[g.rows.E] + static_cast<int64_t>(kTileRows) * g.rows.E;
+  const int turn = gridDim.x >> 3;
+  auto border = [&](int xcd) {
+    const int total = per * g.rows.E, part = (total + 7) >> 3;
+    if (total < kTurns * 8 * turn) return xcd * part < total ? xcd * part : total;
+    // at whole turns, or XCDs with a few tiles more would take a turn more
+    const int t = (tile_behind(before, g.rows.E, per, all * xcd / 8) + turn / 2) / turn * turn;
+    return __builtin_amdgcn_readfirstlane(xcd == 8 ? total : t);
+  };
+  int tile = border(blockIdx.x & 7) + (blockIdx.x >> 3);
+  const int end = border((blockIdx.x & 7) + 1);
+  if (tile >= end) return;
 
   int e, which, i0, h0;
   auto take = [&]() {
