@@ -148,7 +148,7 @@ struct Handle {
   int32_t* off1 = nullptr;       // HT [R]
   int32_t* c2 = nullptr;         // HT [E]
   int32_t* off2 = nullptr;       // HT [E]
-  int32_t* rank_x = nullptr;     // sorted [n_max, K]: rank of (token, k) inside its tile and expert, or -1
+  int32_t* rank_x = nullptr;     // sorted [n_max, K]: ranks of (token, k) inside its tile: by expert | by rank << 8, or -1
   int32_t* place = nullptr;      // sorted [n_max, K]: the entry's row in expert order, or -1
   int32_t* entry_row = nullptr;  // sorted [n_max, K]: the stage-2 row of the entry's rank, or -1
   int32_t* cx = nullptr;         // sorted [E]: rows per expert
@@ -207,7 +207,7 @@ struct LayoutArgs {
   int32_t* c1;           // HT out: stage-1 rows per rank [R]
   int32_t* c2;           // HT out: stage-2 rows per key [E2]
   // With the per-rank stage 2, optionally (hist_x not null) the entries' places in expert order:
-  int32_t* rank_x;       // [n, K] out: in-tile ranks per expert
+  int32_t* rank_x;       // [n, K] out: in-tile ranks by expert | by rank << 8, or -1
   int32_t* hist_x;       // [tiles, E] per-tile expert counts, rewritten as prefixes
   int32_t* cx;           // [E] out: rows per expert
   int32_t* place;        // [n, K] out: rows in expert order

@@ -148,8 +148,12 @@ __global__ __launch_bounds__(kTileThreads) void tile_count_kernel(LayoutArgs a) 
       const int slot = x / K, k = x - slot * K;
       const int key = s_key[slot][k];
       a.rank_e[i0 * K + x] = key >= 0 ? __popc(s_mask[key] & ((1u << slot) - 1u)) : -1;
-      if (by_expert)
-        a.rank_x[i0 * K + x] = key != -1 ? __popc(s_mask[E2 + N + s_e[slot][k]] & ((1u << slot) - 1u)) : -1;
+      if (by_expert) {
+        const uint32_t below = (1u << slot) - 1u;
+        const int e = s_e[slot][k];
+        a.rank_x[i0 * K + x] =
+            key != -1 ? __popc(s_mask[E2 + N + e] & below) | __popc(s_mask[div_l(e)] & below) << 8 : -1;
+      }
     }
   }
   if (a.ht) {
@@ -267,8 +271,8 @@ __device__ __forceinline__ void scan_counts(const int32_t* count, int n, int32_t
   __syncthreads();
 }
 
-// The entries' places in expert order and their ranks' rows: key offset + tile prefix + in-tile rank of each.
-// The rank's row is that of the token's first entry on the rank.  One entry a thread; every workgroup scans the
+// The entries' places in expert order and their ranks' rows: key offset + tile prefix + in-tile rank of each (the
+// latter is the token's, whichever of its entries on the rank asks).  One entry a thread; every workgroup scans the
 // totals itself.
 __global__ __launch_bounds__(kPlaceThreads) void places_kernel(LayoutArgs a) {
   __shared__ int32_t s_expert[kMaxExperts], s_rank[kMaxRanks];
@@ -279,20 +283,14 @@ __global__ __launch_bounds__(kPlaceThreads) void places_kernel(LayoutArgs a) {
   const int64_t x = static_cast<int64_t>(blockIdx.x) * kPlaceThreads + threadIdx.x;
   if (x >= a.n * K) return;
   const int64_t i = x / K;
-  const int k = static_cast<int>(x - i * K);
   const int s = static_cast<int>(i / a.T), t = static_cast<int>(i - static_cast<int64_t>(s) * a.T);
   const int64_t j = static_cast<int64_t>(s) * a.tps + t / kTile;
   const int rx = a.rank_x[x];
   int place = -1, row = -1;
   if (rx >= 0) {
     const int e = a.topk_copy[x], d = e / a.L;
-    place = s_expert[e] + a.hist_x[j * a.E + e] + rx;
-    int first = 0;
-    for (int q = k; q >= 0; --q) {
-      const int r = a.rank_e[i * K + q], eq = a.topk_copy[i * K + q];
-      if (r >= 0 && eq / a.L == d) first = r;   // of a rank's entries one has a rank in the tile
-    }
-    row = s_rank[d] + a.hist_e[j * a.E2 + d] + first;
+    place = s_expert[e] + a.hist_x[j * a.E + e] + (rx & 255);
+    row = s_rank[d] + a.hist_e[j * a.E2 + d] + (rx >> 8);
   }
   a.place[x] = place;
   a.entry_row[x] = row;
