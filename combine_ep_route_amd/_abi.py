@@ -154,11 +154,11 @@ SIGNATURES = {
     "ep_expert_unsort_backward": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _P]),
     "ep_expert_gated": (_S, [_P, _PT, _PT, _PT, _PT, _PT, ctypes.c_int32, _PT, _P]),
     "ep_expert_gated_backward": (_S, [_P, _PT, _PT, _PT, _PT, ctypes.c_int32, _PT, _PT, _PT, _PT, _PT, _P]),
-    "ep_expert_gated_backward_fp8": (_S, [_P, _PT, _PT, _PT, _PT, _PT, ctypes.c_int32, _PT, _PT, _PT, _PT, _PT, _P]),
+    "ep_expert_gated_backward_quantized": (_S, [_P, _PT, _PT, _PT, _PT, _PT, ctypes.c_int32, _PT, _PT, _PT, _PT, _PT, _P]),
     "ep_expert_quantize": (_S, [_P, _PT, _PT, _PT, _P]),
     "ep_expert_linear": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _P]),
     "ep_expert_linear_backward": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _P]),
-    "ep_expert_linear_backward_fp8": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _PT, _P]),
+    "ep_expert_linear_backward_quantized": (_S, [_P, _PT, _PT, _PT, _PT, _PT, _PT, _P]),
     "ep_residual_norm": (_S, [_P, _PT, _PT, _PT, _PT, _PT, ctypes.c_float, ctypes.c_float, ctypes.c_float, _PT, _PT,
                               _P]),
     "ep_residual_norm_workspace": (_S, [_P, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]),

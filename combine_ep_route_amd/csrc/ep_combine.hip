@@ -103,7 +103,7 @@ __global__ __launch_bounds__(KMAX <= 8 ? 1024 : 256) void combine_backward_kerne
       r[k] = k < a.K ? a.loc[i * a.K + k] : -1;
       ok[k] = r[k] >= 0 && r[k] < a.rows;
       if (k < a.K && r[k] >= a.rows && threadIdx.x == 0) atomicOr(a.err, EP_DEVERR_ROW_RANGE);
-      wk[k] = k < a.K ? (a.w ? a.w[i * a.K + k] : 1.0f) : 0.0f;   // no weights: unit weights
+      wk[k] = k < a.K ? a.w[i * a.K + k] : 0.0f;
       dot[k] = 0.0f;
     }
     for (int c = threadIdx.x; c < C; c += blockDim.x) {

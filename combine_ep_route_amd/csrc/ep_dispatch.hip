@@ -553,10 +553,10 @@ __device__ __forceinline__ int64_t rows_in_use(const QuantArgs& a) {
   return __builtin_amdgcn_readlane(sum, 63);
 }
 
-// f(row, first chunk of the lane) for every row in use, split over W waves.
-template <int NV, int ROWS, class F>
-__device__ __forceinline__ void for_rows_in_use(const QuantArgs& a, int W, F f) {
+template <int NV, int ROWS>
+__global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a, int W) {
   const int lane = threadIdx.x & 63;
+  const int C = a.H / 16;
   const int64_t waves = static_cast<int64_t>(gridDim.x) * 4;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int64_t total = a.n * W;
@@ -580,14 +580,7 @@ __device__ __forceinline__ void for_rows_in_use(const QuantArgs& a, int W, F f) 
       if (static_cast<uint32_t>(at) >= static_cast<uint32_t>(a.slots)) continue;
       i = (static_cast<int64_t>(e) * a.S + s) * a.slots + at;
     }
-    f(i, part * NV * 64 + lane);
-  }
-}
-
-template <int NV, int ROWS>
-__global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a, int W) {
-  const int C = a.H / 16;
-  for_rows_in_use<NV, ROWS>(a, W, [&](int64_t i, int c0) {
+    const int c0 = part * NV * 64 + lane;
     Raw raw[NV];
     const u32x4 zero{0, 0, 0, 0};
 #pragma unroll
@@ -607,41 +600,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantArgs a, int W) {
       store_nt(raw[v].a, a.q + i * a.ld_q + 16 * c);
       if ((c & 7) == 0) __builtin_nontemporal_store(raw[v].scale, a.scales + i * a.ld_s + (c >> 3));
     }
-  });
-}
-
-// The way back: bf16_rne(code * scale) of every row in use, ep_dequantize_rows' values.  Eight codes a lane, so that a
-// store instruction writes one run.  The rows are read again by the products behind it: plain stores.
-template <int NV, int ROWS>
-__global__ __launch_bounds__(256) void decode_kernel(QuantArgs a, int W) {
-  typedef __attribute__((ext_vector_type(2))) float f32x2;
-  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
-  typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
-  const int C = a.H / 8;
-  for_rows_in_use<NV, ROWS>(a, W, [&](int64_t i, int c0) {
-    u32x2 q[NV];
-    float s[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = c0 + v * 64;
-      q[v] = c < C ? __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(a.q + i * a.ld_q + 8 * c)) : u32x2{0, 0};
-      s[v] = c < C ? a.scales[i * a.ld_s + (c >> 4)] : 0.0f;
-    }
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = c0 + v * 64;
-      if (c >= C) continue;
-      u32x4 o;
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const int codes = static_cast<int>(q[v][w]);
-        const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(codes, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(codes, true);
-        o[2 * w] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo[0] * s[v], lo[1] * s[v]}, bf16x2));
-        o[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{hi[0] * s[v], hi[1] * s[v]}, bf16x2));
-      }
-      *reinterpret_cast<u32x4*>(a.decoded + i * a.ld_d + 8 * c) = o;
-    }
-  });
+  }
 }
 
 // Chunks per lane in one wave's share of a token: enough memory-level
@@ -686,16 +645,6 @@ hipError_t launch_quantize(const QuantArgs& a, hipStream_t stream) {
   if (a.count) quantize_kernel<kChunksPerLane, kFirst><<<grid, block, 0, stream>>>(a, W);
   else if (a.topk) quantize_kernel<kChunksPerLane, kEntries><<<grid, block, 0, stream>>>(a, W);
   else quantize_kernel<kChunksPerLane, kAll><<<grid, block, 0, stream>>>(a, W);
-  return hipGetLastError();
-}
-
-hipError_t launch_decode(const QuantArgs& a, hipStream_t stream) {
-  if (a.n == 0) return hipSuccess;
-  const int C = a.H / 8;
-  const int W = (C + 64 * kChunksPerLane - 1) / (64 * kChunksPerLane);
-  const dim3 grid(grid_blocks((a.n * W + 3) / 4, 256)), block(256);
-  if (a.count) decode_kernel<kChunksPerLane, kFirst><<<grid, block, 0, stream>>>(a, W);
-  else decode_kernel<kChunksPerLane, kEntries><<<grid, block, 0, stream>>>(a, W);
   return hipGetLastError();
 }
 

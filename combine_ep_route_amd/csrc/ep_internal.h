@@ -290,12 +290,8 @@ struct QuantArgs {
   int32_t E, K, S, T, tps, slots;
   int64_t rows;
   int32_t* err;
-  uint16_t* decoded;      // launch_decode: BF16 [n, H] out, from q and scales
-  int64_t ld_d;           // elements
 };
 hipError_t launch_quantize(const QuantArgs& a, hipStream_t stream);
-// Codes of the experts' rows that hold a message (count, or topk, rank_e and hist_e given) to bf16.
-hipError_t launch_decode(const QuantArgs& a, hipStream_t stream);
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t stream);
 
@@ -320,7 +316,7 @@ hipError_t launch_combine_backward(const CombineBwdArgs& a, hipStream_t stream);
 // Between the ranks' stage-2 rows and rows in expert order.  Every entry (i, k) of a token has a place, the row
 // in expert order, and a row, the one of its rank; entries of a token on the same rank share it.
 struct SortArgs {
-  const uint8_t* x;       // the ranks' rows
+  const uint8_t* x;       // the ranks' rows, or without `row` one row a token
   int64_t ld_x;           // bytes
   int64_t rows_x;
   uint8_t* out;           // rows in expert order
@@ -328,7 +324,7 @@ struct SortArgs {
   int64_t rows_out;
   int32_t bytes;          // of a row, a multiple of 4
   int32_t pad;            // bytes behind them that are written as zeros: the row's last line whole, or 0
-  const int32_t* row;     // [n, K]
+  const int32_t* row;     // [n, K], or null: entry (i, k) has row i
   const int32_t* place;   // [n, K]
   int64_t n;
   int K;
@@ -458,6 +454,25 @@ struct WeightGradArgs {
   int64_t ld_dw[2], dw_expert[2];
 };
 hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check = false);
+
+// Codes of the experts' rows to bf16: bf16_rne(code * scale), ep_dequantize_rows' values.
+// The rows are the first ones, as many as `count` sums up to, or without it the slots of the entries.
+struct DecodeArgs {
+  const uint8_t* x;                   // codes
+  int64_t ld_x;                       // bytes
+  const float* scales;                // one per 128 codes of a row
+  int64_t ld_s;                       // elements
+  int32_t C;                          // codes of a row
+  uint16_t* out;
+  int64_t ld_out;                     // elements
+  int64_t rows;                       // that the tensors hold
+  int64_t n;                          // entries: a bound on the rows in use
+  const int32_t* count;               // [E]
+  const int32_t *topk, *rank_e, *hist_e;   // LL: an entry's expert, its rank among its tile's, the tile's prefix
+  int32_t E, K, S, T, tps, slots;
+  int32_t* err;
+};
+hipError_t launch_decode(const DecodeArgs& a, hipStream_t stream);
 
 // LL with several sources: rows per expert and the list of rows, from the slots' counts [E, S].
 hipError_t launch_list_rows(const int32_t* counts, int E, int S, int slots, int32_t* total, int32_t* list,

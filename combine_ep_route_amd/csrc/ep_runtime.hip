@@ -1031,7 +1031,7 @@ EP_API ep_status_t ep_combine_backward(ep_handle_t handle, const ep_tensor_t* gr
   Group* g = h->g;
   const int H = g->cfg.hidden, K = g->cfg.top_k;
   const bool ll = g->cfg.mode == EP_MODE_LL;
-  // Rows of ranks are weighted already: nothing but the rows to differentiate here, by unit weights.
+  // Rows of ranks are weighted already: only the rows to differentiate here, each a copy of its token's gradient.
   if (g->s2_rank && !g->sorted) return EP_ERR_UNSUPPORTED;
   if (!check2d(grad_out, EP_DTYPE_BF16, h->n, H, EP_TAG_TOKENS, true)) return EP_ERR_INVALID_ARGUMENT;
   if (g->sorted ? topk_weights || expert_out || grad_weights
@@ -1048,6 +1048,27 @@ EP_API ep_status_t ep_combine_backward(ep_handle_t handle, const ep_tensor_t* gr
   if (const ep_status_t st = ensure_device(g, s); st != EP_OK) return st;
   h->stream = s;
   if (const ep_status_t st = ensure_maps(h, s); st != EP_OK) return st;
+  if (g->sorted) {
+    SortArgs a{};
+    a.x = static_cast<const uint8_t*>(grad_out->data);
+    a.ld_x = grad_out->strides[0] * 2;
+    a.rows_x = h->n;
+    a.out = static_cast<uint8_t*>(dy2.data);
+    a.ld_out = dy2.strides[0] * 2;
+    a.rows_out = dy2.sizes[0];
+    a.bytes = 2 * H;
+    a.place = h->row2;   // -1 at all but one of a token's entries on a rank
+    a.n = h->n;
+    a.K = K;
+    a.max_blocks = dispatch_block_cap(g);
+    a.err = g->err;
+    const ep_status_t st = from_hip(launch_sort(a, s));
+    if (st == EP_OK) {
+      ++g->stats.combine_backward_calls;
+      trace(g, "combine_backward", h->n);
+    }
+    return st;
+  }
   CombineBwdArgs a{};
   a.g = static_cast<const uint16_t*>(grad_out->data);
   a.ld_g = grad_out->strides[0];
@@ -1056,7 +1077,7 @@ EP_API ep_status_t ep_combine_backward(ep_handle_t handle, const ep_tensor_t* gr
   a.dy = static_cast<uint16_t*>(dy2.data);
   a.ld_dy = dy2.strides[0];
   a.rows = expert_out ? std::min(dy2.sizes[0], y2.sizes[0]) : dy2.sizes[0];
-  a.w = topk_weights ? static_cast<const float*>(topk_weights->data) : nullptr;
+  a.w = static_cast<const float*>(topk_weights->data);
   a.loc = ll ? h->slot_map : h->row2;
   a.dw = grad_weights ? static_cast<float*>(grad_weights->data) : nullptr;
   a.n = h->n;
@@ -1276,6 +1297,7 @@ EP_API ep_status_t ep_expert_unsort_backward(ep_handle_t handle, const ep_tensor
 namespace {
 
 using expert::AlongArgs;
+using expert::DecodeArgs;
 using expert::ExpertRows;
 using expert::RowGradArgs;
 using expert::WeightGradArgs;
@@ -1359,27 +1381,6 @@ ExpertRows rows_of_experts(const Handle* h, int64_t limit) {
     }
   }
   return r;
-}
-
-// The experts' rows that hold a message, for the quantiser: from what the handle's creation has written; the maps may
-// not have been.
-void rows_in_use(const Handle* h, QuantArgs* a) {
-  const Group* g = h->g;
-  a->n = h->n * g->cfg.top_k;
-  a->E = g->cfg.num_experts;
-  a->err = g->err;
-  if (g->cfg.mode == EP_MODE_LL) {
-    a->topk = h->topk;
-    a->rank_e = h->rank_e;
-    a->hist_e = h->hist_e;
-    a->K = g->cfg.top_k;
-    a->S = g->cfg.num_src_ranks;
-    a->T = h->T;
-    a->tps = h->tps;
-    a->slots = g->cfg.max_tokens_per_rank;
-  } else {
-    a->count = g->sorted ? h->cx : h->c2;
-  }
 }
 
 // Enqueues what the products need first: the rows' list in LL with many
@@ -1543,19 +1544,34 @@ bool coded_rows(const Group* g, const ep_tensor_t* t, const ep_tensor_t* scales,
 }
 
 // The decoding of rows kept in 8 bits into `to`.
-QuantArgs decode_args(const Handle* h, const ep_tensor_t& x, const uint8_t* scales, int64_t ld_scales, int64_t C,
-                      const ep_tensor_t& to, int64_t rows) {
-  QuantArgs q{};
-  rows_in_use(h, &q);
-  q.q = static_cast<uint8_t*>(x.data);
-  q.ld_q = x.strides[0];
-  q.scales = reinterpret_cast<float*>(const_cast<uint8_t*>(scales));
-  q.ld_s = ld_scales / 4;
-  q.H = static_cast<int>(C);
-  q.rows = rows;
-  q.decoded = static_cast<uint16_t*>(to.data);
-  q.ld_d = to.strides[0];
-  return q;
+DecodeArgs decode_args(const Handle* h, const ep_tensor_t& x, const uint8_t* scales, int64_t ld_scales, int64_t C,
+                       const ep_tensor_t& to, int64_t rows) {
+  const Group* g = h->g;
+  DecodeArgs a{};
+  a.x = static_cast<const uint8_t*>(x.data);
+  a.ld_x = x.strides[0];
+  a.scales = reinterpret_cast<const float*>(scales);
+  a.ld_s = ld_scales / 4;
+  a.C = static_cast<int32_t>(C);
+  a.out = static_cast<uint16_t*>(to.data);
+  a.ld_out = to.strides[0];
+  a.rows = rows;
+  a.n = h->n * g->cfg.top_k;
+  a.E = g->cfg.num_experts;
+  a.err = g->err;
+  if (g->cfg.mode == EP_MODE_LL) {
+    a.topk = h->topk;
+    a.rank_e = h->rank_e;
+    a.hist_e = h->hist_e;
+    a.K = g->cfg.top_k;
+    a.S = g->cfg.num_src_ranks;
+    a.T = h->T;
+    a.tps = h->tps;
+    a.slots = g->cfg.max_tokens_per_rank;
+  } else {
+    a.count = g->sorted ? h->cx : h->c2;
+  }
+  return a;
 }
 
 // The gated product's backward pass; `coded`: from rows kept in 8 bits.  Those are decoded once, into the rows' gradient,
@@ -1624,11 +1640,11 @@ ep_status_t gated_backward(ep_handle_t handle, const ep_tensor_t* rows, const ep
   if (const ep_status_t st = fits(expert::launch_row_grad(r, s, true)); st != EP_OK) return st;
   if (const ep_status_t st = fits(expert::launch_weight_grad(w, f32, s, true)); st != EP_OK) return st;
   if (const ep_status_t st = start_products(h, s); st != EP_OK) return st;
-  if (coded) EP_HIP(launch_decode(decode_args(h, x, xs, ld_xs, H, dx, limit), s));
+  if (coded) EP_HIP(expert::launch_decode(decode_args(h, x, xs, ld_xs, H, dx, limit), s));
   EP_HIP(expert::launch_gated_grad(a, activation, s));
   if (grad_w_gate) EP_HIP(expert::launch_weight_grad(w, f32, s));
   if (grad_rows) EP_HIP(expert::launch_row_grad(r, s));   // last: over the decoded rows
-  trace(g, coded ? "expert_gated_backward_fp8" : "expert_gated_backward", h->n);
+  trace(g, coded ? "expert_gated_backward_quantized" : "expert_gated_backward", h->n);
   return EP_OK;
 }
 
@@ -1642,11 +1658,12 @@ EP_API ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_
                         grad_w_gate, grad_w_up, stream);
 }
 
-EP_API ep_status_t ep_expert_gated_backward_fp8(ep_handle_t handle, const ep_tensor_t* rows, const ep_tensor_t* rows_scales,
-                                                const ep_tensor_t* w_gate, const ep_tensor_t* w_up,
-                                                const ep_tensor_t* grad_out, int32_t activation,
-                                                ep_tensor_t* grad_gate, ep_tensor_t* grad_up, ep_tensor_t* grad_rows,
-                                                ep_tensor_t* grad_w_gate, ep_tensor_t* grad_w_up, ep_stream_t stream) {
+EP_API ep_status_t ep_expert_gated_backward_quantized(ep_handle_t handle, const ep_tensor_t* rows,
+                                                      const ep_tensor_t* rows_scales, const ep_tensor_t* w_gate,
+                                                      const ep_tensor_t* w_up, const ep_tensor_t* grad_out,
+                                                      int32_t activation, ep_tensor_t* grad_gate, ep_tensor_t* grad_up,
+                                                      ep_tensor_t* grad_rows, ep_tensor_t* grad_w_gate,
+                                                      ep_tensor_t* grad_w_up, ep_stream_t stream) {
   return gated_backward(handle, rows, rows_scales, true, w_gate, w_up, grad_out, activation, grad_gate, grad_up, grad_rows,
                         grad_w_gate, grad_w_up, stream);
 }
@@ -1675,9 +1692,24 @@ EP_API ep_status_t ep_expert_quantize(ep_handle_t handle, const ep_tensor_t* x_i
   a.ld_q = qd.strides[0];
   a.scales = static_cast<float*>(sd.data);
   a.ld_s = sd.strides[0];
-  rows_in_use(h, &a);
+  // The rows in use follow from what the handle's creation has written; the maps may not have been.
+  a.n = h->n * g->cfg.top_k;
+  a.E = g->cfg.num_experts;
+  if (g->cfg.mode == EP_MODE_LL) {
+    a.topk = h->topk;
+    a.rank_e = h->rank_e;
+    a.hist_e = h->hist_e;
+    a.K = g->cfg.top_k;
+    a.S = g->cfg.num_src_ranks;
+    a.T = h->T;
+    a.tps = h->tps;
+    a.slots = g->cfg.max_tokens_per_rank;
+  } else {
+    a.count = g->sorted ? h->cx : h->c2;
+  }
   a.H = static_cast<int>(C);
   a.rows = std::min({x.sizes[0], qd.sizes[0], sd.sizes[0]});
+  a.err = g->err;
   const ep_status_t st = from_hip(launch_quantize(a, s));
   if (st == EP_OK) trace(g, "expert_quantize", h->n);
   return st;
@@ -1760,10 +1792,10 @@ ep_status_t linear_backward(ep_handle_t handle, const ep_tensor_t* x_in, const e
   if (const ep_status_t st = fits(expert::launch_row_grad(r, s, true)); st != EP_OK) return st;
   if (const ep_status_t st = fits(expert::launch_weight_grad(wg, f32, s, true)); st != EP_OK) return st;
   if (const ep_status_t st = start_products(h, s); st != EP_OK) return st;
-  if (coded && grad_w) EP_HIP(launch_decode(decode_args(h, x, xs, ld_xs, C, dx, limit), s));
+  if (coded && grad_w) EP_HIP(expert::launch_decode(decode_args(h, x, xs, ld_xs, C, dx, limit), s));
   if (grad_w) EP_HIP(expert::launch_weight_grad(wg, f32, s));
   if (grad_x) EP_HIP(expert::launch_row_grad(r, s));   // last: over the decoded rows
-  trace(g, coded ? "expert_linear_backward_fp8" : "expert_linear_backward", h->n);
+  trace(g, coded ? "expert_linear_backward_quantized" : "expert_linear_backward", h->n);
   return EP_OK;
 }
 
@@ -1775,9 +1807,10 @@ EP_API ep_status_t ep_expert_linear_backward(ep_handle_t handle, const ep_tensor
   return linear_backward(handle, x, nullptr, false, w, grad_out, grad_x, grad_w, stream);
 }
 
-EP_API ep_status_t ep_expert_linear_backward_fp8(ep_handle_t handle, const ep_tensor_t* x, const ep_tensor_t* x_scales,
-                                                 const ep_tensor_t* w, const ep_tensor_t* grad_out, ep_tensor_t* grad_x,
-                                                 ep_tensor_t* grad_w, ep_stream_t stream) {
+EP_API ep_status_t ep_expert_linear_backward_quantized(ep_handle_t handle, const ep_tensor_t* x,
+                                                       const ep_tensor_t* x_scales, const ep_tensor_t* w,
+                                                       const ep_tensor_t* grad_out, ep_tensor_t* grad_x,
+                                                       ep_tensor_t* grad_w, ep_stream_t stream) {
   return linear_backward(handle, x, x_scales, true, w, grad_out, grad_x, grad_w, stream);
 }
 

@@ -6,6 +6,7 @@
 //   sort:             S[place(i,k)] = X[row(i,k)]
 //   unsort:           P[r] = bf16_rne(fma chain in k order from +0 of w[i,k] Y[place(i,k)]) over the entries on r
 //   sort, backward:   the same with unit weights
+//   the adjoint of adding the ranks' rows up per token: the sort with the token as row, the rank's row as place
 //   unsort, backward: dY[place(i,k)] = bf16_rne(w[i,k] dP[row(i,k)]), dw[i,k] = <dP[row(i,k)], Y[place(i,k)]>
 //
 // All move rows and compute next to nothing, so the memory bounds them (a copy of 2 GiB: 4.87 TB/s of reads and
@@ -47,6 +48,8 @@ __device__ __forceinline__ u32x4 pack(const float (&f)[8]) {
 }
 
 // Up to kBatch entries of a token from k0 on: row and place, -1 where there is none or the tensors do not hold it.
+// Not MAPPED: a token's one row.
+template <bool MAPPED = true>
 struct Entries {
   int32_t row[kBatch], place[kBatch];
   bool beyond = false;
@@ -55,7 +58,7 @@ struct Entries {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const bool in = k0 + b < K;
-      row[b] = in ? rows[i * K + k0 + b] : -1;
+      row[b] = !in ? -1 : MAPPED ? rows[i * K + k0 + b] : static_cast<int32_t>(i);
       place[b] = in ? places[i * K + k0 + b] : -1;
       beyond |= row[b] >= rows_max || place[b] >= places_max;
       if (row[b] >= rows_max) row[b] = -1;
@@ -74,6 +77,7 @@ struct Entries {
 
 // Every entry loads its row itself: entries of a token that share one meet in the cache (loading it once for all of
 // them took the branches' 51 spilled scalars: the smallest sort 3.45 us, so 3.0).
+template <bool MAPPED>
 __global__ __launch_bounds__(256) void sort_kernel(SortArgs a) {
   const int at = (blockIdx.x * blockDim.x + threadIdx.x) * 16;
   const int end = a.bytes + a.pad;
@@ -81,7 +85,7 @@ __global__ __launch_bounds__(256) void sort_kernel(SortArgs a) {
   const int words = (end - at) >> 2;      // 4-byte words that this lane writes, four at most
   for (int64_t i = blockIdx.y; i < a.n; i += gridDim.y) {
     for (int k0 = 0; k0 < a.K; k0 += kBatch) {
-      const Entries t(a.row, a.place, i, a.K, k0, a.rows_x, a.rows_out);
+      const Entries<MAPPED> t(a.row, a.place, i, a.K, k0, a.rows_x, a.rows_out);
       if (t.beyond && at == 0) atomicOr(a.err, EP_DEVERR_ROW_RANGE);
       u32x4 v[kBatch];
 #pragma unroll
@@ -125,7 +129,7 @@ __global__ __launch_bounds__(256) void unsort_kernel(UnsortArgs a) {
   };
   for (int64_t i = blockIdx.y; i < a.n; i += gridDim.y) {
     if constexpr (FEW) {
-      const Entries t(a.row, a.place, i, a.K, 0, a.rows_out, a.rows_y);
+      const Entries<> t(a.row, a.place, i, a.K, 0, a.rows_out, a.rows_y);
       if (t.beyond && c == 0) atomicOr(a.err, EP_DEVERR_ROW_RANGE);
       u32x4 v[kBatch];
       float w[kBatch];
@@ -195,7 +199,7 @@ __global__ __launch_bounds__(512) void unsort_backward_kernel(UnsortBwdArgs a) {
   const int lane = threadIdx.x & 63, at = threadIdx.x >> 6, waves = blockDim.x >> 6;
   for (int64_t i = blockIdx.x; i < a.n; i += gridDim.x) {
     for (int k0 = 0; k0 < a.K; k0 += kBatch) {
-      const Entries t(a.row, a.place, i, a.K, k0, a.rows_g, a.rows_y);
+      const Entries<> t(a.row, a.place, i, a.K, k0, a.rows_g, a.rows_y);
       if (t.beyond && threadIdx.x == 0) atomicOr(a.err, EP_DEVERR_ROW_RANGE);
       float w[kBatch], dot[kBatch] = {};
 #pragma unroll
@@ -260,7 +264,9 @@ dim3 grid_for(int64_t n, int cols, int max_blocks) {
 hipError_t launch_sort(const SortArgs& a, hipStream_t stream) {
   if (a.n == 0) return hipSuccess;
   const int C = (a.bytes + a.pad + 15) / 16, threads = threads_for(C, 256);
-  sort_kernel<<<grid_for(a.n, (C + threads - 1) / threads, a.max_blocks), threads, 0, stream>>>(a);
+  const dim3 grid = grid_for(a.n, (C + threads - 1) / threads, a.max_blocks);
+  if (a.row) sort_kernel<true><<<grid, threads, 0, stream>>>(a);
+  else sort_kernel<false><<<grid, threads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

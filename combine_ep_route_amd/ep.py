@@ -317,12 +317,13 @@ def ep_expert_gated_backward_fp8(handle: Handle, rows: torch.Tensor, w_gate: tor
                                  rows_scales: Optional[torch.Tensor] = None,
                                  grad_w_gate: Optional[torch.Tensor] = None,
                                  grad_w_up: Optional[torch.Tensor] = None, stream=None) -> None:
+    """ep_expert_gated_backward_quantized."""
     r, rs, g, u = desc(rows, A.EP_TAG_TOKENS), desc(rows_scales, A.EP_TAG_SCALES), desc(w_gate), desc(w_up)
     d = desc(grad_out, A.EP_TAG_TOKENS)
     dg, du = desc(grad_gate, A.EP_TAG_TOKENS), desc(grad_up, A.EP_TAG_TOKENS)
     dr = desc(grad_rows, A.EP_TAG_TOKENS)
     wg, wu = desc(grad_w_gate), desc(grad_w_up)
-    _check("ep_expert_gated_backward_fp8", A.lib().ep_expert_gated_backward_fp8(
+    _check("ep_expert_gated_backward_quantized", A.lib().ep_expert_gated_backward_quantized(
         handle.ptr, _ref(r), _ref(rs), _ref(g), _ref(u), _ref(d), _activation(activation), _ref(dg), _ref(du),
         _ref(dr), _ref(wg), _ref(wu), _stream(stream)))
 
@@ -354,10 +355,11 @@ def ep_expert_linear_backward(handle: Handle, x: torch.Tensor, w: torch.Tensor, 
 def ep_expert_linear_backward_fp8(handle: Handle, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
                                   grad_out: torch.Tensor, grad_x: torch.Tensor,
                                   grad_w: Optional[torch.Tensor] = None, stream=None) -> None:
+    """ep_expert_linear_backward_quantized."""
     xd, xs = desc(x, A.EP_TAG_TOKENS), desc(x_scales, A.EP_TAG_SCALES)
     wd, d = desc(w), desc(grad_out, A.EP_TAG_TOKENS)
     dx, dw = desc(grad_x, A.EP_TAG_TOKENS), desc(grad_w)
-    _check("ep_expert_linear_backward_fp8", A.lib().ep_expert_linear_backward_fp8(
+    _check("ep_expert_linear_backward_quantized", A.lib().ep_expert_linear_backward_quantized(
         handle.ptr, _ref(xd), _ref(xs), _ref(wd), _ref(d), _ref(dx), _ref(dw), _stream(stream)))
 
 

@@ -719,13 +719,13 @@ ep_status_t ep_expert_gated_backward(ep_handle_t handle, const ep_tensor_t *rows
  *                 the last dimension; H a multiple of 128.
  *   grad_rows   : BF16 [rows, H], required.
  * The rest as above; the weights are BF16. */
-ep_status_t ep_expert_gated_backward_fp8(ep_handle_t handle, const ep_tensor_t *rows,
-                                         const ep_tensor_t *rows_scales, const ep_tensor_t *w_gate,
-                                         const ep_tensor_t *w_up, const ep_tensor_t *grad_out,
-                                         int32_t activation, ep_tensor_t *grad_gate,
-                                         ep_tensor_t *grad_up, ep_tensor_t *grad_rows,
-                                         ep_tensor_t *grad_w_gate, ep_tensor_t *grad_w_up,
-                                         ep_stream_t stream);
+ep_status_t ep_expert_gated_backward_quantized(ep_handle_t handle, const ep_tensor_t *rows,
+                                               const ep_tensor_t *rows_scales, const ep_tensor_t *w_gate,
+                                               const ep_tensor_t *w_up, const ep_tensor_t *grad_out,
+                                               int32_t activation, ep_tensor_t *grad_gate,
+                                               ep_tensor_t *grad_up, ep_tensor_t *grad_rows,
+                                               ep_tensor_t *grad_w_gate, ep_tensor_t *grad_w_up,
+                                               ep_stream_t stream);
 
 /* FP8 quantisation of the experts' rows, for an FP8 product behind ep_expert_gated
  * and for a backward pass from 8 bits:
@@ -757,16 +757,16 @@ ep_status_t ep_expert_linear_backward(ep_handle_t handle, const ep_tensor_t *x, 
                                       const ep_tensor_t *grad_out, ep_tensor_t *grad_x,
                                       ep_tensor_t *grad_w, ep_stream_t stream);
 
-/* The same from rows kept in 8 bits (as ep_expert_gated_backward_fp8):
+/* The same from rows kept in 8 bits (as ep_expert_gated_backward_quantized):
  *   x        : FP8_E4M3 [rows, C] at the dispatch geometry, C a multiple of 128.
  *   x_scales : F32 [rows, C/128] (or LL [E, S*T_max, C/128]), contiguous in the
  *              last dimension.
  *   w        : BF16 [E, N, C].
  *   grad_x   : BF16 [rows, C], required. */
-ep_status_t ep_expert_linear_backward_fp8(ep_handle_t handle, const ep_tensor_t *x,
-                                          const ep_tensor_t *x_scales, const ep_tensor_t *w,
-                                          const ep_tensor_t *grad_out, ep_tensor_t *grad_x,
-                                          ep_tensor_t *grad_w, ep_stream_t stream);
+ep_status_t ep_expert_linear_backward_quantized(ep_handle_t handle, const ep_tensor_t *x,
+                                                const ep_tensor_t *x_scales, const ep_tensor_t *w,
+                                                const ep_tensor_t *grad_out, ep_tensor_t *grad_x,
+                                                ep_tensor_t *grad_w, ep_stream_t stream);
 
 /* ----------------------------------------------------------------------- */
 /* Norms around the block                                                    */
