@@ -379,7 +379,7 @@ __global__ __launch_bounds__(C::NT, 2) void weight_grads_kernel(WeightGradArgs g
     if (total < kTurns * 8 * turn) return xcd * part < total ? xcd * part : total;
     // at whole turns, or XCDs with a few tiles more would take a turn more
     const int t = (tile_behind(before, g.rows.E, per, all * xcd / 8) + turn / 2) / turn * turn;
-    return __builtin_amdgcn_readfirstlane(xcd == 8 ? total : t);
+    return __builtin_amdgcn_readfirstlane(xcd == 8 || t > total ? total : t);   // the last turn may be a part of one
   };
   int tile = border(blockIdx.x & 7) + (blockIdx.x >> 3);
   const int end = border((blockIdx.x & 7) + 1);
