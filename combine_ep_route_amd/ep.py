@@ -177,7 +177,10 @@ def ep_layout_noalloc(topk_idx: torch.Tensor, maps: dict, device_error: Optional
                       stream=None, **config) -> None:
     """The handle's maps for topk_idx without a group or an allocation:
     maps is {ep_map_t id: int32 device tensor} for the configuration's mode;
-    config takes ep_create_group's keyword arguments."""
+    config takes ep_create_group's keyword arguments.  The places in expert
+    order come with a handle only."""
+    if not all(0 <= m < 8 for m in maps):
+        raise ValueError(f"ep_layout_noalloc: no map {[m for m in maps if not 0 <= m < 8]}")
     cfg = make_config(**config)
     t = desc(topk_idx, A.EP_TAG_TOPK_IDX)
     descs = [desc(maps[m]) if m in maps else None for m in range(8)]

@@ -23,8 +23,8 @@
  *    without waiting, except the functions documented as blocking.
  *  - A group, and every handle made from it, is used from one stream at a
  *    time, except where a function says otherwise (the experts' products,
- *    ep_expert_quantize, the moves into expert order and back); the library takes no locks, so host threads that
- *    share a group take turns.
+ *    ep_expert_quantize, the moves into expert order and back); the library
+ *    takes no locks, so host threads that share a group take turns.
  *  - Arguments are validated on the host before any HIP call; a rejected call
  *    enqueues nothing.  Routing entries are checked on the device and
  *    reported through the group's device error word (ep_get_device_error).
@@ -319,6 +319,8 @@ ep_status_t ep_handle_get_map(ep_handle_t handle, int32_t which, ep_tensor_t *vi
  *              (E2 = E, or R with the per-rank stage 2), 1-D or [., 1].
  *              Every map of the mode is required and contiguous; the other
  *              mode's entries must be NULL.  Device memory, caller-owned.
+ *              PER_RANK_SORTED gives PER_RANK's maps; the places in expert
+ *              order come with a handle only.
  *   device_error : optional I32 [1] device buffer: set to 0, then to the
  *              EP_DEVERR_* bits of invalid or repeated entries.
  * Its working storage (a copy of topk_idx, in-tile ranks, tile counts, a

@@ -3,8 +3,9 @@ calls refuse without a handle (CPU only; groups on host memory)."""
 import ctypes
 
 import pytest
+import torch
 
-from combine_ep_route_amd import _abi as A
+from combine_ep_route_amd import _abi as A, ep
 from test_abi_host import FAKE, HostPool, _cfg, _create, _t
 
 BAD = A.EP_ERR_INVALID_ARGUMENT
@@ -58,3 +59,12 @@ def test_calls_without_a_handle():
         assert lib.ep_expert_sort_backward(h, r(t), r(t), None) == BAD
         assert lib.ep_expert_unsort(h, r(t), r(w), r(t), None) == BAD
         assert lib.ep_expert_unsort_backward(h, r(t), None, r(w), r(t), None, None) == BAD
+
+
+def test_places_without_a_handle_are_refused():
+    """The layout without a group has no places: asking for them is an error, not a tensor left as it was."""
+    topk = torch.zeros((4, 2), dtype=torch.int32)
+    for which in (A.EP_MAP_HT_SORTED_ROW, A.EP_MAP_HT_SORTED_COUNT):
+        with pytest.raises(ValueError):
+            ep.ep_layout_noalloc(topk, {which: torch.zeros((4, 2), dtype=torch.int32)}, mode="ht",
+                                 ht_stage2="rank_sorted", top_k=2)
