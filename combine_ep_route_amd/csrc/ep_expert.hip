@@ -428,6 +428,40 @@ __global__ __launch_bounds__(C::NT, 2) void weight_grads_kernel(WeightGradArgs g
 }
 
 // ---------------------------------------------------------------------------
+// Rows per expert where several sources fill their own slots (LL)
+// ---------------------------------------------------------------------------
+
+// One workgroup (256 threads) per expert: its rows (e*S + s)*T_max + slot for all sources in order, at the sum of the
+// counts before it.  Each workgroup sums those counts itself: E*S of them at most, from the L2.  64 experts with 4
+// sources: 3 us, the launch.
+__device__ __forceinline__ void list_rows(const int32_t* counts, int e, int S, int slots, int32_t* total, int32_t* list) {
+  __shared__ int part[4];
+  int sum = 0;
+  for (int i = threadIdx.x; i < e * S; i += 256) sum += counts[i];
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+  if (lane_id() == 0) part[wave_id()] = sum;
+  __syncthreads();
+  int at = part[0] + part[1] + part[2] + part[3];
+  const int first = at;
+  for (int s0 = 0; s0 < S; s0 += 64) {
+    const int c = s0 + lane_id() < S ? counts[e * S + s0 + lane_id()] : 0;
+    const int to = scan64(c);
+    const int here = S - s0 < 64 ? S - s0 : 64;
+    for (int q = wave_id(); q < here; q += 4) {
+      const int n = __builtin_amdgcn_readlane(c, q), from = at + __builtin_amdgcn_readlane(to, q) - n;
+      for (int i = lane_id(); i < n; i += 64) list[from + i] = (e * S + s0 + q) * slots + i;
+    }
+    at += __builtin_amdgcn_readlane(to, 63);
+  }
+  if (threadIdx.x == 0) total[e] = at - first;
+}
+__global__ __launch_bounds__(256) void list_rows_kernel(const int32_t* counts, int S, int slots, int32_t* total,
+                                                        int32_t* list) {
+  list_rows(counts, blockIdx.x, S, slots, total, list);
+}
+
+// ---------------------------------------------------------------------------
 // Rows kept in 8 bits, back in bf16
 // ---------------------------------------------------------------------------
 
@@ -435,7 +469,9 @@ __global__ __launch_bounds__(C::NT, 2) void weight_grads_kernel(WeightGradArgs g
 // of 1152: 5.5 us).  A wave takes 2048 codes of a row, eight a lane and load, so that a store instruction writes one run.
 // HT: the rows are the first ones, as many as the counts sum up to.  LL: entry by entry, its tile's prefix and its rank
 // in the tile.  A grid by experts' tiles, each finding its span as the products do: 14 us more at those 2997 rows on
-// 24 experts, 500 us at the 32768.  The products behind it read the rows again: plain stores.
+// 24 experts, 500 us at the 32768.  The products behind it read the rows again: plain stores.  Where they need the rows'
+// list too, the first workgroups make it: a launch less (linear backward of 64 experts, 4 sources of 64 tokens: 53.8 us, 56.5 with
+// two).
 constexpr int kDecodeChunks = 4;   // eight codes of a lane
 
 template <bool FIRST>
@@ -443,9 +479,20 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs a, int W) {
   typedef __attribute__((ext_vector_type(2))) float f32x2;
   typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
   typedef __attribute__((ext_vector_type(2))) int i32x2;
+  int block = blockIdx.x, blocks = gridDim.x;
+  if constexpr (!FIRST) {
+    if (a.list) {
+      if (block < a.E) {
+        list_rows(a.ll_count, block, a.S, a.slots, a.total, a.list);
+        return;
+      }
+      block -= a.E;
+      blocks -= a.E;
+    }
+  }
   const int C = a.C / 8;
-  const int64_t waves = static_cast<int64_t>(gridDim.x) * 4;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * 4 + wave_id();
+  const int64_t waves = static_cast<int64_t>(blocks) * 4;
+  const int64_t first = static_cast<int64_t>(block) * 4 + wave_id();
   int64_t total = a.n * W;
   if constexpr (FIRST) {
     int sum = 0;
@@ -494,38 +541,6 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs a, int W) {
       *reinterpret_cast<i32x4*>(a.out + row * a.ld_out + 8 * c) = o;
     }
   }
-}
-
-// ---------------------------------------------------------------------------
-// Rows per expert where several sources fill their own slots (LL)
-// ---------------------------------------------------------------------------
-
-// One workgroup per expert: its rows (e*S + s)*T_max + slot for all sources in order, at the sum of the
-// counts before it.  Each workgroup sums those counts itself: E*S of them at most, from the L2.  64 experts with 4
-// sources: 3 us, the launch.
-__global__ __launch_bounds__(256) void list_rows_kernel(const int32_t* counts, int S, int slots, int32_t* total,
-                                                        int32_t* list) {
-  __shared__ int part[4];
-  const int e = blockIdx.x;
-  int sum = 0;
-  for (int i = threadIdx.x; i < e * S; i += 256) sum += counts[i];
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
-  if (lane_id() == 0) part[wave_id()] = sum;
-  __syncthreads();
-  int at = part[0] + part[1] + part[2] + part[3];
-  const int first = at;
-  for (int s0 = 0; s0 < S; s0 += 64) {
-    const int c = s0 + lane_id() < S ? counts[e * S + s0 + lane_id()] : 0;
-    const int to = scan64(c);
-    const int here = S - s0 < 64 ? S - s0 : 64;
-    for (int q = wave_id(); q < here; q += 4) {
-      const int n = __builtin_amdgcn_readlane(c, q), from = at + __builtin_amdgcn_readlane(to, q) - n;
-      for (int i = lane_id(); i < n; i += 64) list[from + i] = (e * S + s0 + q) * slots + i;
-    }
-    at += __builtin_amdgcn_readlane(to, 63);
-  }
-  if (threadIdx.x == 0) total[e] = at - first;
 }
 
 // Blocks for at most `rows` rows in all and `per_expert` in one.
@@ -657,9 +672,8 @@ hipError_t launch_weight_grad_as(const WeightGradArgs& g, hipStream_t stream, bo
 }  // namespace
 
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t stream) {
-  if (a.n == 0) return hipSuccess;
   const int W = (a.C / 8 + 64 * kDecodeChunks - 1) / (64 * kDecodeChunks);
-  const dim3 grid(grid_blocks((a.n * W + 3) / 4, 256)), block(256);
+  const dim3 grid(grid_blocks((a.n * W + 3) / 4 + (a.list ? a.E : 0), 256)), block(256);
   if (a.count) decode_kernel<true><<<grid, block, 0, stream>>>(a, W);
   else decode_kernel<false><<<grid, block, 0, stream>>>(a, W);
   return hipGetLastError();

@@ -470,6 +470,8 @@ struct DecodeArgs {
   const int32_t* count;               // [E]
   const int32_t *topk, *rank_e, *hist_e;   // LL: an entry's expert, its rank among its tile's, the tile's prefix
   int32_t E, K, S, T, tps, slots;
+  const int32_t* ll_count;            // LL: launch_list_rows' arguments, if `list` is to be made too
+  int32_t *total, *list;
   int32_t* err;
 };
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t stream);

@@ -1386,11 +1386,11 @@ ExpertRows rows_of_experts(const Handle* h, int64_t limit) {
 // Enqueues what the products need first: the rows' list in LL with many
 // sources.  It is formed at every call, from the handle's counts alone, so a
 // captured call does not depend on what ran outside its graph.
-ep_status_t start_products(Handle* h, hipStream_t s) {
+ep_status_t start_products(Handle* h, hipStream_t s, bool list = true) {
   Group* g = h->g;
   if (const ep_status_t st = ensure_device(g, s); st != EP_OK) return st;
   h->stream = s;
-  if (makes_list(g->cfg))
+  if (list && makes_list(g->cfg))
     EP_HIP(expert::launch_list_rows(h->ll_count, g->cfg.num_experts, g->cfg.num_src_ranks,
                                     g->cfg.max_tokens_per_rank, h->rows_total, h->rows_list, s));
   return EP_OK;
@@ -1543,7 +1543,7 @@ bool coded_rows(const Group* g, const ep_tensor_t* t, const ep_tensor_t* scales,
   return true;
 }
 
-// The decoding of rows kept in 8 bits into `to`.
+// The decoding of rows kept in 8 bits into `to`; it makes the rows' list, if the products go by one.
 DecodeArgs decode_args(const Handle* h, const ep_tensor_t& x, const uint8_t* scales, int64_t ld_scales, int64_t C,
                        const ep_tensor_t& to, int64_t rows) {
   const Group* g = h->g;
@@ -1568,6 +1568,9 @@ DecodeArgs decode_args(const Handle* h, const ep_tensor_t& x, const uint8_t* sca
     a.T = h->T;
     a.tps = h->tps;
     a.slots = g->cfg.max_tokens_per_rank;
+    a.ll_count = h->ll_count;
+    a.total = h->rows_total;
+    a.list = h->rows_list;
   } else {
     a.count = g->sorted ? h->cx : h->c2;
   }
@@ -1639,8 +1642,9 @@ ep_status_t gated_backward(ep_handle_t handle, const ep_tensor_t* rows, const ep
   if (const ep_status_t st = fits(expert::launch_gated_grad(a, activation, s, true)); st != EP_OK) return st;
   if (const ep_status_t st = fits(expert::launch_row_grad(r, s, true)); st != EP_OK) return st;
   if (const ep_status_t st = fits(expert::launch_weight_grad(w, f32, s, true)); st != EP_OK) return st;
-  if (const ep_status_t st = start_products(h, s); st != EP_OK) return st;
-  if (coded) EP_HIP(expert::launch_decode(decode_args(h, x, xs, ld_xs, H, dx, limit), s));
+  const bool decode = coded && h->n > 0;
+  if (const ep_status_t st = start_products(h, s, !decode); st != EP_OK) return st;
+  if (decode) EP_HIP(expert::launch_decode(decode_args(h, x, xs, ld_xs, H, dx, limit), s));
   EP_HIP(expert::launch_gated_grad(a, activation, s));
   if (grad_w_gate) EP_HIP(expert::launch_weight_grad(w, f32, s));
   if (grad_rows) EP_HIP(expert::launch_row_grad(r, s));   // last: over the decoded rows
@@ -1791,8 +1795,9 @@ ep_status_t linear_backward(ep_handle_t handle, const ep_tensor_t* x_in, const e
   const hipStream_t s = as_stream(stream);
   if (const ep_status_t st = fits(expert::launch_row_grad(r, s, true)); st != EP_OK) return st;
   if (const ep_status_t st = fits(expert::launch_weight_grad(wg, f32, s, true)); st != EP_OK) return st;
-  if (const ep_status_t st = start_products(h, s); st != EP_OK) return st;
-  if (coded && grad_w) EP_HIP(expert::launch_decode(decode_args(h, x, xs, ld_xs, C, dx, limit), s));
+  const bool decode = coded && grad_w && h->n > 0;
+  if (const ep_status_t st = start_products(h, s, !decode); st != EP_OK) return st;
+  if (decode) EP_HIP(expert::launch_decode(decode_args(h, x, xs, ld_xs, C, dx, limit), s));
   if (grad_w) EP_HIP(expert::launch_weight_grad(wg, f32, s));
   if (grad_x) EP_HIP(expert::launch_row_grad(r, s));   // last: over the decoded rows
   trace(g, coded ? "expert_linear_backward_quantized" : "expert_linear_backward", h->n);
