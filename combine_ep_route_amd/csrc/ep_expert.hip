@@ -306,12 +306,11 @@ struct WeightGradSrc {
 
 // An expert without rows gets zeros.  Both operands lie across the contraction: they reach the matrix unit by
 // transposing LDS reads.
-// 64 experts of 7168 x 2048: bf16, 512 rows each, both gated gradients 2.5 ms, 760 TFLOP/s; F32, 256 rows each,
-// 1.1 ms, 3.5 TB/s written.  The two bounds add up: the stores of a tile (256 KiB in F32; without rows 0.62 ms in
-// all, 6.0 TB/s) and the short contraction (256 rows more: 0.335 ms, the library's 1440 TFLOP/s).  Two workgroups
-// a CU of 256 x 128 or 128 x 128 gain no overlap and take more loads (a linear backward of 1.7 ms takes 1.9 and
-// 2.2), nor do staggered starts.  Another order of the tiles that reads a quarter of the bytes beyond the L2
-// changes nothing.
+// 64 experts of 7168 x 2048, 256 rows each, F32: 1.1 ms, 3.5 TB/s written.  The two bounds add up: the stores of a
+// tile (256 KiB; without rows 0.62 ms in all, 6.0 TB/s) and the short contraction (256 rows more: 0.335 ms, the
+// library's 1440 TFLOP/s).  Two workgroups a CU of 256 x 128 or 128 x 128 gain no overlap and take more loads (a linear
+// backward of 1.7 ms takes 1.9 and 2.2), nor do staggered starts.  Another order of the tiles that reads a quarter of
+// the bytes beyond the L2 changes nothing.
 template <class C, bool F32, bool LIST>
 __global__ __launch_bounds__(C::NT, 2) void weight_grad_kernel(WeightGradArgs g) {
   const int ht = (g.H + C::BA - 1) / C::BA, it = (g.I + C::BB - 1) / C::BB;
@@ -688,20 +687,33 @@ hipError_t launch_row_grad(const RowGradArgs& g, hipStream_t stream, bool check)
   }
 }
 
-// With fewer than two 256 x 256 tiles a CU the smaller ones fill the chip.  128 rows an expert, F32 / bf16 gradients,
-// us, small tiles and big ones, by the number of big ones:
-//     96 (8 experts of 1024 x 768)     16 / 14   21 / 17       640 (40 of 1024 x 1024)    50 / 42    53 / 40
-//    256 (16 of 1024 x 1024)           26 / 21   25 / 19      1024 (64 of 1024 x 1024)    77 / 64    72 / 52
-//    384 (24 of 1024 x 1024)           34 / 29   37 / 29      1536 (96 of 1024 x 1024)   117 / 92   102 / 79
-//    512 (32 of 1024 x 1024)           42 / 37   40 / 30      2048 (128 of 1024 x 1024)  163 / 121  145 / 100
+// F32 gradients, a workgroup a tile: with fewer than two 256 x 256 tiles a CU the smaller ones fill the chip.  128 rows an
+// expert, us, small tiles and big ones, by the number of big ones:
+//     96 (8 experts of 1024 x 768)     16   21       640 (40 of 1024 x 1024)    50   53
+//    256 (16 of 1024 x 1024)           26   25      1024 (64 of 1024 x 1024)    77   72
+//    384 (24 of 1024 x 1024)           34   37      1536 (96 of 1024 x 1024)   117  102
+//    512 (32 of 1024 x 1024)           42   40      2048 (128 of 1024 x 1024)  163  145
 // Near the border the big ones win where they fill the CUs a whole number of times (256, 512).
+// bf16 gradients, big tiles one after the other: the smaller ones win as long as all of them run at once, two a CU.
+// Linear backward of 4 / 32 / 128 / 384 rows an expert, us, by the number of small tiles:
+//    384 (8 experts of 1024 x 768)    small 15.1 19.4 25.2 27.9   big 16.0 20.5 27.2 31.7
+//    480 (10)                               15.8 19.5 24.8 29.2       16.8 21.2 27.2 32.0
+//    576 (12)                               20.4 23.7 29.6 35.9       17.4 21.3 27.0 32.2
+//   1296 (24 of 1152 x 712, odd)            31.7 34.0 42.0 61.6       27.8 30.9 39.5 60.1
+//   1408 (8 of 2048 x 1408)                 30.1 37.3 46.6 69.2       27.0 34.5 43.8 67.0
+//   1920 (40 of 1024 x 768)                 36.5 39.2 52.7 83.9       30.2 33.0 45.8 77.3
 hipError_t launch_weight_grad(const WeightGradArgs& g, bool f32, hipStream_t stream, bool check) {
-  if (static_cast<int64_t>(g.rows.E) * g.parts * ((g.H + 255) / 256) * ((g.I + 255) / 256) < 512) {
-    using Small = Core<128, 128, 2, 2, true, true, false, 4, 64>;
-    return f32 ? launch_weight_grad_as<Small, true>(g, stream, check) : launch_weight_grad_as<Small, false>(g, stream, check);
-  }
+  using Small = Core<128, 128, 2, 2, true, true, false, 4, 64>;
   using Big = Core<256, 256, 2, 4, true, true, false, 4, 64>;
-  return f32 ? launch_weight_grad_as<Big, true>(g, stream, check) : launch_weight_grads_as<Big>(g, stream, check);
+  const int64_t matrices = static_cast<int64_t>(g.rows.E) * g.parts;
+  const int64_t small = matrices * ((g.H + 127) / 128) * ((g.I + 127) / 128);
+  const int64_t big = matrices * ((g.H + 255) / 256) * ((g.I + 255) / 256);
+  if (f32) {
+    return big < 2 * kCus ? launch_weight_grad_as<Small, true>(g, stream, check)
+                          : launch_weight_grad_as<Big, true>(g, stream, check);
+  }
+  return small <= 2 * kCus ? launch_weight_grad_as<Small, false>(g, stream, check)
+                           : launch_weight_grads_as<Big>(g, stream, check);
 }
 
 }  // namespace expert
