@@ -1,6 +1,8 @@
 // The experts' products on the received rows: the gated feed-forward's first half, the linear product
 // behind it, and their backward passes.  One grid covers all experts; which rows an expert holds is read
 // from the handle's counts on the device, so nothing waits for the host.
+#include <cmath>
+
 #include "ep_expert_dev.h"
 #include "ep_internal.h"
 
@@ -580,16 +582,21 @@ hipError_t launch_along_as(const AlongArgs& a, hipStream_t stream, bool check) {
 // the experts as a router leaves them make many tiles of the average's multiple: at 128 rows on average (256
 // experts of 7168 x 2048, bf16) the big tile takes 2.35 ms, the middle one 2.67.
 // Few big tiles leave CUs idle: 88 of them (8 experts, 256 rows each) take 48 us, middle ones 37.
-// No more middle tiles than CUs (by the average rows): each has a CU's LDS to itself, and a ring of four stages keeps
+// No more middle tiles than CUs, as a random routing leaves the rows: each has a CU's LDS to itself, and a ring of four stages keeps
 // three of them in flight instead of one.  bf16, 8 experts of 1024 x 768, us, two stages / four: gated 15.1 / 11.1 of 32
 // rows each, 17.2 / 14.4 of 128; linear 10.3 / 9.7 and 14.9 / 13.0.  With more tiles two workgroups share a CU, which
-// four stages leave no room for: 24 experts of 1152 x 712, 48 rows each, gated 19.9 / 25.8.
+// four stages leave no room for: 24 experts of 1152 x 712, 48 rows each, gated 19.9 / 25.8.  With 128 rows each on average
+// half of the experts have two row tiles: 16 of 1024 x 768, gated, 21.6 / 26.5.
 enum Size { kSmall, kMiddle, kMiddleDeep, kBig };
 Size tile_size(const ExpertRows& r, int64_t rows, int64_t col_tiles, int64_t middle_col_tiles) {
   const int64_t each = rows / r.E;
   if (each <= 24) return kSmall;
   if (each > 96 && r.E * ((each + 255) / 256) * col_tiles >= 256) return kBig;
-  return r.E * ((each + 127) / 128) * middle_col_tiles <= kCus ? kMiddleDeep : kMiddle;
+  // an expert's row tiles on average, its rows being spread by the square root of their number
+  auto more_than = [&](int64_t n) { return 0.5 * std::erfc((n - each) / std::sqrt(2.0 * each)); };
+  const int64_t least = (each - 1) / 128;
+  const double row_tiles = least + more_than(128 * least) + more_than(128 * (least + 1));
+  return r.E * row_tiles * middle_col_tiles <= kCus ? kMiddleDeep : kMiddle;
 }
 
 template <bool F8, int KIND, int ACT>
