@@ -466,13 +466,16 @@ __global__ __launch_bounds__(256) void list_rows_kernel(const int32_t* counts, i
 // Rows kept in 8 bits, back in bf16
 // ---------------------------------------------------------------------------
 
-// out = bf16_rne(code * scale) on the experts' rows: memory bounds it (32768 rows of 7168: 104 us, 6.9 TB/s; 2997
-// of 1152: 5.5 us).  A wave takes 2048 codes of a row, eight a lane and load, so that a store instruction writes one run.
-// HT: the rows are the first ones, as many as the counts sum up to.  LL: entry by entry, its tile's prefix and its rank
-// in the tile.  A grid by experts' tiles, each finding its span as the products do: 14 us more at those 2997 rows on
-// 24 experts, 500 us at the 32768.  The products behind it read the rows again: plain stores.  Where they need the rows'
-// list too, the first workgroups make it: a launch less (linear backward of 64 experts, 4 sources of 64 tokens: 53.8 us, 56.5 with
-// two).
+// out = bf16_rne(code * scale) on the experts' rows.  The product has up to 28 bits, an operand of the matrix unit 8: the
+// rounding is ep_dequantize_rows' own, so that gradients from kept codes have the bits of those from kept bf16 rows.  The
+// gated gradients are 0.0033 of their norm off 64 bits so, 0.0023 with rows that bf16 holds, 0.0017 with their own
+// rounding alone; the scales cannot be applied behind the products instead, as those of the weights sum over rows.
+// Memory bounds it (32768 rows of 7168: 104 us, 6.9 TB/s; 2997 of 1152: 5.5 us).  A wave takes 2048 codes of a row, eight
+// a lane and load, so that a store instruction writes one run.  HT: the rows are the first ones, as many as the counts
+// sum up to.  LL: entry by entry, its tile's prefix and its rank in the tile.  A grid by experts' tiles, each finding its
+// span as the products do: 14 us more at those 2997 rows on 24 experts, 500 us at the 32768.  The products behind it read
+// the rows again: plain stores.  Where they need the rows' list too, the first workgroups make it: a launch less (linear
+// backward of 64 experts, 4 sources of 64 tokens: 53.8 us, 56.5 with two).
 constexpr int kDecodeChunks = 4;   // eight codes of a lane
 
 template <bool FIRST>
