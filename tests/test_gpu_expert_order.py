@@ -300,6 +300,50 @@ def test_the_combine_behind_and_its_adjoint():
             assert ei.value.status == A.EP_ERR_INVALID_ARGUMENT
 
 
+@pytest.mark.parametrize("spoilt", [False, True], ids=["valid", "invalid"])
+@pytest.mark.parametrize("g", GEOMETRIES[1:], ids=ids[1:])
+def test_the_combine_adjoint(g, spoilt):
+    """Every rank's row of a token is a copy of the token's gradient: strided, in tensors that hold fewer rows, with a cap
+    on the CUs, captured."""
+    say(f"combine adjoint {g}, {'invalid' if spoilt else 'valid'} entries")
+    topk = np.argsort(np.random.default_rng(7).random((g["S"] * g["T"], g["E"])), axis=1)[:, :g["K"]].astype(np.int32)
+    with Ranks(**g, topk=invalid(topk, g["E"], 8) if spoilt else topk) as r:
+        ep.ep_get_device_error(r.group)   # of the entries
+        token = torch.zeros(r.rows, dtype=torch.int64, device="cuda")
+        token[r.row_of] = r.entry // r.K
+        grad = normal((r.n, r.H + 8), 1)[:, :r.H]
+        want = grad[token]
+
+        def rows(more, pad=0):
+            return torch.full((r.rows + more, r.H + pad), STALE, dtype=BF16, device="cuda")
+
+        wide = rows(2, 16)
+        ep.ep_combine_backward(r.handle, grad, None, wide[:, :r.H])
+        assert torch.equal(wide[:r.rows, :r.H], want)
+        assert bool((wide[r.rows:] == STALE).all()) and bool((wide[:, r.H:] == STALE).all())
+        assert ep.ep_get_device_error(r.group) == 0
+        short = rows(0)
+        keep = r.rows // 2
+        ep.ep_combine_backward(r.handle, grad, None, short[:keep])
+        assert torch.equal(short[:keep], want[:keep]) and bool((short[keep:] == STALE).all())
+        assert ep.ep_get_device_error(r.group) == A.EP_DEVERR_ROW_RANGE
+        capped = ep.ep_create_group(**dict(r.group.config, num_cus=1))
+        h = ep.ep_create_handle(capped, r.idx)
+        few = rows(0)
+        ep.ep_combine_backward(h, grad, None, few)
+        assert torch.equal(few, want)
+        ep.ep_destroy_group(capped)
+        out, graph = rows(0), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            ep.ep_combine_backward(r.handle, grad, None, out)
+        for turn in range(3):
+            grad.copy_(normal((r.n, r.H), 20 + turn))
+            out.fill_(STALE)
+            graph.replay()
+            assert torch.equal(out, grad[token]), turn
+
+
 def refused(status, fn, *args, **kw):
     with pytest.raises(ep.EpError) as ei:
         fn(*args, **kw)

@@ -47,3 +47,20 @@ def test_every_tile_once(E, H, I, kind):
             # an fp32 sum of the rows' products, rounded to bf16: half a step, and of what the sum is off by
             off = len(at) * 2.0 ** -24 * (a.abs() @ b.abs())
             near(room[e], want, off + HALF * (want.abs() + off), f"expert {e}")
+
+
+@pytest.mark.parametrize("S,T,E,H,I", [(1, 90, 60, 1024, 768), (3, 40, 40, 1024, 768), (12, 9, 48, 1040, 776), (2, 200, 30, 784, 1288)],
+                         ids=str)
+def test_slots_of_several_sources(S, T, E, H, I):
+    """LL: an expert's rows in one run, in runs that are looked up, and in a list; some experts without a row."""
+    say(f"weight gradients of {E} experts, {I} x {H}, {S} sources of {T} tokens")
+    with Routing("ll", S, T, E, 2, H, seed=2, skip=(0, E // 2, E - 1)) as r:
+        x, dy = row_tensor(r, I, 1), row_tensor(r, H, 2)
+        room = torch.full((E + 1, H, I), -7.25, dtype=BF16, device="cuda")
+        ep.ep_expert_linear_backward(r.handle, x, normal((E, H, I), 3), dy, grad_w=room[:E])
+        assert bool((room[E] == -7.25).all()), "written behind the last expert"
+        for e, at in enumerate(r.expert_rows):
+            a, b = dy[at].to(D).t(), x[at].to(D)
+            want = a @ b
+            off = len(at) * 2.0 ** -24 * (a.abs() @ b.abs())
+            near(room[e], want, off + HALF * (want.abs() + off), f"expert {e}")
