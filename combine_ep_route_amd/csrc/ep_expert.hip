@@ -585,11 +585,11 @@ hipError_t launch_along_as(const AlongArgs& a, hipStream_t stream, bool check) {
 // the experts as a router leaves them make many tiles of the average's multiple: at 128 rows on average (256
 // experts of 7168 x 2048, bf16) the big tile takes 2.35 ms, the middle one 2.67.
 // Few big tiles leave CUs idle: 88 of them (8 experts, 256 rows each) take 48 us, middle ones 37.
-// No more middle tiles than CUs, as a random routing leaves the rows: each has a CU's LDS to itself, and a ring of four stages keeps
-// three of them in flight instead of one.  bf16, 8 experts of 1024 x 768, us, two stages / four: gated 15.1 / 11.1 of 32
-// rows each, 17.2 / 14.4 of 128; linear 10.3 / 9.7 and 14.9 / 13.0.  With more tiles two workgroups share a CU, which
-// four stages leave no room for: 24 experts of 1152 x 712, 48 rows each, gated 19.9 / 25.8.  With 128 rows each on average
-// half of the experts have two row tiles: 16 of 1024 x 768, gated, 21.6 / 26.5.
+// No more middle tiles than CUs, as a random routing leaves the rows: each has a CU's LDS to itself, and a ring of four
+// stages keeps three of them in flight instead of one.  bf16, 8 experts of 1024 x 768, us, two stages / four: gated
+// 15.1 / 11.1 of 32 rows each, 17.2 / 14.4 of 128; linear 10.3 / 9.7 and 14.9 / 13.0.  With more tiles two workgroups
+// share a CU, which four stages leave no room for: 24 experts of 1152 x 712, 48 rows each, gated 19.9 / 25.8.  With 128
+// rows each on average half of the experts have two row tiles: 16 of 1024 x 768, gated, 21.6 / 26.5.
 enum Size { kSmall, kMiddle, kMiddleDeep, kBig };
 Size tile_size(const ExpertRows& r, int64_t rows, int64_t col_tiles, int64_t middle_col_tiles) {
   const int64_t each = rows / r.E;

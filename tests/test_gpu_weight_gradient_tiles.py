@@ -9,9 +9,14 @@ import pytest
 import torch
 
 from expert_util import BF16, D, HALF, Routing, near, normal, row_tensor
-from gpu_util import ep, say
+from gpu_util import ep, need_gpu, say
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
 
 
 def routing(kind, E, T):
